@@ -195,7 +195,7 @@ typedef enum { GEMM_SCHED_DEFAULT = 0, GEMM_SCHED_STATIC = 1, GEMM_SCHED_CLC = 2
 
 /* What the last successful launch on this host thread ran. */
 typedef struct gemm_launch_info {
-  int path;          /* gemm_path actually used (0 if no launch) */
+  int path;          /* gemm_path actually used (0 if no launch, and for the expert and 4-bit-weight calls) */
   int grid;          /* CTAs launched */
   int cluster;       /* CTAs per cluster */
   int block;         /* threads per CTA */
@@ -468,6 +468,131 @@ int gemm_bf16_tn_skinny_noalloc(int64_t M, int64_t N, int64_t K,
                                 const void *C, int64_t ldc,
                                 void *D, int64_t ldd,
                                 float alpha, float beta, int out_dtype, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Mixture-of-experts MLP: tokens to expert order and back.
+ *
+ * A router gives each of T tokens k expert slots.  gemm_expert_dispatch
+ * sorts the slots by expert and copies the tokens' rows into that order, so
+ * that expert e's rows are the contiguous block offsets[e] .. offsets[e+1]
+ * of one matrix: the A operand of one gemm_problem (gemm_bf16_tn_grouped) or
+ * of gemm_w4_tn_experts.  gemm_expert_combine adds each token's expert rows
+ * with the router's weights.  Both have their gradients.
+ *
+ *   offsets[e]      = number of slots with an expert below e, e = 0..E
+ *   slot_row[t,j]   = offsets[e] + number of earlier slots (t', j') < (t, j)
+ *                     of the same expert e = ids[t,j]; -1 for a dropped slot
+ *   row_token[r]    = the token whose slot went to row r; -1 for the rows
+ *                     from offsets[E] on
+ *
+ * A slot is dropped when its id is outside [0, E) (for example -1: padding
+ * tokens, or slots over an expert's capacity).  Row matrices have T*k rows
+ * whatever is dropped; the rows from offsets[E] on belong to no slot.
+ *
+ * Rows hold H elements of dtype GEMM_OUT_BF16 or GEMM_OUT_F32, in row-major
+ * matrices whose leading dimension is at least H.  Any alignment to the
+ * element size is accepted; where every base address and row pitch is a
+ * multiple of 16 bytes the kernels move 16 bytes at a time, which is faster.
+ * Sums are taken in fp32 in slot order and rounded once, so results are the
+ * same from run to run.
+ *
+ * The plan's arrays are device memory owned by the caller; dispatch writes
+ * them and the other calls read them, checking every row against [0, T*k).
+ * All calls are asynchronous on `stream` with programmatic stream
+ * serialisation, like the GEMM kernels.  Sorting more than 2048 slots uses
+ * the library's workspace of the stream; where it would have to be allocated
+ * or grown during stream capture, the call returns
+ * GEMM_ERR_INVALID_VALUE. */
+typedef struct gemm_expert_plan {
+  int64_t tokens;      /* T; T*k below 2^31 */
+  int slots;           /* k, 1..64 */
+  int experts;         /* E, 1..1024 */
+  int32_t *offsets;    /* E + 1 */
+  int32_t *slot_row;   /* T*k */
+  int32_t *row_token;  /* T*k */
+} gemm_expert_plan;
+
+/* Fills the plan from ids (T x k, row stride ld_ids >= k elements; int64 when
+ * ids_64bit is 1, int32 when 0) and copies rows: Xs[slot_row[t,j]] = X[t],
+ * zeros in the rows from offsets[E] on.  X = NULL or H = 0: only the plan.
+ * X holds T rows, Xs T*k; they must not overlap each other or the plan. */
+int gemm_expert_dispatch(const gemm_expert_plan *plan, const void *ids, int64_t ld_ids, int ids_64bit,
+                         int64_t H, const void *X, int64_t ldx, int dtype, void *Xs, int64_t ldxs, void *stream);
+
+/* Gradient of the copy: dX[t] = sum over j of dXs[slot_row[t,j]] (zero where
+ * every slot is dropped). */
+int gemm_expert_dispatch_backward(const gemm_expert_plan *plan, int64_t H, const void *dXs, int64_t lddxs, int dtype,
+                                  void *dX, int64_t lddx, void *stream);
+
+/* out[t] = sum over j of weights[t,j] * Y[slot_row[t,j]], dropped slots left
+ * out (zero where all are).  weights: T x k, row stride ldw, bf16
+ * (weights_dtype 0) or fp32 (1).  Y: T*k rows. */
+int gemm_expert_combine(const gemm_expert_plan *plan, int64_t H, const void *Y, int64_t ldy, int dtype,
+                        const void *weights, int64_t ldw, int weights_dtype, void *out, int64_t ldo, void *stream);
+
+/* Gradients of gemm_expert_combine for the gradient dout (T x H, dtype):
+ *
+ *   dY[slot_row[t,j]] = weights[t,j] * dout[t]   (zeros from offsets[E] on)
+ *   dweights[t,j]     = <dout[t], Y[slot_row[t,j]]>   (0 for dropped slots)
+ *
+ * dweights has the type of weights.  dY or dweights may be NULL where it is
+ * not wanted; without dweights, Y may be NULL. */
+int gemm_expert_combine_backward(const gemm_expert_plan *plan, int64_t H, const void *Y, int64_t ldy,
+                                 const void *dout, int64_t lddo, int dtype,
+                                 const void *weights, int64_t ldw, int weights_dtype,
+                                 void *dY, int64_t lddy, void *dweights, int64_t lddw, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Products with 4-bit weights, for few tokens (decode).
+ *
+ * A gemm_w4_matrix describes `count` weight matrices (one, or one per
+ * expert) of N x K 4-bit codes q with a scale and an optional zero point for
+ * every `group` consecutive k of a row:
+ *
+ *     W[n,k] = scales[n, k / group] * (q[n,k] - zeros[n, k / group])
+ *
+ *   codes   two to a byte, the even k in the low four bits; rows of ldc
+ *           codes, ldc >= K and a multiple of 32; 16-byte aligned
+ *   scales  bf16 (scales_dtype 0) or fp32 (1), ceil(K / group) per row, row
+ *           stride lds
+ *   zeros   unsigned bytes of 0..127 (the low seven bits count), row stride
+ *           ldz, or NULL for a zero point of 8 everywhere
+ *   group   32, 64, 128 or a multiple of 256 (at least K: one scale a row)
+ *   strides from one matrix to the next: stride_codes in codes (a multiple
+ *           of 32, at least N * ldc), stride_scales and stride_zeros in
+ *           elements; not used when count is 1
+ *
+ * All are device memory owned by the caller. */
+typedef struct gemm_w4_matrix {
+  int64_t N, K, count;
+  int group, scales_dtype;
+  const void *codes; int64_t ldc, stride_codes;
+  const void *scales; int64_t lds, stride_scales;
+  const void *zeros; int64_t ldz, stride_zeros;
+} gemm_w4_matrix;
+
+/* D = act(alpha * A * W^T) with A (M x K) bf16 and D (M x N) bf16 or fp32;
+ * W->count is 1.  A follows the rules of gemm_bf16_tn (16-byte aligned, lda a
+ * multiple of 8); D is aligned to its element size, ldd >= N.  activation is
+ * a gemm_activation.  The differences q - zero are exact in the tensor-core
+ * product, and the scales multiply fp32 sums of a group: the weights are not
+ * rounded.  Any M is computed; the weights are read once for every 16 tokens,
+ * so the call is meant for decode batches and for larger M a bf16 GEMM is
+ * the faster choice.  M or N = 0 returns GEMM_OK with no launch; K = 0 gives
+ * act(0). */
+int gemm_w4_tn(int64_t M, const void *A, int64_t lda, const gemm_w4_matrix *W, void *D, int64_t ldd,
+               float alpha, int out_dtype, int activation, void *stream);
+
+/* The same by expert, for rows in a dispatch plan's order:
+ *
+ *     D[r] = act(alpha * A[r'] * W_e^T),  offsets[e] <= r < offsets[e+1]
+ *
+ * for all R = T*k rows of the plan, zeros from offsets[E] on; W->count equals
+ * the plan's experts.  r' = row_token[r] when gather is 1 (A has T rows: the
+ * tokens themselves, so that no copy in expert order is needed), r when it is
+ * 0 (A has T*k rows in expert order).  Experts without rows are not read. */
+int gemm_w4_tn_experts(const gemm_expert_plan *plan, const void *A, int64_t lda, int gather, const gemm_w4_matrix *W,
+                       void *D, int64_t ldd, float alpha, int out_dtype, int activation, void *stream);
 
 #ifdef __cplusplus
 }

@@ -39,7 +39,8 @@ EXPORTED = ["gemm_bf16_tn", "gemm_bf16_tn_ex", "gemm_get_status", "gemm_get_stat
             "gemm_last_error_string", "gemm_last_launch_info", "gemm_shutdown", "gemm_version",
             "gemm_bf16_tn_skinny_noalloc", "gemm_bf16_tn_bias_act", "gemm_fp8_tn", "gemm_fp8_tn_ex",
             "gemm_bf16_tn_grouped", "gemm_bf16_tn_batched", "gemm_plan", "gemm_stream_read",
-            "gemm_mma_rate", "gemm_fp8_tn_bias_act"]
+            "gemm_mma_rate", "gemm_fp8_tn_bias_act", "gemm_expert_dispatch", "gemm_expert_dispatch_backward",
+            "gemm_expert_combine", "gemm_expert_combine_backward", "gemm_w4_tn", "gemm_w4_tn_experts"]
 
 FP8_E4M3, FP8_E5M2 = 0, 1
 SCHED_DEFAULT, SCHED_STATIC, SCHED_CLC = 0, 1, 2
@@ -91,6 +92,21 @@ class LaunchInfo(ctypes.Structure):
                 for f, _ in self._fields_}
 
 
+class ExpertPlanInfo(ctypes.Structure):
+    """gemm_expert_plan: sizes and device pointers of a dispatch plan."""
+    _fields_ = [("tokens", ctypes.c_int64), ("slots", ctypes.c_int), ("experts", ctypes.c_int),
+                ("offsets", ctypes.c_void_p), ("slot_row", ctypes.c_void_p), ("row_token", ctypes.c_void_p)]
+
+
+class W4MatrixInfo(ctypes.Structure):
+    """gemm_w4_matrix: sizes and device pointers of 4-bit weight matrices."""
+    _fields_ = [("N", ctypes.c_int64), ("K", ctypes.c_int64), ("count", ctypes.c_int64),
+                ("group", ctypes.c_int), ("scales_dtype", ctypes.c_int),
+                ("codes", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("stride_codes", ctypes.c_int64),
+                ("scales", ctypes.c_void_p), ("lds", ctypes.c_int64), ("stride_scales", ctypes.c_int64),
+                ("zeros", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("stride_zeros", ctypes.c_int64)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -132,6 +148,20 @@ def load(path: str = LIB_PATH):
         lib.gemm_bf16_tn_batched.restype = i32
         lib.gemm_bf16_tn_ex.argtypes = args + [ctypes.POINTER(GemmConfig)]
         lib.gemm_bf16_tn_ex.restype = i32
+        plan, w4 = ctypes.POINTER(ExpertPlanInfo), ctypes.POINTER(W4MatrixInfo)
+        lib.gemm_expert_dispatch.argtypes = [plan, vp, i64, i32, i64, vp, i64, i32, vp, i64, vp]
+        lib.gemm_expert_dispatch.restype = i32
+        lib.gemm_expert_dispatch_backward.argtypes = [plan, i64, vp, i64, i32, vp, i64, vp]
+        lib.gemm_expert_dispatch_backward.restype = i32
+        lib.gemm_expert_combine.argtypes = [plan, i64, vp, i64, i32, vp, i64, i32, vp, i64, vp]
+        lib.gemm_expert_combine.restype = i32
+        lib.gemm_expert_combine_backward.argtypes = [plan, i64, vp, i64, vp, i64, i32, vp, i64, i32, vp, i64, vp, i64,
+                                                     vp]
+        lib.gemm_expert_combine_backward.restype = i32
+        lib.gemm_w4_tn.argtypes = [i64, vp, i64, w4, vp, i64, f32, i32, i32, vp]
+        lib.gemm_w4_tn.restype = i32
+        lib.gemm_w4_tn_experts.argtypes = [plan, vp, i64, i32, w4, vp, i64, f32, i32, i32, vp]
+        lib.gemm_w4_tn_experts.restype = i32
         lib.gemm_get_status.argtypes = [vp]
         lib.gemm_get_status.restype = i32
         lib.gemm_get_status_detail.restype = i32
@@ -297,4 +327,238 @@ def gemm(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, out_dtype=None, ou
             out.data_ptr(), out.stride(0), float(alpha), float(beta), code, stream)
     rc = gemm_bf16_tn_ex(*args, config=config) if config is not None else gemm_bf16_tn(*args)
     _check(rc)
+    return out
+
+
+def gemm_expert_dispatch(plan, ids, ld_ids, ids_64bit, H, X, ldx, dtype, Xs, ldxs, stream) -> int:
+    """Raw C-ABI call (plan: ExpertPlanInfo); returns the gemm_status code."""
+    return load().gemm_expert_dispatch(plan, ids or None, ld_ids, ids_64bit, H, X or None, ldx, dtype, Xs or None,
+                                       ldxs, stream or None)
+
+
+def gemm_expert_dispatch_backward(plan, H, dXs, lddxs, dtype, dX, lddx, stream) -> int:
+    """Raw C-ABI call: dX[t] = sum_j dXs[slot_row[t, j]]."""
+    return load().gemm_expert_dispatch_backward(plan, H, dXs or None, lddxs, dtype, dX or None, lddx, stream or None)
+
+
+def gemm_expert_combine(plan, H, Y, ldy, dtype, weights, ldw, weights_dtype, out, ldo, stream) -> int:
+    """Raw C-ABI call: out[t] = sum_j weights[t, j] * Y[slot_row[t, j]]."""
+    return load().gemm_expert_combine(plan, H, Y or None, ldy, dtype, weights or None, ldw, weights_dtype,
+                                      out or None, ldo, stream or None)
+
+
+def gemm_expert_combine_backward(plan, H, Y, ldy, dout, lddo, dtype, weights, ldw, weights_dtype, dY, lddy,
+                                 dweights, lddw, stream) -> int:
+    """Raw C-ABI call of the combine's gradients (dY or dweights may be 0)."""
+    return load().gemm_expert_combine_backward(plan, H, Y or None, ldy, dout or None, lddo, dtype, weights or None,
+                                               ldw, weights_dtype, dY or None, lddy, dweights or None, lddw,
+                                               stream or None)
+
+
+def gemm_w4_tn(M, A, lda, W, D, ldd, alpha, out_dtype, activation, stream) -> int:
+    """Raw C-ABI call (W: W4MatrixInfo): D = act(alpha * A * W^T)."""
+    return load().gemm_w4_tn(M, A or None, lda, W, D or None, ldd, alpha, out_dtype, activation, stream or None)
+
+
+def gemm_w4_tn_experts(plan, A, lda, gather, W, D, ldd, alpha, out_dtype, activation, stream) -> int:
+    """Raw C-ABI call: gemm_w4_tn with each expert's matrix for its rows of the plan."""
+    return load().gemm_w4_tn_experts(plan, A or None, lda, gather, W, D or None, ldd, alpha, out_dtype, activation,
+                                     stream or None)
+
+
+def _out_code(dtype, what):
+    import torch
+    if dtype == torch.bfloat16:
+        return OUT_BF16
+    if dtype == torch.float32:
+        return OUT_F32
+    raise ValueError(f"{what} must be torch.bfloat16 or torch.float32, not {dtype}")
+
+
+def _rows_of(t, rows, width, what):
+    """Checks a (rows, width) CUDA matrix with unit column stride; returns its row stride."""
+    if t.dim() != 2 or not t.is_cuda or t.shape[0] != rows or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{what} must be a CUDA matrix of {rows} x {'H' if width is None else width}, "
+                         f"not {tuple(t.shape)} on {t.device}")
+    ld, unit = t.stride()
+    if unit != 1 and t.shape[1] > 1 and t.shape[0] > 0:
+        raise ValueError(f"{what} must have unit column stride")
+    return max(ld, t.shape[1])
+
+
+def _stream_of(t, stream):
+    if stream is not None:
+        return stream
+    import torch
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+class ExpertPlan:
+    """A dispatch plan: int32 CUDA tensors offsets (E + 1), slot_row (T, k) and
+    row_token (T * k), filled by expert_dispatch() and read by the other calls.
+    A program keeps one per shape and fills it again at every step."""
+
+    def __init__(self, tokens: int, slots: int, experts: int, device):
+        import torch
+        buf = torch.empty(experts + 1 + 2 * tokens * slots, dtype=torch.int32, device=device)
+        n = tokens * slots
+        self._set(buf[2 * n:], buf[:n].view(tokens, slots), buf[n:2 * n], experts)
+
+    @classmethod
+    def of(cls, offsets, slot_row, row_token, experts: int | None = None):
+        """A plan over tensors that the caller filled."""
+        plan = cls.__new__(cls)
+        plan._set(offsets, slot_row, row_token, offsets.numel() - 1 if experts is None else experts)
+        return plan
+
+    def _set(self, offsets, slot_row, row_token, experts):
+        import torch
+        for name, t in (("offsets", offsets), ("slot_row", slot_row), ("row_token", row_token)):
+            if t.dtype != torch.int32 or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor")
+        if slot_row.dim() != 2 or offsets.numel() != experts + 1 or row_token.numel() != slot_row.numel():
+            raise ValueError("a plan has experts + 1 offsets, (tokens, slots) slot rows and tokens * slots row tokens")
+        self.offsets, self.slot_row, self.row_token = offsets, slot_row, row_token
+        self.tokens, self.slots = slot_row.shape
+        self.experts, self.rows = experts, slot_row.numel()
+        self.info = ExpertPlanInfo(self.tokens, self.slots, experts, offsets.data_ptr(), slot_row.data_ptr(),
+                                   row_token.data_ptr())
+
+
+class W4Matrix:
+    """4-bit weights as gemm_w4() and gemm_w4_experts() take them.
+
+    codes: uint8 CUDA tensor (N, bytes) or (E, N, bytes), two codes to a byte
+    with the even k in the low half, rows of a multiple of 16 bytes.
+    scales: bf16 or fp32 (.., N, ceil(K / group)); zeros: uint8 of that shape,
+    or None for a zero point of 8.  W[n, k] = scales[n, k // group] *
+    (q[n, k] - zeros[n, k // group])."""
+
+    def __init__(self, codes, scales, zeros=None, K: int | None = None, group: int = 128):
+        import torch
+        K = 2 * codes.shape[-1] if K is None else K
+        if codes.dtype != torch.uint8 or codes.dim() not in (2, 3) or not codes.is_cuda or codes.stride(-1) != 1:
+            raise ValueError("codes must be a 2-D or 3-D uint8 CUDA tensor with unit stride along K")
+        if codes.shape[-1] * 2 < K:
+            raise ValueError(f"codes hold {2 * codes.shape[-1]} values a row, fewer than K = {K}")
+        want = tuple(codes.shape[:-1]) + (-(-K // group),)
+        for name, t in (("scales", scales), ("zeros", zeros)):
+            if t is not None and (tuple(t.shape) != want or not t.is_cuda or (t.stride(-1) != 1 and want[-1] > 1)):
+                raise ValueError(f"{name} must be a CUDA tensor of {want} with unit stride along the groups")
+        if zeros is not None and zeros.dtype != torch.uint8:
+            raise ValueError("zeros must be uint8")
+        self.codes, self.scales, self.zeros, self.group = codes, scales, zeros, group
+        self.N, self.K, self.count = codes.shape[-2], K, codes.shape[0] if codes.dim() == 3 else 1
+        strides = lambda t: (0, 0) if t is None else (t.stride(-2), t.stride(0) if t.dim() == 3 else 0)  # noqa: E731
+        (lc, sc), (ls, ss), (lz, sz) = strides(codes), strides(scales), strides(zeros)
+        self.info = W4MatrixInfo(self.N, K, self.count, group, _out_code(scales.dtype, "scales"),
+                                 codes.data_ptr(), 2 * lc, 2 * sc, scales.data_ptr(), ls, ss,
+                                 0 if zeros is None else zeros.data_ptr(), lz, sz)
+
+
+def expert_dispatch(ids, plan: ExpertPlan, X=None, out=None, stream=None):
+    """Fills `plan` from ids (tokens, slots), int32 or int64 with ids outside
+    [0, experts) dropped, and returns X's rows in expert order (None without X):
+    Xs[plan.slot_row[t, j]] = X[t], zeros past plan.offsets[experts]."""
+    import torch
+    wide = ids.dtype == torch.int64
+    if not wide and ids.dtype != torch.int32:
+        raise ValueError("ids must be int32 or int64")
+    ld_ids = _rows_of(ids, plan.tokens, plan.slots, "ids")
+    H, x, ldx, o, ldo, code = 0, 0, 0, 0, 0, OUT_BF16
+    if X is not None:
+        code, ldx = _out_code(X.dtype, "X"), _rows_of(X, plan.tokens, None, "X")
+        H, x = X.shape[1], X.data_ptr()
+        if out is None:
+            out = torch.empty((plan.rows, H), dtype=X.dtype, device=X.device)
+        if out.dtype != X.dtype:
+            raise ValueError("out must have X's type")
+        o, ldo = out.data_ptr(), _rows_of(out, plan.rows, H, "out")
+    _check(gemm_expert_dispatch(plan.info, ids.data_ptr(), ld_ids, int(wide), H, x, ldx, code, o, ldo,
+                                _stream_of(ids, stream)))
+    return out if X is not None else None
+
+
+def expert_dispatch_backward(plan: ExpertPlan, dXs, out=None, stream=None):
+    """Gradient of expert_dispatch's copy: dX[t] = sum_j dXs[slot_row[t, j]]."""
+    return _combine(plan, dXs, None, out, stream)
+
+
+def expert_combine(plan: ExpertPlan, Y, weights, out=None, stream=None):
+    """out[t] = sum_j weights[t, j] * Y[slot_row[t, j]] (weights: (tokens, slots) bf16 or fp32)."""
+    return _combine(plan, Y, weights, out, stream)
+
+
+def _combine(plan, Y, weights, out, stream):
+    import torch
+    code, ldy = _out_code(Y.dtype, "rows"), _rows_of(Y, plan.rows, None, "rows")
+    H = Y.shape[1]
+    if out is None:
+        out = torch.empty((plan.tokens, H), dtype=Y.dtype, device=Y.device)
+    if out.dtype != Y.dtype:
+        raise ValueError("out must have the rows' type")
+    ldo = _rows_of(out, plan.tokens, H, "out")
+    s = _stream_of(Y, stream)
+    if weights is None:
+        _check(gemm_expert_dispatch_backward(plan.info, H, Y.data_ptr(), ldy, code, out.data_ptr(), ldo, s))
+    else:
+        ldw = _rows_of(weights, plan.tokens, plan.slots, "weights")
+        _check(gemm_expert_combine(plan.info, H, Y.data_ptr(), ldy, code, weights.data_ptr(), ldw,
+                                   _out_code(weights.dtype, "weights"), out.data_ptr(), ldo, s))
+    return out
+
+
+def expert_combine_backward(plan: ExpertPlan, Y, weights, dout, dY=None, dweights=None, stream=None):
+    """Gradients of expert_combine: (dY, dweights), in Y's and weights' types."""
+    import torch
+    code, ldy = _out_code(Y.dtype, "Y"), _rows_of(Y, plan.rows, None, "Y")
+    H = Y.shape[1]
+    if dout.dtype != Y.dtype:
+        raise ValueError("dout must have Y's type")
+    lddo = _rows_of(dout, plan.tokens, H, "dout")
+    wcode, ldw = _out_code(weights.dtype, "weights"), _rows_of(weights, plan.tokens, plan.slots, "weights")
+    if dY is None:
+        dY = torch.empty((plan.rows, H), dtype=Y.dtype, device=Y.device)
+    if dweights is None:
+        dweights = torch.empty((plan.tokens, plan.slots), dtype=weights.dtype, device=Y.device)
+    if dY.dtype != Y.dtype or dweights.dtype != weights.dtype:
+        raise ValueError("dY and dweights must have Y's and weights' types")
+    _check(gemm_expert_combine_backward(plan.info, H, Y.data_ptr(), ldy, dout.data_ptr(), lddo, code,
+                                        weights.data_ptr(), ldw, wcode, dY.data_ptr(),
+                                        _rows_of(dY, plan.rows, H, "dY"), dweights.data_ptr(),
+                                        _rows_of(dweights, plan.tokens, plan.slots, "dweights"),
+                                        _stream_of(Y, stream)))
+    return dY, dweights
+
+
+def gemm_w4(A, W: W4Matrix, alpha: float = 1.0, activation: int = ACT_NONE, out_dtype=None, out=None, stream=None):
+    """D = act(alpha * A @ W.T) for few tokens: A (M, K) bf16, W one matrix of 4-bit weights."""
+    return _w4(None, A, W, False, alpha, activation, out_dtype, out, stream)
+
+
+def gemm_w4_experts(A, W: W4Matrix, plan: ExpertPlan, gather: bool = False, alpha: float = 1.0,
+                    activation: int = ACT_NONE, out_dtype=None, out=None, stream=None):
+    """gemm_w4 for rows in expert order, W one matrix per expert; zeros in the rows past plan.offsets[experts].
+    gather=False: A holds plan.rows rows in expert order; True: A holds the tokens, read through plan.row_token."""
+    return _w4(plan, A, W, gather, alpha, activation, out_dtype, out, stream)
+
+
+def _w4(plan, A, W, gather, alpha, activation, out_dtype, out, stream):
+    import torch
+    if A.dtype != torch.bfloat16:
+        raise ValueError("A must be bf16")
+    rows = A.shape[0] if plan is None else plan.tokens if gather else plan.rows
+    lda = _rows_of(A, rows, W.K, "A")
+    M = rows if plan is None else plan.rows
+    if out is None:
+        out = torch.empty((M, W.N), dtype=out_dtype or torch.bfloat16, device=A.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out must have out_dtype")
+    code, ldd = _out_code(out.dtype, "out"), _rows_of(out, M, W.N, "out")
+    s = _stream_of(A, stream)
+    if plan is None:
+        _check(gemm_w4_tn(M, A.data_ptr(), lda, W.info, out.data_ptr(), ldd, alpha, code, activation, s))
+    else:
+        _check(gemm_w4_tn_experts(plan.info, A.data_ptr(), lda, int(gather), W.info, out.data_ptr(), ldd, alpha,
+                                  code, activation, s))
     return out

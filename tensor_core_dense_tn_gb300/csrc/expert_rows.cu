@@ -1,0 +1,652 @@
+// Tokens to expert order and back: the two ends of a mixture-of-experts MLP
+// around the grouped products (gemm_expert_* in include/gemm_tn.h).
+//
+//   dispatch            slot s = t k + j goes to row offsets[e] + #{s' < s : id(s') = e}, e = id(s);
+//                       Xs[row] = X[t]
+//   dispatch backward   dX[t]   = sum_j dXs[slot_row[t, j]]            (combine with weights of one)
+//   combine             out[t]  = sum_j w[t, j] Y[slot_row[t, j]]
+//   combine backward    dY[slot_row[t, j]] = w[t, j] dout[t],  dw[t, j] = <dout[t], Y[slot_row[t, j]]>
+//
+// All of them are bound by memory.  Every kernel works token by token, so
+// that the token's row is read (or written) once and only the k expert rows
+// move per slot; walking the expert rows instead would read X k times.  Sums
+// run over j in order in fp32 and are rounded once, with no atomics on data,
+// so results do not change from run to run.  Rows that no slot fills (dropped
+// slots) are set to zero by the token loop, T rows apart.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace gtn {
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// ---------------------------------------------------------------- sorting
+__device__ __forceinline__ int load_id(const ExpertParams& p, int s) {
+  const int t = s / p.k, j = s - t * p.k;
+  const long long at = (long long)t * p.ld_ids + j;
+  const long long v = p.ids64 ? static_cast<const long long*>(p.ids)[at] : static_cast<const int*>(p.ids)[at];
+  return v >= 0 && v < p.E ? (int)v : p.E;   // E = dropped
+}
+
+// Histogram of one chunk of slots: hist[chunk][e].
+__global__ void __launch_bounds__(1024) expert_hist_kernel(ExpertParams p) {
+  extern __shared__ int h[];
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) h[e] = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  __syncthreads();
+  const int lo = blockIdx.x * p.chunk, hi = min(p.n, lo + p.chunk);
+  for (int s = lo + threadIdx.x; s < hi; s += blockDim.x) {
+    const int e = load_id(p, s);
+    if (e < p.E) atomicAdd(&h[e], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[(long long)blockIdx.x * p.E + e] = h[e];
+}
+
+// Exclusive sum over the 32 lanes' values held in shared memory h[0..n), in
+// place, by one block; `carry` has one int per warp.
+__device__ void block_exclusive_scan(int* h, int n, int* carry) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int base = 0;
+  for (int at = 0; at < n; at += blockDim.x) {
+    const int i = at + threadIdx.x;
+    const int v = i < n ? h[i] : 0;
+    int x = v;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) carry[warp] = x;
+    __syncthreads();
+    int before = base, total = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) before += carry[w];
+      total += carry[w];
+    }
+    if (i < n) h[i] = before + x - v;
+    base += total;
+    __syncthreads();
+  }
+}
+
+// Rows of one chunk's slots.  Every block adds up the histograms before its
+// own chunk (and all of them, for the experts' offsets), ranks its slots in
+// slot order, one contiguous part per warp, and writes their rows.
+__global__ void __launch_bounds__(1024) expert_rank_kernel(ExpertParams p) {
+  extern __shared__ int sm[];
+  const int E = p.E, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  int* start = sm;                                       // E + 1: next row of each expert
+  int* total = sm + E + 1;                               // E + 1
+  int* carry = sm + 2 * (E + 1);                         // 32
+  uint16_t* wh = reinterpret_cast<uint16_t*>(carry + 32);   // warps x E
+  griddep_wait();
+  griddep_launch_dependents();
+  for (int e = tid; e < 2 * (E + 1); e += blockDim.x) sm[e] = 0;
+  __syncthreads();
+  // parts of the chunks added by different threads, joined by integer adds
+  const int parts = max(1, (int)blockDim.x / E);
+  for (int i = tid; i < parts * E; i += blockDim.x) {
+    const int e = i % E, part = i / E;
+    int before = 0, all = 0;
+    for (int c = part; c < p.chunks; c += parts) {
+      const int v = p.hist[(long long)c * E + e];
+      all += v;
+      if (c < (int)blockIdx.x) before += v;
+    }
+    atomicAdd(&start[e], before);
+    atomicAdd(&total[e], all);
+  }
+  __syncthreads();
+  block_exclusive_scan(total, E + 1, carry);
+  for (int e = tid; e < E; e += blockDim.x) start[e] += total[e];
+  const int V = total[E];
+  if (blockIdx.x == 0)
+    for (int e = tid; e <= E; e += blockDim.x) p.offsets[e] = total[e];
+  for (int r = V + blockIdx.x * blockDim.x + tid; r < p.n; r += gridDim.x * blockDim.x) p.row_token[r] = -1;
+  __syncthreads();
+
+  // Steps of blockDim slots per warp part; kSteps warps' worth in registers.
+  constexpr int kSteps = 4;
+  const int lo = blockIdx.x * p.chunk, hi = min(p.n, lo + p.chunk);
+  for (int base = lo; base < hi; base += kSteps * (int)blockDim.x) {
+    for (int i = tid; i < warps * E; i += blockDim.x) wh[i] = 0;
+    __syncthreads();
+    int id[kSteps], rank[kSteps];
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int s = base + (warp * kSteps + q) * 32 + lane;
+      id[q] = s < hi ? load_id(p, s) : E;
+    }
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, id[q]);
+      const int prior = id[q] < E ? wh[warp * E + id[q]] : 0;
+      rank[q] = prior + __popc(same & ((1u << lane) - 1));
+      __syncwarp();
+      if (id[q] < E && lane == __ffs(same) - 1) wh[warp * E + id[q]] = (uint16_t)(prior + __popc(same));
+      __syncwarp();
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += blockDim.x) {   // exclusive over the warps, and on to the next steps
+      int x = 0;
+      for (int w = 0; w < warps; ++w) {
+        const int v = wh[w * E + e];
+        wh[w * E + e] = (uint16_t)x;
+        x += v;
+      }
+      total[e] = start[e];
+      start[e] += x;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < kSteps; ++q) {
+      const int s = base + (warp * kSteps + q) * 32 + lane;
+      if (s < hi) {
+        int row = -1;
+        if (id[q] < E) {
+          row = total[id[q]] + wh[warp * E + id[q]] + rank[q];
+          p.row_token[row] = s / p.k;
+        }
+        p.slot_row[s] = row;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------- rows
+// A chunk of CH bytes of a row (16 where every row allows it, else one element).
+template <int CH> struct Raw;
+template <> struct Raw<16> { using T = uint4; };
+template <> struct Raw<4> { using T = uint32_t; };
+template <> struct Raw<2> { using T = uint16_t; };
+
+template <int CH>
+__device__ __forceinline__ typename Raw<CH>::T zero_raw() {
+  if constexpr (CH == 16) return make_uint4(0, 0, 0, 0);
+  else return 0;
+}
+
+// CH bytes <-> fp32 values (ES = element size).
+template <int ES, int CH>
+__device__ __forceinline__ void unpack(typename Raw<CH>::T v, float (&x)[CH / ES]) {
+  if constexpr (CH == 16 && ES == 2) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else if constexpr (CH == 16) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+  } else if constexpr (ES == 4) {
+    x[0] = __uint_as_float(v);
+  } else {
+    x[0] = __uint_as_float((uint32_t)v << 16);
+  }
+}
+
+template <int ES, int CH>
+__device__ __forceinline__ typename Raw<CH>::T pack(const float (&x)[CH / ES]) {
+  if constexpr (CH == 16 && ES == 2) {
+    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                      pack_bf16x2(x[6], x[7]));
+  } else if constexpr (CH == 16) {
+    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+  } else if constexpr (ES == 4) {
+    return __float_as_uint(x[0]);
+  } else {
+    return (uint16_t)pack_bf16x2(x[0], 0.0f);
+  }
+}
+
+template <int CH>
+__device__ __forceinline__ typename Raw<CH>::T ldc(const void* base, long long row_bytes, long long row, int c) {
+  return reinterpret_cast<const typename Raw<CH>::T*>(static_cast<const char*>(base) + row * row_bytes)[c];
+}
+template <int CH>
+__device__ __forceinline__ void stc(void* base, long long row_bytes, long long row, int c, typename Raw<CH>::T v) {
+  reinterpret_cast<typename Raw<CH>::T*>(static_cast<char*>(base) + row * row_bytes)[c] = v;
+}
+
+__device__ __forceinline__ float load_weight(const ExpertParams& p, int t, int j) {
+  if (!p.weights) return 1.0f;
+  const long long at = (long long)t * p.ld_w + j;
+  if (p.w_f32) return static_cast<const float*>(p.weights)[at];
+  return __uint_as_float((uint32_t) static_cast<const uint16_t*>(p.weights)[at] << 16);
+}
+
+// Row of slot j of token t; -1 where it is dropped (or not a row at all).
+__device__ __forceinline__ int load_row(const ExpertParams& p, int t, int j) {
+  if (j >= p.k) return -1;
+  const int r = p.slot_row[t * p.k + j];
+  return r >= 0 && r < p.n ? r : -1;
+}
+
+// Copies token t's row to the rows r[0..count); U chunks per lane in flight.
+template <int CH, int U>
+__device__ __forceinline__ void copy_row(const ExpertParams& p, int t, const int* r, int count, int lane, int lanes) {
+  using R = typename Raw<CH>::T;
+  for (int c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += lanes * U * gridDim.y) {
+    R x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * lanes < p.nch) x[u] = ldc<CH>(p.in, p.in_pitch, t, c0 + u * lanes);
+    for (int j = 0; j < count; ++j) {
+      if (r[j] < 0) continue;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (c0 + u * lanes < p.nch) stc<CH>(p.out, p.out_pitch, r[j], c0 + u * lanes, x[u]);
+    }
+  }
+}
+
+// Zeroes row r of p.out, by `lanes` threads of each of the gridDim.y blocks.
+template <int CH>
+__device__ __forceinline__ void zero_row(const ExpertParams& p, long long r, int lane, int lanes) {
+  for (int c = lane + lanes * blockIdx.y; c < p.nch; c += lanes * gridDim.y) stc<CH>(p.out, p.out_pitch, r, c, zero_raw<CH>());
+}
+
+// Rows past 16-byte chunks: the last H % (16 / ES) elements of each row go
+// element by element through the same code, as a second, short "row".
+template <int ES>
+__device__ __forceinline__ ExpertParams tail_of(ExpertParams p, int ch) {
+  const long long done = (long long)p.nch * ch;
+  p.in = static_cast<const char*>(p.in) + done;
+  if (p.out) p.out = static_cast<char*>(p.out) + done;
+  if (p.in2) p.in2 = static_cast<const char*>(p.in2) + done;
+  p.nch = p.tail;
+  p.tail = 0;
+  return p;
+}
+
+template <int ES, int CH, int U>
+__global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(ExpertParams p) {
+  extern __shared__ int rows[];   // (threads / lanes) x k
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lanes = p.lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int per = kRowThreads / lanes;
+  const int t0 = blockIdx.x * per;
+  for (int i = threadIdx.x; i < per * p.k; i += kRowThreads) {
+    const int t = t0 + i / p.k;
+    rows[i] = t < p.T ? load_row(p, t, i % p.k) : -1;
+  }
+  const int V = p.offsets[p.E];
+  __syncthreads();
+  const int t = t0 + group;
+  if (t >= p.T) return;
+  copy_row<CH, U>(p, t, rows + group * p.k, p.k, lane, lanes);
+  if (p.tail) copy_row<ES, 1>(tail_of<ES>(p, CH), t, rows + group * p.k, p.k, lane, lanes);
+  for (long long r = V + t; r < p.n; r += p.T) {
+    zero_row<CH>(p, r, lane, lanes);
+    if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
+  }
+}
+
+// The whole dispatch of few slots in one launch: every block counts its own
+// slots' rows against all ids (held in shared memory), then copies.
+template <int ES, int CH, int U>
+__global__ void __launch_bounds__(kRowThreads) expert_dispatch_small_kernel(ExpertParams p) {
+  extern __shared__ int sm[];
+  const int lanes = p.lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int per = kRowThreads / lanes;
+  const int t0 = blockIdx.x * per;
+  int* ids = sm;               // n
+  int* rows = sm + p.n;        // per * k
+  __shared__ int filled;
+  if (threadIdx.x == 0) filled = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  __syncthreads();
+  int mine = 0;
+  for (int s = threadIdx.x; s < p.n; s += kRowThreads) {
+    ids[s] = load_id(p, s);
+    mine += ids[s] < p.E;
+  }
+  if (mine) atomicAdd(&filled, mine);
+  __syncthreads();
+  const int wl = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = kRowThreads / 32;
+  for (int i = warp; i < per * p.k; i += warps) {      // a warp counts one slot's row
+    const int s = t0 * p.k + i;
+    int row = -1;
+    if (s < p.n && ids[s] < p.E) {
+      const int e = ids[s];
+      int c = 0;
+      for (int o = wl; o < p.n; o += 32) c += ids[o] < e || (ids[o] == e && o < s);
+      row = __reduce_add_sync(0xFFFFFFFFu, c);
+    }
+    if (wl == 0) {
+      rows[i] = row;
+      if (s < p.n && blockIdx.y == 0) {
+        p.slot_row[s] = row;
+        if (row >= 0) p.row_token[row] = s / p.k;
+      }
+    }
+  }
+  const int V = filled;
+  if (blockIdx.y == 0) {
+    for (int e = blockIdx.x * warps + warp; e <= p.E; e += gridDim.x * warps) {
+      int c = 0;
+      for (int o = wl; o < p.n; o += 32) c += ids[o] < e;
+      c = __reduce_add_sync(0xFFFFFFFFu, c);
+      if (wl == 0) p.offsets[e] = c;
+    }
+    for (int r = V + blockIdx.x * kRowThreads + threadIdx.x; r < p.n; r += gridDim.x * kRowThreads) p.row_token[r] = -1;
+  }
+  __syncthreads();
+  const int t = t0 + group;
+  if (t >= p.T) return;
+  copy_row<CH, U>(p, t, rows + group * p.k, p.k, lane, lanes);
+  if (p.tail) copy_row<ES, 1>(tail_of<ES>(p, CH), t, rows + group * p.k, p.k, lane, lanes);
+  if (p.nch + p.tail > 0)
+    for (long long r = V + t; r < p.n; r += p.T) {
+      zero_row<CH>(p, r, lane, lanes);
+      if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
+    }
+}
+
+// out[t] = sum_j w_j in[r_j], slots in blocks of KU with all their loads in flight.
+template <int ES, int CH, int KU, int U>
+__device__ __forceinline__ void combine_row(const ExpertParams& p, int t, int lane, int lanes) {
+  using R = typename Raw<CH>::T;
+  constexpr int V = CH / ES;
+  for (int c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += lanes * U * gridDim.y) {
+    float acc[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[u][v] = 0.0f;
+    for (int j0 = 0; j0 < p.k; j0 += KU) {
+      int r[KU];
+      float w[KU];
+#pragma unroll
+      for (int j = 0; j < KU; ++j) {
+        r[j] = load_row(p, t, j0 + j);
+        w[j] = r[j] >= 0 ? load_weight(p, t, j0 + j) : 0.0f;
+      }
+      R x[KU][U];
+#pragma unroll
+      for (int j = 0; j < KU; ++j)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          x[j][u] = r[j] >= 0 && c0 + u * lanes < p.nch ? ldc<CH>(p.in, p.in_pitch, r[j], c0 + u * lanes) : zero_raw<CH>();
+#pragma unroll
+      for (int j = 0; j < KU; ++j)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          float f[V];
+          unpack<ES, CH>(x[j][u], f);
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[u][v] = fmaf(w[j], f[v], acc[u][v]);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u * lanes < p.nch) stc<CH>(p.out, p.out_pitch, t, c0 + u * lanes, pack<ES, CH>(acc[u]));
+  }
+}
+
+template <int ES, int CH, int KU, int U>
+__global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(ExpertParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lanes = p.lanes, t = blockIdx.x * (kRowThreads / lanes) + threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  if (t >= p.T) return;
+  combine_row<ES, CH, KU, U>(p, t, lane, lanes);
+  if (p.tail) combine_row<ES, ES, KU, 1>(tail_of<ES>(p, CH), t, lane, lanes);
+}
+
+// in = dout, in2 = Y, out = dY.  Adds the lane's part of <dout, Y_j> to dot[j].
+template <int ES, int CH, int KU, int U>
+__device__ __forceinline__ void combine_back_row(const ExpertParams& p, int t, const int (&r)[KU], const float (&w)[KU],
+                                                 float (&dot)[KU], int lane, int lanes) {
+  using R = typename Raw<CH>::T;
+  constexpr int V = CH / ES;
+  for (int c0 = lane; c0 < p.nch; c0 += lanes * U) {
+    R d[U], y[KU][U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      d[u] = c0 + u * lanes < p.nch ? ldc<CH>(p.in, p.in_pitch, t, c0 + u * lanes) : zero_raw<CH>();
+    if (p.dweights) {
+#pragma unroll
+      for (int j = 0; j < KU; ++j)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          y[j][u] = r[j] >= 0 && c0 + u * lanes < p.nch ? ldc<CH>(p.in2, p.in2_pitch, r[j], c0 + u * lanes) : zero_raw<CH>();
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (c0 + u * lanes >= p.nch) continue;
+      float f[V];
+      unpack<ES, CH>(d[u], f);
+#pragma unroll
+      for (int j = 0; j < KU; ++j) {
+        if (r[j] < 0) continue;
+        if (p.dweights) {
+          float g[V];
+          unpack<ES, CH>(y[j][u], g);
+#pragma unroll
+          for (int v = 0; v < V; ++v) dot[j] = fmaf(f[v], g[v], dot[j]);
+        }
+        if (p.out) {
+          float o[V];
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[v] = w[j] * f[v];
+          stc<CH>(p.out, p.out_pitch, r[j], c0 + u * lanes, pack<ES, CH>(o));
+        }
+      }
+    }
+  }
+}
+
+template <int ES, int CH, int KU, int U>
+__global__ void __launch_bounds__(kRowThreads) expert_combine_back_kernel(ExpertParams p) {
+  __shared__ float part[KU][kRowThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lanes = p.lanes, per = kRowThreads / lanes;    // lanes is a multiple of 32
+  const int t = blockIdx.x * per + threadIdx.x / lanes, lane = threadIdx.x % lanes;
+  const int wl = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int j0 = 0; j0 < p.k; j0 += KU) {
+    int r[KU];
+    float w[KU], dot[KU];
+#pragma unroll
+    for (int j = 0; j < KU; ++j) {
+      r[j] = t < p.T ? load_row(p, t, j0 + j) : -1;
+      w[j] = r[j] >= 0 ? load_weight(p, t, j0 + j) : 0.0f;
+      dot[j] = 0.0f;
+    }
+    if (t < p.T) {
+      combine_back_row<ES, CH, KU, U>(p, t, r, w, dot, lane, lanes);
+      if (p.tail) combine_back_row<ES, ES, KU, 1>(tail_of<ES>(p, CH), t, r, w, dot, lane, lanes);
+    }
+    if (p.dweights) {
+#pragma unroll
+      for (int j = 0; j < KU; ++j) {
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) dot[j] += __shfl_xor_sync(0xFFFFFFFFu, dot[j], d);
+        if (wl == 0) part[j][warp] = dot[j];
+      }
+      __syncthreads();
+      const int warps = lanes / 32, tg = threadIdx.x / KU, j = threadIdx.x % KU;   // one thread per (token, slot)
+      if (tg < per && blockIdx.x * per + tg < p.T && j0 + j < p.k) {
+        float s = 0.0f;
+        for (int i = 0; i < warps; ++i) s += part[j][tg * warps + i];
+        const long long at = (long long)(blockIdx.x * per + tg) * p.ld_dw + j0 + j;
+        if (p.w_f32) static_cast<float*>(p.dweights)[at] = s;
+        else static_cast<uint16_t*>(p.dweights)[at] = (uint16_t)pack_bf16x2(s, 0.0f);
+      }
+      __syncthreads();
+    }
+  }
+  if (p.out && t < p.T) {
+    const int V = p.offsets[p.E];
+    for (long long r = V + t; r < p.n; r += p.T) {
+      zero_row<CH>(p, r, lane, lanes);
+      if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- launches
+cudaError_t launch(const void* kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, ExpertParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* args[1] = {&p};
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+// Lanes per token: the power of two in [least, 256] that covers the row with
+// U chunks per lane.
+int lanes_for(long long nch, int U, int least) {
+  int l = least;
+  while (l < kRowThreads && (long long)l * U < nch) l *= 2;
+  return l;
+}
+
+// Token blocks, and where they are too few for the GPU, blocks along the row.
+dim3 row_grid(const ExpertParams& p, int U, int sms) {
+  const int per = kRowThreads / p.lanes;
+  const long long gx = ((long long)p.T + per - 1) / per;
+  const long long cols = (p.nch + (long long)p.lanes * U - 1) / ((long long)p.lanes * U);
+  long long gy = 1;
+  while (gy * 2 <= cols && gx * gy < 2 * sms) gy *= 2;
+  return dim3((unsigned)gx, (unsigned)gy);
+}
+
+// Chunks of a row for this launch's alignment; false = element by element.
+void set_chunks(ExpertParams* p, int es, bool vec) {
+  if (vec) {
+    p->nch = (int)(p->H * es / 16);
+    p->tail = (int)(p->H - (long long)p->nch * 16 / es);
+  } else {
+    p->nch = (int)p->H;
+    p->tail = 0;
+  }
+}
+
+bool row_aligned(const void* base, long long pitch) {
+  return !base || ((reinterpret_cast<uintptr_t>(base) & 15u) == 0 && pitch % 16 == 0);
+}
+
+}  // namespace
+
+int expert_chunks(long long n) {
+  const long long c = (n + 1023) / 1024;
+  return (int)(c < 1 ? 1 : (c > kExpertMaxChunks ? kExpertMaxChunks : c));
+}
+
+cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info) {
+  const bool vec = row_aligned(p.in, p.in_pitch) && row_aligned(p.out, p.out_pitch);
+  set_chunks(&p, es, vec);
+  const int U = vec ? 2 : 4;
+  p.lanes = lanes_for(p.nch, U, 8);
+  if (p.n <= kExpertSmallSlots) {
+    if (p.lanes < 32) p.lanes = 32;    // counting rows is the work here: 8 tokens a block at most
+    if (p.T < 1) p.lanes = kRowThreads;
+    dim3 grid = row_grid(p, U, sms);
+    if (grid.x < 1) grid.x = 1;
+    const size_t smem = ((size_t)p.n + (size_t)(kRowThreads / p.lanes) * p.k) * sizeof(int);
+    const void* f = !vec ? (es == 2 ? (const void*)expert_dispatch_small_kernel<2, 2, 4>
+                                    : (const void*)expert_dispatch_small_kernel<4, 4, 4>)
+                         : (es == 2 ? (const void*)expert_dispatch_small_kernel<2, 16, 2>
+                                    : (const void*)expert_dispatch_small_kernel<4, 16, 2>);
+    *info = LaunchInfo{};
+    info->grid = grid.x * grid.y; info->cluster = 1; info->block = kRowThreads; info->smem_bytes = (int)smem;
+    info->kernel = "expert_dispatch_small_kernel";
+    return launch(f, grid, kRowThreads, smem, stream, p);
+  }
+  const size_t rank_smem = (2 * ((size_t)p.E + 1) + 32) * sizeof(int) + (size_t)32 * p.E * sizeof(uint16_t);
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && !configured[dev]) {
+    e = cudaFuncSetAttribute((const void*)expert_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)((2 * (kExpertMax + 1) + 32) * sizeof(int) + 32 * kExpertMax * sizeof(uint16_t)));
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  p.chunks = expert_chunks(p.n);
+  p.chunk = (int)(((long long)p.n + p.chunks - 1) / p.chunks);
+  if ((e = launch((const void*)expert_hist_kernel, dim3(p.chunks), 1024, (size_t)p.E * sizeof(int), stream, p))) return e;
+  if ((e = launch((const void*)expert_rank_kernel, dim3(p.chunks), 1024, rank_smem, stream, p))) return e;
+  *info = LaunchInfo{};
+  info->grid = p.chunks; info->cluster = 1; info->block = 1024; info->smem_bytes = (int)rank_smem;
+  info->kernel = "expert_rank_kernel";
+  if (p.H == 0) return cudaSuccess;
+  const dim3 grid = row_grid(p, U, sms);
+  const size_t smem = (size_t)(kRowThreads / p.lanes) * p.k * sizeof(int);
+  const void* f = !vec ? (es == 2 ? (const void*)expert_gather_kernel<2, 2, 4> : (const void*)expert_gather_kernel<4, 4, 4>)
+                       : (es == 2 ? (const void*)expert_gather_kernel<2, 16, 2> : (const void*)expert_gather_kernel<4, 16, 2>);
+  info->grid = grid.x * grid.y; info->block = kRowThreads; info->smem_bytes = (int)smem;
+  info->kernel = "expert_gather_kernel";
+  return launch(f, grid, kRowThreads, smem, stream, p);
+}
+
+namespace {
+
+template <int KU>
+const void* combine_fn(int es, bool vec) {
+  constexpr int U = KU >= 8 ? 1 : (KU >= 4 ? 2 : 4), US = KU >= 8 ? 2 : 4;
+  if (vec) return es == 2 ? (const void*)expert_combine_kernel<2, 16, KU, U> : (const void*)expert_combine_kernel<4, 16, KU, U>;
+  return es == 2 ? (const void*)expert_combine_kernel<2, 2, KU, US> : (const void*)expert_combine_kernel<4, 4, KU, US>;
+}
+template <int KU>
+const void* combine_back_fn(int es, bool vec) {
+  constexpr int U = KU >= 4 ? 1 : 2, US = KU >= 8 ? 2 : 4;
+  if (vec) return es == 2 ? (const void*)expert_combine_back_kernel<2, 16, KU, U> : (const void*)expert_combine_back_kernel<4, 16, KU, U>;
+  return es == 2 ? (const void*)expert_combine_back_kernel<2, 2, KU, US> : (const void*)expert_combine_back_kernel<4, 4, KU, US>;
+}
+int slots_unrolled(int k) { return k <= 1 ? 1 : (k <= 2 ? 2 : (k <= 4 ? 4 : 8)); }
+
+}  // namespace
+
+cudaError_t launch_expert_combine(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info) {
+  const bool vec = row_aligned(p.in, p.in_pitch) && row_aligned(p.out, p.out_pitch);
+  set_chunks(&p, es, vec);
+  const int ku = slots_unrolled(p.k);
+  const int U = vec ? (ku >= 8 ? 1 : (ku >= 4 ? 2 : 4)) : (ku >= 8 ? 2 : 4);
+  p.lanes = lanes_for(p.nch, U, 1);
+  const dim3 grid = row_grid(p, U, sms);
+  const void* f = ku == 1 ? combine_fn<1>(es, vec) : ku == 2 ? combine_fn<2>(es, vec) : ku == 4 ? combine_fn<4>(es, vec)
+                                                                                                 : combine_fn<8>(es, vec);
+  *info = LaunchInfo{};
+  info->grid = grid.x * grid.y; info->cluster = 1; info->block = kRowThreads;
+  info->kernel = "expert_combine_kernel";
+  return launch(f, grid, kRowThreads, 0, stream, p);
+}
+
+cudaError_t launch_expert_combine_back(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info) {
+  const bool vec = row_aligned(p.in, p.in_pitch) && row_aligned(p.out, p.out_pitch) && row_aligned(p.in2, p.in2_pitch);
+  set_chunks(&p, es, vec);
+  const int ku = slots_unrolled(p.k);
+  const int U = vec ? (ku >= 4 ? 1 : 2) : (ku >= 8 ? 2 : 4);
+  p.lanes = lanes_for(p.nch, U, 32);
+  const int per = kRowThreads / p.lanes;
+  const dim3 grid((p.T + per - 1) / per);
+  const void* f = ku == 1 ? combine_back_fn<1>(es, vec) : ku == 2 ? combine_back_fn<2>(es, vec)
+                  : ku == 4 ? combine_back_fn<4>(es, vec) : combine_back_fn<8>(es, vec);
+  *info = LaunchInfo{};
+  info->grid = grid.x; info->cluster = 1; info->block = kRowThreads;
+  info->kernel = "expert_combine_back_kernel";
+  return launch(f, grid, kRowThreads, 0, stream, p);
+}
+
+}  // namespace gtn

@@ -773,6 +773,254 @@ int run_batched(int64_t batch, int64_t M, int64_t N, int64_t K, const void* A, i
   return GEMM_OK;
 }
 
+// ---------------------------------------------------------------- experts
+int dtype_bytes(int dtype) { return dtype == GEMM_OUT_F32 ? 4 : 2; }
+
+bool aligned_to(const void* p, int bytes) { return reinterpret_cast<uintptr_t>(p) % (uintptr_t)bytes == 0; }
+
+// A T x k or row matrix argument: present, wide enough, on its element size.
+int check_rows(const char* what, const void* base, int64_t ld, int64_t width, int esize) {
+  if (!base) return fail(GEMM_ERR_INVALID_VALUE, "%s is NULL", what);
+  if (ld < width)
+    return fail(GEMM_ERR_INVALID_VALUE, "leading dimension of %s (%lld) below its row length (%lld)", what,
+                (long long)ld, (long long)width);
+  if (!aligned_to(base, esize)) return fail(GEMM_ERR_MISALIGNED, "%s must be aligned to its element size", what);
+  return GEMM_OK;
+}
+
+int check_dtype(const char* what, int dtype) {
+  if (dtype != GEMM_OUT_BF16 && dtype != GEMM_OUT_F32)
+    return fail(GEMM_ERR_INVALID_VALUE, "%s must be 0 (bf16) or 1 (fp32), got %d", what, dtype);
+  return GEMM_OK;
+}
+
+// Validates the plan and the row length, and fills the sizes of *p.
+int check_plan(const gemm_expert_plan* plan, int64_t H, ExpertParams* p) {
+  *p = ExpertParams{};
+  if (!plan) return fail(GEMM_ERR_INVALID_VALUE, "plan is NULL");
+  if (plan->tokens < 0 || plan->slots < 1 || plan->slots > kExpertMaxSlots || plan->experts < 1 ||
+      plan->experts > kExpertMax)
+    return fail(GEMM_ERR_INVALID_VALUE, "plan needs tokens >= 0, 1..%d slots and 1..%d experts (got %lld, %d, %d)",
+                kExpertMaxSlots, kExpertMax, (long long)plan->tokens, plan->slots, plan->experts);
+  const int64_t kMaxDim = (int64_t)1 << 31;
+  if (plan->tokens >= kMaxDim || plan->tokens * plan->slots >= kMaxDim - 4096)
+    return fail(GEMM_ERR_INVALID_VALUE, "tokens * slots must be below 2^31 - 4096");
+  if (H < 0 || H >= kMaxDim) return fail(GEMM_ERR_INVALID_VALUE, "row length must be in [0, 2^31), got %lld", (long long)H);
+  if (!plan->offsets || (plan->tokens > 0 && (!plan->slot_row || !plan->row_token)))
+    return fail(GEMM_ERR_INVALID_VALUE, "an array of the plan is NULL");
+  if (!aligned_to(plan->offsets, 4) || !aligned_to(plan->slot_row, 4) || !aligned_to(plan->row_token, 4))
+    return fail(GEMM_ERR_MISALIGNED, "the plan's arrays must be aligned to 4 bytes");
+  p->T = (int)plan->tokens;
+  p->k = plan->slots;
+  p->E = plan->experts;
+  p->n = p->T * p->k;
+  p->H = H;
+  p->offsets = plan->offsets;
+  p->slot_row = plan->slot_row;
+  p->row_token = plan->row_token;
+  return GEMM_OK;
+}
+
+int finish_launch(cudaError_t e, const LaunchInfo& li) {
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return fail(GEMM_ERR_LAUNCH, "kernel launch failed: %s", cudaGetErrorString(e));
+  }
+  record_launch(li);
+  return GEMM_OK;
+}
+
+int run_expert_dispatch(const gemm_expert_plan* plan, const void* ids, int64_t ld_ids, int ids_64bit, int64_t H,
+                        const void* X, int64_t ldx, int dtype, void* Xs, int64_t ldxs, void* stream_v) {
+  t_error.clear();
+  ExpertParams p;
+  int rc = check_plan(plan, X ? H : 0, &p);
+  if (rc) return rc;
+  if (ids_64bit != 0 && ids_64bit != 1) return fail(GEMM_ERR_INVALID_VALUE, "ids_64bit must be 0 or 1, got %d", ids_64bit);
+  if (p.T > 0 && (rc = check_rows("ids", ids, ld_ids, p.k, ids_64bit ? 8 : 4))) return rc;
+  int es = 2;
+  if (p.H > 0 && p.T > 0) {
+    if ((rc = check_dtype("dtype", dtype))) return rc;
+    es = dtype_bytes(dtype);
+    if ((rc = check_rows("X", X, ldx, H, es)) || (rc = check_rows("Xs", Xs, ldxs, H, es))) return rc;
+    p.in = X;
+    p.in_pitch = ldx * es;
+    p.out = Xs;
+    p.out_pitch = ldxs * es;
+  } else {
+    p.H = 0;
+  }
+  p.ids = ids;
+  p.ld_ids = ld_ids;
+  p.ids64 = ids_64bit;
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = init_device(&dev, &st))) return rc;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+  if (p.n > kExpertSmallSlots) {
+    Workspace* w = nullptr;
+    if ((rc = get_workspace(dev, stream, (size_t)expert_chunks(p.n) * p.E, 0, &w))) return rc;
+    p.hist = reinterpret_cast<int*>(w->partials);
+  }
+  LaunchInfo li = {};
+  return finish_launch(launch_expert_dispatch(p, es, st->sms, stream, &li), li);
+}
+
+// Combine, and with weights == nullptr the gradient of the dispatch copy.
+int run_expert_combine(const gemm_expert_plan* plan, int64_t H, const void* Y, int64_t ldy, int dtype,
+                       const void* weights, int64_t ldw, int weights_dtype, bool weighted, void* out, int64_t ldo,
+                       void* stream) {
+  t_error.clear();
+  ExpertParams p;
+  int rc = check_plan(plan, H, &p);
+  if (rc || (rc = check_dtype("dtype", dtype))) return rc;
+  if (weighted && (rc = check_dtype("weights_dtype", weights_dtype))) return rc;
+  if (p.T == 0 || H == 0) return GEMM_OK;
+  const int es = dtype_bytes(dtype);
+  if ((rc = check_rows(weighted ? "Y" : "dXs", Y, ldy, H, es)) || (rc = check_rows(weighted ? "out" : "dX", out, ldo, H, es)))
+    return rc;
+  if (weighted) {
+    if ((rc = check_rows("weights", weights, ldw, p.k, dtype_bytes(weights_dtype)))) return rc;
+    p.weights = weights;
+    p.ld_w = ldw;
+    p.w_f32 = weights_dtype == GEMM_OUT_F32;
+  }
+  p.in = Y;
+  p.in_pitch = ldy * es;
+  p.out = out;
+  p.out_pitch = ldo * es;
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = init_device(&dev, &st))) return rc;
+  LaunchInfo li = {};
+  return finish_launch(launch_expert_combine(p, es, st->sms, static_cast<cudaStream_t>(stream), &li), li);
+}
+
+int run_expert_combine_backward(const gemm_expert_plan* plan, int64_t H, const void* Y, int64_t ldy, const void* dout,
+                                int64_t lddo, int dtype, const void* weights, int64_t ldw, int weights_dtype, void* dY,
+                                int64_t lddy, void* dweights, int64_t lddw, void* stream) {
+  t_error.clear();
+  ExpertParams p;
+  int rc = check_plan(plan, H, &p);
+  if (rc || (rc = check_dtype("dtype", dtype)) || (rc = check_dtype("weights_dtype", weights_dtype))) return rc;
+  if (p.T == 0 || (!dY && !dweights)) return GEMM_OK;
+  const int es = dtype_bytes(dtype), ws = dtype_bytes(weights_dtype);
+  if (H > 0 && (rc = check_rows("dout", dout, lddo, H, es))) return rc;
+  if ((rc = check_rows("weights", weights, ldw, p.k, ws))) return rc;
+  if (dweights && ((H > 0 && (rc = check_rows("Y", Y, ldy, H, es))) ||
+                   (rc = check_rows("dweights", dweights, lddw, p.k, ws))))
+    return rc;
+  if (dY && H > 0 && (rc = check_rows("dY", dY, lddy, H, es))) return rc;
+  p.weights = weights;
+  p.ld_w = ldw;
+  p.w_f32 = weights_dtype == GEMM_OUT_F32;
+  p.dweights = dweights;
+  p.ld_dw = lddw;
+  p.in = dout;
+  p.in_pitch = lddo * es;
+  p.in2 = dweights ? Y : nullptr;
+  p.in2_pitch = ldy * es;
+  p.out = H > 0 ? dY : nullptr;
+  p.out_pitch = lddy * es;
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = init_device(&dev, &st))) return rc;
+  LaunchInfo li = {};
+  return finish_launch(launch_expert_combine_back(p, es, st->sms, static_cast<cudaStream_t>(stream), &li), li);
+}
+
+// ---------------------------------------------------------------- 4-bit weights
+// plan == nullptr: the dense form of M rows; else R = plan's slots by expert.
+int run_w4(int64_t M, const gemm_expert_plan* plan, int gather, const void* A, int64_t lda, const gemm_w4_matrix* W,
+           void* D, int64_t ldd, float alpha, int out_dtype, int activation, void* stream_v) {
+  t_error.clear();
+  int rc = check_dtype("out_dtype", out_dtype);
+  if (rc) return rc;
+  if (activation < GEMM_ACT_NONE || activation > GEMM_ACT_SILU)
+    return fail(GEMM_ERR_INVALID_VALUE, "unknown activation %d", activation);
+  if (!W) return fail(GEMM_ERR_INVALID_VALUE, "W is NULL");
+  const int64_t kMaxDim = (int64_t)1 << 31;
+  if (M < 0 || W->N < 0 || W->K < 0 || M >= kMaxDim - 4096 || W->N >= kMaxDim - 4096 || W->K >= kMaxDim - 4096)
+    return fail(GEMM_ERR_INVALID_VALUE, "sizes must be in [0, 2^31 - 4096): M=%lld N=%lld K=%lld", (long long)M,
+                (long long)W->N, (long long)W->K);
+  const int g = W->group;
+  if (g != 32 && g != 64 && g != 128 && (g < kW4StageK || g % kW4StageK))
+    return fail(GEMM_ERR_INVALID_VALUE, "group must be 32, 64, 128 or a multiple of 256, got %d", g);
+  if ((rc = check_dtype("scales_dtype", W->scales_dtype))) return rc;
+  W4Params p = {};
+  if (plan) {
+    ExpertParams ep;
+    if ((rc = check_plan(plan, 0, &ep))) return rc;
+    if (gather != 0 && gather != 1) return fail(GEMM_ERR_INVALID_VALUE, "gather must be 0 or 1, got %d", gather);
+    if (W->count != ep.E)
+      return fail(GEMM_ERR_INVALID_VALUE, "W holds %lld matrices for %d experts", (long long)W->count, ep.E);
+    M = ep.n;
+    p.offsets = ep.offsets;
+    p.E = ep.E;
+    p.a_rows = gather ? ep.row_token : nullptr;
+    p.a_count = gather ? ep.T : ep.n;
+  } else {
+    if (W->count != 1) return fail(GEMM_ERR_INVALID_VALUE, "W must hold one matrix, got %lld", (long long)W->count);
+    p.a_count = (int)M;
+  }
+  if (M == 0 || W->N == 0) return GEMM_OK;
+  const int esize = dtype_bytes(out_dtype);
+  if ((rc = check_rows("D", D, ldd, W->N, esize))) return rc;
+  p.ngroups = (int)((W->K + g - 1) / g);
+  if (W->K > 0) {
+    if ((rc = check_rows("A", A, lda, W->K, 2))) return rc;
+    if (!aligned16(A) || lda % 8)
+      return fail(GEMM_ERR_MISALIGNED, "A must be 16-byte aligned with lda a multiple of 8");
+    if ((rc = check_rows("codes", W->codes, W->ldc, W->K, 1))) return rc;
+    if (!aligned16(W->codes) || W->ldc % 32)
+      return fail(GEMM_ERR_MISALIGNED, "codes must be 16-byte aligned with ldc a multiple of 32");
+    if ((rc = check_rows("scales", W->scales, W->lds, p.ngroups, dtype_bytes(W->scales_dtype)))) return rc;
+    if (W->zeros && (rc = check_rows("zeros", W->zeros, W->ldz, p.ngroups, 1))) return rc;
+    if (W->count > 1) {
+      if (W->stride_codes < W->N * W->ldc || W->stride_scales < 0 || W->stride_zeros < 0)
+        return fail(GEMM_ERR_INVALID_VALUE, "stride_codes (%lld) must be at least N * ldc, and no stride negative",
+                    (long long)W->stride_codes);
+      if (W->stride_codes % 32) return fail(GEMM_ERR_MISALIGNED, "stride_codes must be a multiple of 32");
+    }
+  }
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = init_device(&dev, &st))) return rc;
+  CUtensorMap tm;
+  memset(&tm, 0, sizeof tm);
+  if (W->K > 0) {
+    const int64_t stride = W->count > 1 ? W->stride_codes : W->N * W->ldc;
+    if ((rc = encode_3d(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, W->codes, (W->K + 1) / 2, W->N, W->count, W->ldc / 2,
+                        stride / 2, kW4StageK / 2, kW4TileRows, CU_TENSOR_MAP_SWIZZLE_128B, "codes")))
+      return rc;
+  }
+  p.M = (int)M;
+  p.N = (int)W->N;
+  p.K = (int)W->K;
+  p.group = g;
+  p.scales = W->scales;
+  p.ld_s = W->lds;
+  p.stride_s = W->stride_scales;
+  p.s_f32 = W->scales_dtype == GEMM_OUT_F32;
+  p.zeros = static_cast<const uint8_t*>(W->zeros);
+  p.ld_z = W->ldz;
+  p.stride_z = W->stride_zeros;
+  p.A = A;
+  p.lda = lda;
+  p.D = D;
+  p.ldd = ldd;
+  p.out_f32 = out_dtype == GEMM_OUT_F32;
+  p.act = activation;
+  p.alpha = alpha;
+  p.num_kb = (int)((W->K + kW4StageK - 1) / kW4StageK);
+  const int active = plan ? (int)(p.E < M ? p.E : M) : 1;
+  p.split = w4_split((W->N + kW4TileRows - 1) / kW4TileRows * active, p.num_kb, st->sms);
+  p.timeout_ns = timeout_ns(nullptr);
+  p.status = st->status;
+  LaunchInfo li = {};
+  return finish_launch(launch_w4(tm, p, active, static_cast<cudaStream_t>(stream_v), &li), li);
+}
+
 }  // namespace
 
 // Sets the text gemm_last_error_string returns on this thread, for entry
@@ -874,6 +1122,39 @@ int gemm_fp8_tn(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, con
                 float alpha, float beta, int out_dtype, void* stream) {
   return gemm_fp8_tn_ex(M, N, K, A, lda, B, ldb, fp8_format, scale_a, scale_b, C, ldc, D, ldd, alpha, beta,
                         out_dtype, stream, nullptr);
+}
+
+int gemm_expert_dispatch(const gemm_expert_plan* plan, const void* ids, int64_t ld_ids, int ids_64bit, int64_t H,
+                         const void* X, int64_t ldx, int dtype, void* Xs, int64_t ldxs, void* stream) {
+  return gtn::run_expert_dispatch(plan, ids, ld_ids, ids_64bit, H, X, ldx, dtype, Xs, ldxs, stream);
+}
+
+int gemm_expert_dispatch_backward(const gemm_expert_plan* plan, int64_t H, const void* dXs, int64_t lddxs, int dtype,
+                                  void* dX, int64_t lddx, void* stream) {
+  return gtn::run_expert_combine(plan, H, dXs, lddxs, dtype, nullptr, 0, 0, false, dX, lddx, stream);
+}
+
+int gemm_expert_combine(const gemm_expert_plan* plan, int64_t H, const void* Y, int64_t ldy, int dtype,
+                        const void* weights, int64_t ldw, int weights_dtype, void* out, int64_t ldo, void* stream) {
+  return gtn::run_expert_combine(plan, H, Y, ldy, dtype, weights, ldw, weights_dtype, true, out, ldo, stream);
+}
+
+int gemm_expert_combine_backward(const gemm_expert_plan* plan, int64_t H, const void* Y, int64_t ldy, const void* dout,
+                                 int64_t lddo, int dtype, const void* weights, int64_t ldw, int weights_dtype, void* dY,
+                                 int64_t lddy, void* dweights, int64_t lddw, void* stream) {
+  return gtn::run_expert_combine_backward(plan, H, Y, ldy, dout, lddo, dtype, weights, ldw, weights_dtype, dY, lddy,
+                                          dweights, lddw, stream);
+}
+
+int gemm_w4_tn(int64_t M, const void* A, int64_t lda, const gemm_w4_matrix* W, void* D, int64_t ldd, float alpha,
+               int out_dtype, int activation, void* stream) {
+  return gtn::run_w4(M, nullptr, 0, A, lda, W, D, ldd, alpha, out_dtype, activation, stream);
+}
+
+int gemm_w4_tn_experts(const gemm_expert_plan* plan, const void* A, int64_t lda, int gather, const gemm_w4_matrix* W,
+                       void* D, int64_t ldd, float alpha, int out_dtype, int activation, void* stream) {
+  if (!plan) return gtn::fail(GEMM_ERR_INVALID_VALUE, "plan is NULL");
+  return gtn::run_w4(0, plan, gather, A, lda, W, D, ldd, alpha, out_dtype, activation, stream);
 }
 
 int gemm_plan(int64_t M, int64_t N, int64_t K, int fp8_inputs, int num_sms, const gemm_tn_config* cfg,

@@ -126,6 +126,75 @@ struct SkinnyParams {
   int* status;
 };
 
+// Mixture-of-experts rows (expert_rows.cu): tokens to expert order and back.
+constexpr int kExpertMax = 1024;          // experts
+constexpr int kExpertMaxSlots = 64;       // slots per token
+constexpr int kExpertSmallSlots = 2048;   // slots that one launch sorts and copies
+constexpr int kExpertMaxChunks = 128;     // chunks of slots of a larger sort
+
+struct ExpertParams {
+  int T, k, E;         // tokens, slots per token, experts
+  int n;               // T * k
+  long long H;         // elements per row
+  int* offsets;        // E + 1: first row of each expert
+  int* slot_row;       // n: row of each slot, -1 = dropped
+  int* row_token;      // n: token of each row, -1 past the last
+  const void* ids;     // dispatch: expert of each slot
+  int ids64;
+  long long ld_ids;
+  const void* weights; // combine: T x k, or nullptr for ones
+  int w_f32;
+  long long ld_w;
+  void* dweights;      // combine backward: T x k or nullptr
+  long long ld_dw;
+  const void* in; long long in_pitch;      // rows read (bytes): X, Y or dout
+  const void* in2; long long in2_pitch;    // combine backward: Y
+  void* out; long long out_pitch;          // rows written: Xs, out, dX or dY
+  int* hist;           // chunks x E
+  int chunks, chunk;   // chunks of a large sort, slots per chunk
+  int nch, tail;       // launch: chunks per row, elements after them
+  int lanes;           // launch: threads per token
+};
+
+struct LaunchInfo;
+// es: bytes per element (2 = bf16, 4 = fp32).  p.hist is needed where p.n > kExpertSmallSlots.
+int expert_chunks(long long n);
+cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info);
+cudaError_t launch_expert_combine(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info);
+cudaError_t launch_expert_combine_back(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info);
+
+// Products with 4-bit weights (gemm_w4.cu).
+constexpr int kW4TileRows = 128;          // weight rows per tile
+constexpr int kW4StageK = 256;            // k per ring stage: 128 bytes of codes per row
+
+struct W4Params {
+  int M, N, K;         // M: rows of A (dense) or sorted rows (experts)
+  int group, ngroups;  // k per scale, scales per row
+  const void* scales; long long ld_s, stride_s;    // elements
+  int s_f32;
+  const uint8_t* zeros; long long ld_z, stride_z;  // nullptr = 8 everywhere
+  const void* A; long long lda;                    // bf16
+  const int* a_rows;   // experts: row of A of each sorted row, or nullptr
+  int a_count;         // rows of A
+  const int* offsets;  // experts: E + 1, or nullptr
+  int E;
+  void* D; long long ldd;
+  int out_f32, act;
+  float alpha;
+  int split;           // k-parts per tile (cluster size): 1, 2, 4 or 8
+  int num_kb;          // ceil(K / kW4StageK)
+  int slab;            // launch: stages whose activations and scales are staged together
+  int stages;          // launch: ring stages
+  uint64_t timeout_ns;
+  int* status;
+};
+
+// k-parts per tile for `tiles` tiles of num_kb stages on `sms` SMs.
+int w4_split(long long tiles, int num_kb, int sms);
+// tm: codes as {byte of the row, row, matrix}, 128 x 128 x 1 boxes, 128-byte swizzle.
+// active: matrices that can have rows (1 for the dense form).
+cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, cudaStream_t stream, LaunchInfo* info);
+
 struct LaunchInfo {
   int path;            // 1 = 1-SM tiled, 2 = 2-SM tiled, 3 = skinny
   int grid, cluster, block;
