@@ -366,31 +366,44 @@ def gemm_w4_tn_experts(plan, A, lda, gather, W, D, ldd, alpha, out_dtype, activa
                                      stream or None)
 
 
+_torch = None
+_CODES = {}         # torch type -> gemm_out_dtype, filled with _torch
+
+
+def _t():
+    """The torch module, imported by the first wrapper that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _CODES.update({torch.bfloat16: OUT_BF16, torch.float32: OUT_F32})
+        _torch = torch
+    return _torch
+
+
 def _out_code(dtype, what):
-    import torch
-    if dtype == torch.bfloat16:
-        return OUT_BF16
-    if dtype == torch.float32:
-        return OUT_F32
-    raise ValueError(f"{what} must be torch.bfloat16 or torch.float32, not {dtype}")
+    _torch or _t()
+    code = _CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"{what} must be torch.bfloat16 or torch.float32, not {dtype}")
+    return code
 
 
 def _rows_of(t, rows, width, what):
     """Checks a (rows, width) CUDA matrix with unit column stride; returns its row stride."""
-    if t.dim() != 2 or not t.is_cuda or t.shape[0] != rows or (width is not None and t.shape[1] != width):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != rows or (width is not None and shape[1] != width) or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA matrix of {rows} x {'H' if width is None else width}, "
-                         f"not {tuple(t.shape)} on {t.device}")
-    ld, unit = t.stride()
-    if unit != 1 and t.shape[1] > 1 and t.shape[0] > 0:
+                         f"not {tuple(shape)} on {t.device}")
+    ld, wide = stride[0], shape[1]
+    if stride[1] != 1 and wide > 1 and rows > 0:
         raise ValueError(f"{what} must have unit column stride")
-    return max(ld, t.shape[1])
+    return ld if ld > wide else wide
 
 
-def _stream_of(t, stream):
-    if stream is not None:
-        return stream
-    import torch
-    return torch.cuda.current_stream(t.device).cuda_stream
+def _stream_of(t):
+    """The current stream of t's device, as an integer (torch.cuda.current_stream() makes an object first,
+    several microseconds that a decode step's calls would each wait for)."""
+    return _torch._C._cuda_getCurrentRawStream(t.get_device()) or None
 
 
 class ExpertPlan:
@@ -399,7 +412,7 @@ class ExpertPlan:
     A program keeps one per shape and fills it again at every step."""
 
     def __init__(self, tokens: int, slots: int, experts: int, device):
-        import torch
+        torch = _t()
         buf = torch.empty(experts + 1 + 2 * tokens * slots, dtype=torch.int32, device=device)
         n = tokens * slots
         self._set(buf[2 * n:], buf[:n].view(tokens, slots), buf[n:2 * n], experts)
@@ -412,7 +425,7 @@ class ExpertPlan:
         return plan
 
     def _set(self, offsets, slot_row, row_token, experts):
-        import torch
+        torch = _t()
         for name, t in (("offsets", offsets), ("slot_row", slot_row), ("row_token", row_token)):
             if t.dtype != torch.int32 or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous int32 tensor")
@@ -435,7 +448,7 @@ class W4Matrix:
     (q[n, k] - zeros[n, k // group])."""
 
     def __init__(self, codes, scales, zeros=None, K: int | None = None, group: int = 128):
-        import torch
+        torch = _t()
         K = 2 * codes.shape[-1] if K is None else K
         if codes.dtype != torch.uint8 or codes.dim() not in (2, 3) or not codes.is_cuda or codes.stride(-1) != 1:
             raise ValueError("codes must be a 2-D or 3-D uint8 CUDA tensor with unit stride along K")
@@ -460,22 +473,26 @@ def expert_dispatch(ids, plan: ExpertPlan, X=None, out=None, stream=None):
     """Fills `plan` from ids (tokens, slots), int32 or int64 with ids outside
     [0, experts) dropped, and returns X's rows in expert order (None without X):
     Xs[plan.slot_row[t, j]] = X[t], zeros past plan.offsets[experts]."""
-    import torch
+    torch = _torch or _t()
     wide = ids.dtype == torch.int64
     if not wide and ids.dtype != torch.int32:
         raise ValueError("ids must be int32 or int64")
     ld_ids = _rows_of(ids, plan.tokens, plan.slots, "ids")
-    H, x, ldx, o, ldo, code = 0, 0, 0, 0, 0, OUT_BF16
+    H, x, ldx, o, ldo, code = 0, None, 0, None, 0, OUT_BF16
     if X is not None:
         code, ldx = _out_code(X.dtype, "X"), _rows_of(X, plan.tokens, None, "X")
         H, x = X.shape[1], X.data_ptr()
         if out is None:
-            out = torch.empty((plan.rows, H), dtype=X.dtype, device=X.device)
-        if out.dtype != X.dtype:
-            raise ValueError("out must have X's type")
-        o, ldo = out.data_ptr(), _rows_of(out, plan.rows, H, "out")
-    _check(gemm_expert_dispatch(plan.info, ids.data_ptr(), ld_ids, int(wide), H, x, ldx, code, o, ldo,
-                                _stream_of(ids, stream)))
+            out, ldo = torch.empty((plan.rows, H), dtype=X.dtype, device=X.device), H
+        else:
+            if out.dtype != X.dtype:
+                raise ValueError("out must have X's type")
+            ldo = _rows_of(out, plan.rows, H, "out")
+        o = out.data_ptr()
+    rc = (_lib or load()).gemm_expert_dispatch(plan.info, ids.data_ptr(), ld_ids, wide, H, x, ldx, code, o, ldo,
+                                               _stream_of(ids) if stream is None else stream or None)
+    if rc:
+        _check(rc)
     return out if X is not None else None
 
 
@@ -490,27 +507,31 @@ def expert_combine(plan: ExpertPlan, Y, weights, out=None, stream=None):
 
 
 def _combine(plan, Y, weights, out, stream):
-    import torch
+    torch = _torch or _t()
     code, ldy = _out_code(Y.dtype, "rows"), _rows_of(Y, plan.rows, None, "rows")
     H = Y.shape[1]
+    if weights is not None:
+        wcode, ldw = _out_code(weights.dtype, "weights"), _rows_of(weights, plan.tokens, plan.slots, "weights")
     if out is None:
-        out = torch.empty((plan.tokens, H), dtype=Y.dtype, device=Y.device)
-    if out.dtype != Y.dtype:
-        raise ValueError("out must have the rows' type")
-    ldo = _rows_of(out, plan.tokens, H, "out")
-    s = _stream_of(Y, stream)
-    if weights is None:
-        _check(gemm_expert_dispatch_backward(plan.info, H, Y.data_ptr(), ldy, code, out.data_ptr(), ldo, s))
+        out, ldo = torch.empty((plan.tokens, H), dtype=Y.dtype, device=Y.device), H
     else:
-        ldw = _rows_of(weights, plan.tokens, plan.slots, "weights")
-        _check(gemm_expert_combine(plan.info, H, Y.data_ptr(), ldy, code, weights.data_ptr(), ldw,
-                                   _out_code(weights.dtype, "weights"), out.data_ptr(), ldo, s))
+        if out.dtype != Y.dtype:
+            raise ValueError("out must have the rows' type")
+        ldo = _rows_of(out, plan.tokens, H, "out")
+    lib, s = _lib or load(), _stream_of(Y) if stream is None else stream or None
+    if weights is None:
+        rc = lib.gemm_expert_dispatch_backward(plan.info, H, Y.data_ptr(), ldy, code, out.data_ptr(), ldo, s)
+    else:
+        rc = lib.gemm_expert_combine(plan.info, H, Y.data_ptr(), ldy, code, weights.data_ptr(), ldw, wcode,
+                                     out.data_ptr(), ldo, s)
+    if rc:
+        _check(rc)
     return out
 
 
 def expert_combine_backward(plan: ExpertPlan, Y, weights, dout, dY=None, dweights=None, stream=None):
     """Gradients of expert_combine: (dY, dweights), in Y's and weights' types."""
-    import torch
+    torch = _torch or _t()
     code, ldy = _out_code(Y.dtype, "Y"), _rows_of(Y, plan.rows, None, "Y")
     H = Y.shape[1]
     if dout.dtype != Y.dtype:
@@ -523,11 +544,12 @@ def expert_combine_backward(plan: ExpertPlan, Y, weights, dout, dY=None, dweight
         dweights = torch.empty((plan.tokens, plan.slots), dtype=weights.dtype, device=Y.device)
     if dY.dtype != Y.dtype or dweights.dtype != weights.dtype:
         raise ValueError("dY and dweights must have Y's and weights' types")
-    _check(gemm_expert_combine_backward(plan.info, H, Y.data_ptr(), ldy, dout.data_ptr(), lddo, code,
-                                        weights.data_ptr(), ldw, wcode, dY.data_ptr(),
-                                        _rows_of(dY, plan.rows, H, "dY"), dweights.data_ptr(),
-                                        _rows_of(dweights, plan.tokens, plan.slots, "dweights"),
-                                        _stream_of(Y, stream)))
+    rc = (_lib or load()).gemm_expert_combine_backward(
+        plan.info, H, Y.data_ptr(), ldy, dout.data_ptr(), lddo, code, weights.data_ptr(), ldw, wcode, dY.data_ptr(),
+        _rows_of(dY, plan.rows, H, "dY"), dweights.data_ptr(), _rows_of(dweights, plan.tokens, plan.slots, "dweights"),
+        _stream_of(Y) if stream is None else stream or None)
+    if rc:
+        _check(rc)
     return dY, dweights
 
 
@@ -544,21 +566,25 @@ def gemm_w4_experts(A, W: W4Matrix, plan: ExpertPlan, gather: bool = False, alph
 
 
 def _w4(plan, A, W, gather, alpha, activation, out_dtype, out, stream):
-    import torch
+    torch = _torch or _t()
     if A.dtype != torch.bfloat16:
         raise ValueError("A must be bf16")
     rows = A.shape[0] if plan is None else plan.tokens if gather else plan.rows
     lda = _rows_of(A, rows, W.K, "A")
     M = rows if plan is None else plan.rows
     if out is None:
-        out = torch.empty((M, W.N), dtype=out_dtype or torch.bfloat16, device=A.device)
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise ValueError("out must have out_dtype")
-    code, ldd = _out_code(out.dtype, "out"), _rows_of(out, M, W.N, "out")
-    s = _stream_of(A, stream)
-    if plan is None:
-        _check(gemm_w4_tn(M, A.data_ptr(), lda, W.info, out.data_ptr(), ldd, alpha, code, activation, s))
+        out, ldd = torch.empty((M, W.N), dtype=out_dtype or torch.bfloat16, device=A.device), W.N
     else:
-        _check(gemm_w4_tn_experts(plan.info, A.data_ptr(), lda, int(gather), W.info, out.data_ptr(), ldd, alpha,
-                                  code, activation, s))
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out must have out_dtype")
+        ldd = _rows_of(out, M, W.N, "out")
+    code = _out_code(out.dtype, "out")
+    lib, s = _lib or load(), _stream_of(A) if stream is None else stream or None
+    if plan is None:
+        rc = lib.gemm_w4_tn(M, A.data_ptr(), lda, W.info, out.data_ptr(), ldd, alpha, code, activation, s)
+    else:
+        rc = lib.gemm_w4_tn_experts(plan.info, A.data_ptr(), lda, gather, W.info, out.data_ptr(), ldd, alpha, code,
+                                    activation, s)
+    if rc:
+        _check(rc)
     return out

@@ -1014,11 +1014,12 @@ int run_w4(int64_t M, const gemm_expert_plan* plan, int gather, const void* A, i
   p.alpha = alpha;
   p.num_kb = (int)((W->K + kW4StageK - 1) / kW4StageK);
   const int active = plan ? (int)(p.E < M ? p.E : M) : 1;
-  p.split = w4_split((W->N + kW4TileRows - 1) / kW4TileRows * active, p.num_kb, st->sms);
+  const int64_t blocks = plan ? active : (M + 7) / 8;
+  if ((W->N + kW4TileRows - 1) / kW4TileRows * blocks >= kMaxDim) return fail(GEMM_ERR_INVALID_VALUE, "too many tiles");
   p.timeout_ns = timeout_ns(nullptr);
   p.status = st->status;
   LaunchInfo li = {};
-  return finish_launch(launch_w4(tm, p, active, static_cast<cudaStream_t>(stream_v), &li), li);
+  return finish_launch(launch_w4(tm, p, active, st->sms, static_cast<cudaStream_t>(stream_v), &li), li);
 }
 
 }  // namespace

@@ -181,19 +181,17 @@ struct W4Params {
   void* D; long long ldd;
   int out_f32, act;
   float alpha;
-  int split;           // k-parts per tile (cluster size): 1, 2, 4 or 8
+  int split;           // launch: k-parts per tile (cluster size), 1, 2, 4 or 8
   int num_kb;          // ceil(K / kW4StageK)
-  int slab;            // launch: stages whose activations and scales are staged together
-  int stages;          // launch: ring stages
   uint64_t timeout_ns;
   int* status;
 };
 
-// k-parts per tile for `tiles` tiles of num_kb stages on `sms` SMs.
-int w4_split(long long tiles, int num_kb, int sms);
+// k-parts per tile for `items` tiles of num_kb stages on `sms` SMs.
+int w4_split(long long items, int num_kb, int sms);
 // tm: codes as {byte of the row, row, matrix}, 128 x 128 x 1 boxes, 128-byte swizzle.
 // active: matrices that can have rows (1 for the dense form).
-cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, cudaStream_t stream, LaunchInfo* info);
+cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, int sms, cudaStream_t stream, LaunchInfo* info);
 
 struct LaunchInfo {
   int path;            // 1 = 1-SM tiled, 2 = 2-SM tiled, 3 = skinny
