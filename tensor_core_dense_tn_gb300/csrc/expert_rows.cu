@@ -277,21 +277,28 @@ __device__ __forceinline__ int load_row(const ExpertParams& p, int t, int j) {
   return r >= 0 && r < p.n ? r : -1;
 }
 
-// Copies token t's row to the rows r[0..count); U chunks per lane in flight.
+// Chunks c0, c0 + lanes, ... of token t's row.
 template <int CH, int U>
-__device__ __forceinline__ void copy_row(const ExpertParams& p, int t, const int* r, int count, int lane, int lanes) {
-  using R = typename Raw<CH>::T;
-  for (int c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += lanes * U * gridDim.y) {
-    R x[U];
+__device__ __forceinline__ void load_chunks(const ExpertParams& p, int t, int c0, int lanes, typename Raw<CH>::T (&x)[U]) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (c0 + u * lanes < p.nch) x[u] = ldc<CH>(p.in, p.in_pitch, t, c0 + u * lanes);
+  for (int u = 0; u < U; ++u)
+    if (c0 + u * lanes < p.nch) x[u] = ldc<CH>(p.in, p.in_pitch, t, c0 + u * lanes);
+}
+
+// Copies token t's row to the rows r[0..count), from the chunks in x on; U
+// chunks per lane in flight.
+template <int CH, int U>
+__device__ __forceinline__ void copy_row(const ExpertParams& p, int t, const int* r, int count, int lane, int lanes,
+                                         typename Raw<CH>::T (&x)[U]) {
+  const int step = lanes * U * gridDim.y;
+  for (int c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += step) {
     for (int j = 0; j < count; ++j) {
       if (r[j] < 0) continue;
 #pragma unroll
       for (int u = 0; u < U; ++u)
         if (c0 + u * lanes < p.nch) stc<CH>(p.out, p.out_pitch, r[j], c0 + u * lanes, x[u]);
     }
+    load_chunks<CH, U>(p, t, c0 + step, lanes, x);
   }
 }
 
@@ -314,24 +321,35 @@ __device__ __forceinline__ ExpertParams tail_of(ExpertParams p, int ch) {
   return p;
 }
 
+// The elements past the last whole chunk, where there are some.
+template <int ES>
+__device__ __forceinline__ void copy_tail(const ExpertParams& tail, int t, const int* r, int count, int lane, int lanes) {
+  typename Raw<ES>::T x[1];
+  load_chunks<ES, 1>(tail, t, lane + lanes * blockIdx.y, lanes, x);
+  copy_row<ES, 1>(tail, t, r, count, lane, lanes, x);
+}
+
 template <int ES, int CH, int U>
 __global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(ExpertParams p) {
   extern __shared__ int rows[];   // (threads / lanes) x k
-  griddep_wait();
-  griddep_launch_dependents();
   const int lanes = p.lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   const int per = kRowThreads / lanes;
-  const int t0 = blockIdx.x * per;
+  const int t0 = blockIdx.x * per, t = t0 + group;
+  // (Loading here takes 1.3 of 54 us off 8192 x 8 slots of 2048 bf16; asking
+  // for X in L2 while the slots are sorted gained nothing.)  The sort's kernels waited for whatever wrote X, so it is there before they end.
+  typename Raw<CH>::T x[U];
+  if (t < p.T) load_chunks<CH, U>(p, t, lane + lanes * U * blockIdx.y, lanes, x);
+  griddep_wait();
+  griddep_launch_dependents();
   for (int i = threadIdx.x; i < per * p.k; i += kRowThreads) {
     const int t = t0 + i / p.k;
     rows[i] = t < p.T ? load_row(p, t, i % p.k) : -1;
   }
   const int V = p.offsets[p.E];
   __syncthreads();
-  const int t = t0 + group;
   if (t >= p.T) return;
-  copy_row<CH, U>(p, t, rows + group * p.k, p.k, lane, lanes);
-  if (p.tail) copy_row<ES, 1>(tail_of<ES>(p, CH), t, rows + group * p.k, p.k, lane, lanes);
+  copy_row<CH, U>(p, t, rows + group * p.k, p.k, lane, lanes, x);
+  if (p.tail) copy_tail<ES>(tail_of<ES>(p, CH), t, rows + group * p.k, p.k, lane, lanes);
   for (long long r = V + t; r < p.n; r += p.T) {
     zero_row<CH>(p, r, lane, lanes);
     if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
@@ -345,13 +363,15 @@ __global__ void __launch_bounds__(kRowThreads) expert_dispatch_small_kernel(Expe
   extern __shared__ int sm[];
   const int lanes = p.lanes, group = threadIdx.x / lanes, lane = threadIdx.x % lanes;
   const int per = kRowThreads / lanes;
-  const int t0 = blockIdx.x * per;
+  const int t0 = blockIdx.x * per, t = t0 + group;
   int* ids = sm;               // n
   int* rows = sm + p.n;        // per * k
   __shared__ int filled;
   if (threadIdx.x == 0) filled = 0;
   griddep_wait();
   griddep_launch_dependents();
+  typename Raw<CH>::T x[U];
+  if (t < p.T) load_chunks<CH, U>(p, t, lane + lanes * U * blockIdx.y, lanes, x);
   __syncthreads();
   int mine = 0;
   for (int s = threadIdx.x; s < p.n; s += kRowThreads) {
@@ -389,10 +409,9 @@ __global__ void __launch_bounds__(kRowThreads) expert_dispatch_small_kernel(Expe
     for (int r = V + blockIdx.x * kRowThreads + threadIdx.x; r < p.n; r += gridDim.x * kRowThreads) p.row_token[r] = -1;
   }
   __syncthreads();
-  const int t = t0 + group;
   if (t >= p.T) return;
-  copy_row<CH, U>(p, t, rows + group * p.k, p.k, lane, lanes);
-  if (p.tail) copy_row<ES, 1>(tail_of<ES>(p, CH), t, rows + group * p.k, p.k, lane, lanes);
+  copy_row<CH, U>(p, t, rows + group * p.k, p.k, lane, lanes, x);
+  if (p.tail) copy_tail<ES>(tail_of<ES>(p, CH), t, rows + group * p.k, p.k, lane, lanes);
   if (p.nch + p.tail > 0)
     for (long long r = V + t; r < p.n; r += p.T) {
       zero_row<CH>(p, r, lane, lanes);
@@ -453,7 +472,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(ExpertParam
 
 // in = dout, in2 = Y, out = dY.  Adds the lane's part of <dout, Y_j> to dot[j].
 // Three rows move for each slot and none is read again: with loads and stores
-// marked so, 16384 x 4 rows of 4096 bf16 take 179 us (6.7 TB/s) against 202.
+// marked so, 16384 x 4 rows of 4096 bf16 take 180 us (6.7 TB/s) against 202.
 // The other kernels do not gain (combine loses 7%).
 template <int ES, int CH, int KU, int U>
 __device__ __forceinline__ void combine_back_row(const ExpertParams& p, int t, const int (&r)[KU], const float (&w)[KU],
@@ -605,7 +624,8 @@ int expert_chunks(long long n) {
 cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info) {
   const bool vec = row_aligned(p.in, p.in_pitch) && row_aligned(p.out, p.out_pitch);
   set_chunks(&p, es, vec);
-  const int U = vec ? 2 : 4;
+  // 8192 rows of 1001 bf16, one slot each: 24.3 / 23.6 / 18.8 us with U = 2 / 4 / 8.
+  const int U = vec ? 2 : 8;
   p.lanes = lanes_for(p.nch, U, 8);
   if (p.n <= kExpertSmallSlots) {
     if (p.lanes < 32) p.lanes = 32;    // counting rows is the work here: 8 tokens a block at most
@@ -613,8 +633,8 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
     dim3 grid = row_grid(p, U, sms);
     if (grid.x < 1) grid.x = 1;
     const size_t smem = ((size_t)p.n + (size_t)(kRowThreads / p.lanes) * p.k) * sizeof(int);
-    const void* f = !vec ? (es == 2 ? (const void*)expert_dispatch_small_kernel<2, 2, 4>
-                                    : (const void*)expert_dispatch_small_kernel<4, 4, 4>)
+    const void* f = !vec ? (es == 2 ? (const void*)expert_dispatch_small_kernel<2, 2, 8>
+                                    : (const void*)expert_dispatch_small_kernel<4, 4, 8>)
                          : (es == 2 ? (const void*)expert_dispatch_small_kernel<2, 16, 2>
                                     : (const void*)expert_dispatch_small_kernel<4, 16, 2>);
     *info = LaunchInfo{};
@@ -653,7 +673,7 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
   if (p.H == 0) return cudaSuccess;
   const dim3 grid = row_grid(p, U, sms);
   const size_t smem = (size_t)(kRowThreads / p.lanes) * p.k * sizeof(int);
-  const void* f = !vec ? (es == 2 ? (const void*)expert_gather_kernel<2, 2, 4> : (const void*)expert_gather_kernel<4, 4, 4>)
+  const void* f = !vec ? (es == 2 ? (const void*)expert_gather_kernel<2, 2, 8> : (const void*)expert_gather_kernel<4, 4, 8>)
                        : (es == 2 ? (const void*)expert_gather_kernel<2, 16, 2> : (const void*)expert_gather_kernel<4, 16, 2>);
   info->grid = grid.x * grid.y; info->block = kRowThreads; info->smem_bytes = (int)smem;
   info->kernel = "expert_gather_kernel";
@@ -662,16 +682,32 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
 
 namespace {
 
+// Chunks per lane in flight, for KU slots at once.  Measured in us, 8192
+// tokens (4096 for four slots), rows of 4096 bf16 in 16-byte chunks, rows of
+// 1001 elements one by one:
+//                    16-byte, U = 1 / 2 / 4     elements, U = 1 / 2 / 4 / 8
+//   combine, KU = 1   29.5 / 27.0 / 24.9         - / 20.8 / 23.6 / 12.5 (bf16)
+//            KU = 2   36.4 / 36.9 / 39.4         - / 24.6 / 27.3 / 28.3 (fp32)
+//            KU = 4   28.6 / 36.5 / -           44.2 / - / 52.5 / 52.6 (bf16)
+//   gradient KU = 1   35.7 / 33.3 / -             - / 33.3 / 25.1 / 20.6 (bf16)
+//            KU = 2   54.5 / 52.8 / -             - / 35.1 / 33.7 / 29.3 (fp32)
+//            KU = 4   46.9 / - / -              72.2 / - / 52.0 / 52.0 (bf16)
+// and with 2048 tokens of 8 slots, 1001 bf16 one by one: combine 27.9 / 22.2
+// with U = 1 / 2, gradient 36.3 / 30.8 with U = 2 / 4.  (KU = 2 with rows of 1000 bf16: 10.7 / 9.8 / 11.0, so U = 2.)
+constexpr int combine_chunks(int ku, bool vec) { return vec ? (ku >= 4 ? 1 : 4 / ku) : (ku == 4 ? 1 : (ku == 1 ? 8 : 2)); }
+constexpr int back_chunks(int ku, bool vec) { return vec ? (ku >= 4 ? 1 : 2) : (ku >= 4 ? 4 : 8); }
+
 template <int KU>
 const void* combine_fn(int es, bool vec) {
-  constexpr int U = KU >= 8 ? 1 : (KU >= 4 ? 2 : 4), US = KU >= 8 ? 2 : 4;
+  constexpr int U = combine_chunks(KU, true), US = combine_chunks(KU, false);
   if (vec) return es == 2 ? (const void*)expert_combine_kernel<2, 16, KU, U> : (const void*)expert_combine_kernel<4, 16, KU, U>;
   return es == 2 ? (const void*)expert_combine_kernel<2, 2, KU, US> : (const void*)expert_combine_kernel<4, 4, KU, US>;
 }
 template <int KU>
 const void* combine_back_fn(int es, bool vec) {
-  constexpr int U = KU >= 4 ? 1 : 2, US = KU >= 8 ? 2 : 4;
-  if (vec) return es == 2 ? (const void*)expert_combine_back_kernel<2, 16, KU, U> : (const void*)expert_combine_back_kernel<4, 16, KU, U>;
+  constexpr int U = back_chunks(KU, true), US = back_chunks(KU, false);
+  if (vec)
+    return es == 2 ? (const void*)expert_combine_back_kernel<2, 16, KU, U> : (const void*)expert_combine_back_kernel<4, 16, KU, U>;
   return es == 2 ? (const void*)expert_combine_back_kernel<2, 2, KU, US> : (const void*)expert_combine_back_kernel<4, 4, KU, US>;
 }
 int slots_unrolled(int k) { return k <= 1 ? 1 : (k <= 2 ? 2 : (k <= 4 ? 4 : 8)); }
@@ -682,7 +718,7 @@ cudaError_t launch_expert_combine(ExpertParams p, int es, int sms, cudaStream_t 
   const bool vec = row_aligned(p.in, p.in_pitch) && row_aligned(p.out, p.out_pitch);
   set_chunks(&p, es, vec);
   const int ku = slots_unrolled(p.k);
-  const int U = vec ? (ku >= 8 ? 1 : (ku >= 4 ? 2 : 4)) : (ku >= 8 ? 2 : 4);
+  const int U = combine_chunks(ku, vec);
   p.lanes = lanes_for(p.nch, U, 1);
   const dim3 grid = row_grid(p, U, sms);
   const void* f = ku == 1 ? combine_fn<1>(es, vec) : ku == 2 ? combine_fn<2>(es, vec) : ku == 4 ? combine_fn<4>(es, vec)
@@ -697,7 +733,7 @@ cudaError_t launch_expert_combine_back(ExpertParams p, int es, int sms, cudaStre
   const bool vec = row_aligned(p.in, p.in_pitch) && row_aligned(p.out, p.out_pitch) && row_aligned(p.in2, p.in2_pitch);
   set_chunks(&p, es, vec);
   const int ku = slots_unrolled(p.k);
-  const int U = vec ? (ku >= 4 ? 1 : 2) : (ku >= 8 ? 2 : 4);
+  const int U = back_chunks(ku, vec);
   p.lanes = lanes_for(p.nch, U, 32);
   const int per = kRowThreads / p.lanes;
   const dim3 grid((p.T + per - 1) / per);
