@@ -555,8 +555,8 @@ int gemm_expert_combine_backward(const gemm_expert_plan *plan, int64_t H, const 
  *           codes, ldc >= K and a multiple of 32; 16-byte aligned
  *   scales  bf16 (scales_dtype 0) or fp32 (1), ceil(K / group) per row, row
  *           stride lds
- *   zeros   unsigned bytes of 0..127 (the low seven bits count), row stride
- *           ldz, or NULL for a zero point of 8 everywhere
+ *   zeros   unsigned bytes, row stride ldz, or NULL for a zero point of 8
+ *           everywhere
  *   group   32, 64, 128 or a multiple of 256 (at least K: one scale a row)
  *   strides from one matrix to the next: stride_codes in codes (a multiple
  *           of 32, at least N * ldc), stride_scales and stride_zeros in

@@ -16,11 +16,29 @@
 // through registers, a slab of eight groups ahead.  Eight warps multiply: two
 // sets, each half of a stage's k, of four warps with 32 rows each.
 //
+// Measured (replayed in a graph, weights larger than L2 in rotation, against
+// the time of a copy of the same bytes):
+//    1 token  x 8192 x 8192,  groups of 128                    12.7 us   5.1
+//   16 tokens x 28672 x 4096, groups of 128, zero points       26.3 us   9.2
+//    5 tokens x 5000 x 2000,  groups of 32, fp32 result         8.6 us   0.9
+//    1 token through 8 of 64 experts of 4096 x 2048            13.1 us   5.1
+//   32 tokens, 2 of 16 experts of 8192 x 4096, groups of 64    66.7 us  42.9
+// What bounds it is the multiplying warps' instructions, not memory: with the
+// ring alone (nothing multiplied) the same calls take 8.8, 13.7, 6.4, 9.0 and
+// 48.5 us, with two stages instead of four they take as long as with four
+// (the last one 75.7), and with the weights in L2 they gain 1.5 us.  A stage
+// is about 3500 warp instructions, a stage of one warp (four steps) 1250
+// cycles where one CTA has the SM and 1650 where two do.  Removing the
+// unpacking or the mma alone gains 10%, both 45%.  Slower or equal: one CTA
+// per SM with 16 multiplying warps; three CTAs; 96-row tiles; ranges of equal
+// length across tiles joined in memory (24.3 us for 16 tokens, but 13.9 us
+// for one and 76.7 for 32); activations by bulk copies.
+//
 // mma.sync and not tcgen05.mma: the latter takes at least 27 ns whatever its
 // number of columns up to 64, so that 128 x 256 weights hold the tensor core
 // 0.44 us and more, and 16 KiB arrive every 0.37 us.  With the weights
 // unpacked into Tensor Memory as its A operand it was right and slower: 103
-// against 73 us for 32 tokens through 16 experts of 8192 x 4096.
+// us for the last of these calls.
 //
 // Fragments.  mma.m16n8k16 sums over k, so k may be permuted as long as both
 // operands agree.  A lane (row r = lane / 4, q = lane % 4) reads the word that
@@ -54,7 +72,6 @@ constexpr int kSets = 2;                            // halves of a stage's steps
 constexpr int kWarpSteps = kSteps / kSets;
 constexpr int kErrTimeout = -5;
 constexpr int kCtasPerSm = 2;
-constexpr int kPrefetch = 8;                        // boxes per CTA prefetched to L2 before the wait
 constexpr int kMaxSplit = 8;
 
 // Waits (bounded) for a phase; false if it gave up or another warp did.
@@ -453,25 +470,33 @@ __device__ __forceinline__ void w4_multiply(const W4Params& p, const W4Block& k,
       if (p.split > 1) cluster_sync();
       else named_bar_sync(1, 32 * kWarps);
       const int rows = kW4TileRows / p.split, shift = 31 - __clz(rows);
-      for (int i = tid; i < count * rows; i += 32 * kWarps) {
-        const int m = i >> shift, rr = part * rows + (i & (rows - 1)), n = w.n0 + rr;
-        float v = 0.0f;
+      constexpr int kMine = kTok * kW4TileRows / (32 * kWarps);
+      float v[kMine];
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        const int i = tid + x * 32 * kWarps, m = i >> shift, rr = part * rows + (i & (rows - 1));
+        v[x] = 0.0f;
+        if (m >= count) continue;
         if (p.split > 1) {
           const uint32_t at = smem_u32(k.red + m * kRedPitch + rr);
-          float x[kMaxSplit];
+          float y[kMaxSplit];
 #pragma unroll
-          for (int j = 0; j < kMaxSplit; ++j) x[j] = j < p.split ? ld_cluster_f32(mapa_shared(at, j)) : 0.0f;
+          for (int j = 0; j < kMaxSplit; ++j) y[j] = j < p.split ? ld_cluster_f32(mapa_shared(at, j)) : 0.0f;
 #pragma unroll
-          for (int j = 0; j < kMaxSplit; ++j) v += x[j];
+          for (int j = 0; j < kMaxSplit; ++j) v[x] += y[j];
         } else {
-          v = k.red[m * kRedPitch + rr];
+          v[x] = k.red[m * kRedPitch + rr];
         }
-        if (n < p.N) {
-          v = activate(p.alpha * (kUnit * v), p.act);
-          const long long d = (m0 + m) * p.ldd + n;
-          if (p.out_f32) static_cast<float*>(p.D)[d] = v;
-          else static_cast<uint16_t*>(p.D)[d] = (uint16_t)pack_bf16x2(v, 0.0f);
-        }
+        v[x] *= p.alpha * kUnit;
+      }
+      activate_chunk(v, p.act);
+#pragma unroll
+      for (int x = 0; x < kMine; ++x) {
+        const int i = tid + x * 32 * kWarps, m = i >> shift, n = w.n0 + part * rows + (i & (rows - 1));
+        if (m >= count || n >= p.N) continue;
+        const long long d = (long long)(m0 + m) * p.ldd + n;
+        if (p.out_f32) static_cast<float*>(p.D)[d] = v[x];
+        else static_cast<uint16_t*>(p.D)[d] = (uint16_t)pack_bf16x2(v[x], 0.0f);
       }
       if (p.split > 1) cluster_sync();   // the sums are read: no part leaves or writes again before
       else named_bar_sync(1, 32 * kWarps);
@@ -517,13 +542,6 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_w4_kernel(const __grid_const
     fence_mbar_init();
     abort_word = 0;
     if (p.num_kb > 0) tma_prefetch_desc(&tm);
-  }
-  // The dense form's codes start on their way to L2 during the previous
-  // kernel's tail.  A prefetch reads no value: what that kernel might still
-  // write there is seen by the loads after the wait.
-  if (tid == 0 && !p.offsets) {
-    const int tile = k.first / ((p.M + 8 * NT - 1) / (8 * NT));
-    for (int i = 0; i < min(kPrefetch, k.count_kb); ++i) tma_prefetch_l2_3d(&tm, (k.kb0 + i) * 128, tile * kW4TileRows, 0);
   }
   griddep_wait();
   griddep_launch_dependents();
@@ -579,8 +597,9 @@ cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, int sms, cu
   if (e != cudaSuccess) return e;
   if (dev < 64 && !configured[dev]) {
     for (int f = 1; f <= kSteps; f *= 2) {
-      if ((e = cudaFuncSetAttribute(kernel_for<1>(f), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_for(1, f) + list_bytes(kExpertMax)))) return e;
-      if ((e = cudaFuncSetAttribute(kernel_for<2>(f), cudaFuncAttributeMaxDynamicSharedMemorySize, smem_for(2, f) + list_bytes(kExpertMax)))) return e;
+      constexpr cudaFuncAttribute kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+      if ((e = cudaFuncSetAttribute(kernel_for<1>(f), kSmem, smem_for(1, f) + list_bytes(kExpertMax)))) return e;
+      if ((e = cudaFuncSetAttribute(kernel_for<2>(f), kSmem, smem_for(2, f) + list_bytes(kExpertMax)))) return e;
     }
     configured[dev] = true;
   }

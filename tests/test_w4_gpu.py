@@ -97,6 +97,24 @@ def test_dense(M, N, K, group, zeros, sdtype, out):
     assert torch.isnan(D[:, N:]).all()
 
 
+@pytest.mark.parametrize("M,N,K,group", [(3, 200, 1030, 32), (11, 130, 2000, 768), (2, 257, 700, 128), (16, 64, 900, 64)])
+@pytest.mark.parametrize("sdtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pad,skip", [(0, 0), (1, 1), (2, 3)])
+def test_every_zero_point_and_scales_at_odd_addresses(M, N, K, group, sdtype, pad, skip):
+    codes, scales, _ = (None if t is None else t[0] for t in make(1, N, K, group, False, sdtype, 7 + K))
+    groups = scales.shape[1]
+    flat_s = torch.full((skip + N * (groups + pad),), float("nan"), device="cuda", dtype=DT[sdtype])
+    flat_z = torch.full((skip + N * (groups + pad),), 255, device="cuda", dtype=torch.uint8)
+    odd_s = flat_s[skip:].view(N, groups + pad)[:, :groups]
+    odd_z = flat_z[skip:].view(N, groups + pad)[:, :groups]
+    odd_s.copy_(scales)
+    odd_z.copy_(torch.randint(0, 256, (N, groups), generator=gen(K), device="cuda", dtype=torch.uint8))
+    A = acts(M, K, 6)
+    D = g.gemm_w4(A, g.W4Matrix(codes, odd_s, odd_z, K=K, group=group), out_dtype=torch.float32)
+    status()
+    check(D, A, (codes, odd_s, odd_z), K, group)
+
+
 @pytest.mark.parametrize("act", [g.ACT_RELU, g.ACT_GELU, g.ACT_GELU_TANH, g.ACT_SILU])
 def test_activation_and_alpha(act):
     mat = make(1, 300, 512, 128, True, "bf16", 1)
