@@ -200,7 +200,8 @@ __global__ void __launch_bounds__(1024) expert_rank_kernel(ExpertParams p) {
 }
 
 // ---------------------------------------------------------------- rows
-// A chunk of CH bytes of a row (16 where every row allows it, else one element).
+// A chunk of CH bytes of a row: 16 where every row allows it, else 4 (one fp32
+// or two bf16 elements), else one bf16 element.
 template <int CH> struct Raw;
 template <> struct Raw<16> { using T = uint4; };
 template <> struct Raw<4> { using T = unsigned int; };
@@ -226,6 +227,9 @@ __device__ __forceinline__ void unpack(typename Raw<CH>::T v, float (&x)[CH / ES
     x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y); x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
   } else if constexpr (ES == 4) {
     x[0] = __uint_as_float(v);
+  } else if constexpr (CH == 4) {
+    x[0] = __uint_as_float(v << 16);
+    x[1] = __uint_as_float(v & 0xFFFF0000u);
   } else {
     x[0] = __uint_as_float((uint32_t)v << 16);
   }
@@ -240,6 +244,8 @@ __device__ __forceinline__ typename Raw<CH>::T pack(const float (&x)[CH / ES]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
   } else if constexpr (ES == 4) {
     return __float_as_uint(x[0]);
+  } else if constexpr (CH == 4) {
+    return pack_bf16x2(x[0], x[1]);
   } else {
     return (uint16_t)pack_bf16x2(x[0], 0.0f);
   }
@@ -336,7 +342,8 @@ __global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(ExpertParams
   const int per = kRowThreads / lanes;
   const int t0 = blockIdx.x * per, t = t0 + group;
   // (Loading here takes 1.3 of 54 us off 8192 x 8 slots of 2048 bf16; asking
-  // for X in L2 while the slots are sorted gained nothing.)  The sort's kernels waited for whatever wrote X, so it is there before they end.
+  // for X in L2 while the slots are sorted gained nothing.)  The sort's
+  // kernels waited for whatever wrote X, so it is there before they end.
   typename Raw<CH>::T x[U];
   if (t < p.T) load_chunks<CH, U>(p, t, lane + lanes * U * blockIdx.y, lanes, x);
   griddep_wait();
@@ -599,19 +606,24 @@ dim3 row_grid(const ExpertParams& p, int U, int sms) {
   return dim3((unsigned)gx, (unsigned)gy);
 }
 
-// Chunks of a row for this launch's alignment; false = element by element.
-void set_chunks(ExpertParams* p, int es, bool vec) {
-  if (vec) {
-    p->nch = (int)(p->H * es / 16);
-    p->tail = (int)(p->H - (long long)p->nch * 16 / es);
-  } else {
-    p->nch = (int)p->H;
-    p->tail = 0;
-  }
+// Bytes per chunk that these rows' addresses allow: 16, 4 or one element.
+int chunk_bytes(int es, const void* a, long long pitch_a, const void* b, long long pitch_b, const void* c = nullptr,
+                long long pitch_c = 0) {
+  const unsigned long long at = reinterpret_cast<uintptr_t>(a) | (unsigned long long)pitch_a | reinterpret_cast<uintptr_t>(b) |
+                                (b ? (unsigned long long)pitch_b : 0) | reinterpret_cast<uintptr_t>(c) |
+                                (c ? (unsigned long long)pitch_c : 0);
+  return at % 16 == 0 ? 16 : (at % 4 == 0 ? 4 : es);
 }
 
-bool row_aligned(const void* base, long long pitch) {
-  return !base || ((reinterpret_cast<uintptr_t>(base) & 15u) == 0 && pitch % 16 == 0);
+void set_chunks(ExpertParams* p, int es, int ch) {
+  p->nch = (int)(p->H * es / ch);
+  p->tail = (int)(p->H - (long long)p->nch * ch / es);
+}
+
+template <template <int, int> class Pick>
+const void* kernel_of(int es, int ch) {
+  if (es == 4) return ch == 16 ? Pick<4, 16>::get() : Pick<4, 4>::get();
+  return ch == 16 ? Pick<2, 16>::get() : (ch == 4 ? Pick<2, 4>::get() : Pick<2, 2>::get());
 }
 
 }  // namespace
@@ -621,11 +633,24 @@ int expert_chunks(long long n) {
   return (int)(c < 1 ? 1 : (c > kExpertMaxChunks ? kExpertMaxChunks : c));
 }
 
+namespace {
+
+// 8192 rows of 1002 bf16, one slot each: 15.2 / 12.6 us with 4 / 8 chunks of 4
+// bytes; of 1001, 24.3 / 23.6 / 18.8 us with 2 / 4 / 8 elements.
+constexpr int gather_chunks(int ch) { return ch == 16 ? 2 : 8; }
+template <int ES, int CH> struct SmallDispatch {
+  static const void* get() { return (const void*)expert_dispatch_small_kernel<ES, CH, gather_chunks(CH)>; }
+};
+template <int ES, int CH> struct Gather {
+  static const void* get() { return (const void*)expert_gather_kernel<ES, CH, gather_chunks(CH)>; }
+};
+
+}  // namespace
+
 cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info) {
-  const bool vec = row_aligned(p.in, p.in_pitch) && row_aligned(p.out, p.out_pitch);
-  set_chunks(&p, es, vec);
-  // 8192 rows of 1001 bf16, one slot each: 24.3 / 23.6 / 18.8 us with U = 2 / 4 / 8.
-  const int U = vec ? 2 : 8;
+  const int ch = chunk_bytes(es, p.in, p.in_pitch, p.out, p.out_pitch);
+  set_chunks(&p, es, ch);
+  const int U = gather_chunks(ch);
   p.lanes = lanes_for(p.nch, U, 8);
   if (p.n <= kExpertSmallSlots) {
     if (p.lanes < 32) p.lanes = 32;    // counting rows is the work here: 8 tokens a block at most
@@ -633,10 +658,7 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
     dim3 grid = row_grid(p, U, sms);
     if (grid.x < 1) grid.x = 1;
     const size_t smem = ((size_t)p.n + (size_t)(kRowThreads / p.lanes) * p.k) * sizeof(int);
-    const void* f = !vec ? (es == 2 ? (const void*)expert_dispatch_small_kernel<2, 2, 8>
-                                    : (const void*)expert_dispatch_small_kernel<4, 4, 8>)
-                         : (es == 2 ? (const void*)expert_dispatch_small_kernel<2, 16, 2>
-                                    : (const void*)expert_dispatch_small_kernel<4, 16, 2>);
+    const void* f = kernel_of<SmallDispatch>(es, ch);
     *info = LaunchInfo{};
     info->grid = grid.x * grid.y; info->cluster = 1; info->block = kRowThreads; info->smem_bytes = (int)smem;
     info->kernel = "expert_dispatch_small_kernel";
@@ -673,8 +695,7 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
   if (p.H == 0) return cudaSuccess;
   const dim3 grid = row_grid(p, U, sms);
   const size_t smem = (size_t)(kRowThreads / p.lanes) * p.k * sizeof(int);
-  const void* f = !vec ? (es == 2 ? (const void*)expert_gather_kernel<2, 2, 8> : (const void*)expert_gather_kernel<4, 4, 8>)
-                       : (es == 2 ? (const void*)expert_gather_kernel<2, 16, 2> : (const void*)expert_gather_kernel<4, 16, 2>);
+  const void* f = kernel_of<Gather>(es, ch);
   info->grid = grid.x * grid.y; info->block = kRowThreads; info->smem_bytes = (int)smem;
   info->kernel = "expert_gather_kernel";
   return launch(f, grid, kRowThreads, smem, stream, p);
@@ -682,47 +703,47 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
 
 namespace {
 
-// Chunks per lane in flight, for KU slots at once.  Measured in us, 8192
-// tokens (4096 for four slots), rows of 4096 bf16 in 16-byte chunks, rows of
-// 1001 elements one by one:
-//                    16-byte, U = 1 / 2 / 4     elements, U = 1 / 2 / 4 / 8
-//   combine, KU = 1   29.5 / 27.0 / 24.9         - / 20.8 / 23.6 / 12.5 (bf16)
-//            KU = 2   36.4 / 36.9 / 39.4         - / 24.6 / 27.3 / 28.3 (fp32)
-//            KU = 4   28.6 / 36.5 / -           44.2 / - / 52.5 / 52.6 (bf16)
-//   gradient KU = 1   35.7 / 33.3 / -             - / 33.3 / 25.1 / 20.6 (bf16)
-//            KU = 2   54.5 / 52.8 / -             - / 35.1 / 33.7 / 29.3 (fp32)
-//            KU = 4   46.9 / - / -              72.2 / - / 52.0 / 52.0 (bf16)
-// and with 2048 tokens of 8 slots, 1001 bf16 one by one: combine 27.9 / 22.2
-// with U = 1 / 2, gradient 36.3 / 30.8 with U = 2 / 4.  (KU = 2 with rows of 1000 bf16: 10.7 / 9.8 / 11.0, so U = 2.)
-constexpr int combine_chunks(int ku, bool vec) { return vec ? (ku >= 4 ? 1 : 4 / ku) : (ku == 4 ? 1 : (ku == 1 ? 8 : 2)); }
-constexpr int back_chunks(int ku, bool vec) { return vec ? (ku >= 4 ? 1 : 2) : (ku >= 4 ? 4 : 8); }
+// Chunks per lane in flight, for KU slots at once.  Measured in us with rows
+// of 4096 bf16 in 16-byte chunks and rows of 1002 bf16 in 4-byte ones, 8192
+// tokens of one and two slots, 4096 of four, 2048 of eight:
+//                    16-byte, U = 1 / 2 / 4     4-byte, U = 1 / 2 / 4 / 8
+//   combine, KU = 1   29.5 / 27.0 / 24.9         - / - / 9.5 / 6.6
+//            KU = 2   36.4 / 36.9 / 39.4         - / 17.2 / 13.2 / -
+//            KU = 4   28.6 / 36.5 / -           15.1 / 11.4 / - / -
+//            KU = 8   26.0 / - / -              11.9 / 10.3 / - / -
+//   gradient KU = 1   35.7 / 33.3 / -            - / - / 13.3 / 12.3
+//            KU = 2   54.5 / 52.8 / -            - / - / 18.3 / 16.0
+//            KU = 4   46.9 / - / -               - / 18.9 / 15.3 / -
+//            KU = 8   47.3 / - / -               - / 22.7 / 18.1 / -
+// (KU = 2 with rows of 1000 bf16: 10.7 / 9.8 / 11.0, so U = 2.  With rows of 1001
+// bf16, one element at a time, these calls take 12.2, 30.4, 22.3 and 22.3 us
+// and for the gradient 20.7, 27.4, 26.7 and 30.9.)
+constexpr int combine_chunks(int ku, int ch) { return ch == 16 ? (ku >= 4 ? 1 : 4 / ku) : (ku >= 4 ? 2 : 8 / ku); }
+constexpr int back_chunks(int ku, int ch) { return ch == 16 ? (ku >= 4 ? 1 : 2) : (ku >= 4 ? 4 : 8); }
 
-template <int KU>
-const void* combine_fn(int es, bool vec) {
-  constexpr int U = combine_chunks(KU, true), US = combine_chunks(KU, false);
-  if (vec) return es == 2 ? (const void*)expert_combine_kernel<2, 16, KU, U> : (const void*)expert_combine_kernel<4, 16, KU, U>;
-  return es == 2 ? (const void*)expert_combine_kernel<2, 2, KU, US> : (const void*)expert_combine_kernel<4, 4, KU, US>;
-}
-template <int KU>
-const void* combine_back_fn(int es, bool vec) {
-  constexpr int U = back_chunks(KU, true), US = back_chunks(KU, false);
-  if (vec)
-    return es == 2 ? (const void*)expert_combine_back_kernel<2, 16, KU, U> : (const void*)expert_combine_back_kernel<4, 16, KU, U>;
-  return es == 2 ? (const void*)expert_combine_back_kernel<2, 2, KU, US> : (const void*)expert_combine_back_kernel<4, 4, KU, US>;
-}
+template <int KU> struct ForSlots {
+  template <int ES, int CH> struct Combine {
+    static const void* get() { return (const void*)expert_combine_kernel<ES, CH, KU, combine_chunks(KU, CH)>; }
+  };
+  template <int ES, int CH> struct Back {
+    static const void* get() { return (const void*)expert_combine_back_kernel<ES, CH, KU, back_chunks(KU, CH)>; }
+  };
+};
 int slots_unrolled(int k) { return k <= 1 ? 1 : (k <= 2 ? 2 : (k <= 4 ? 4 : 8)); }
 
 }  // namespace
 
 cudaError_t launch_expert_combine(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info) {
-  const bool vec = row_aligned(p.in, p.in_pitch) && row_aligned(p.out, p.out_pitch);
-  set_chunks(&p, es, vec);
+  const int ch = chunk_bytes(es, p.in, p.in_pitch, p.out, p.out_pitch);
+  set_chunks(&p, es, ch);
   const int ku = slots_unrolled(p.k);
-  const int U = combine_chunks(ku, vec);
+  const int U = combine_chunks(ku, ch);
   p.lanes = lanes_for(p.nch, U, 1);
   const dim3 grid = row_grid(p, U, sms);
-  const void* f = ku == 1 ? combine_fn<1>(es, vec) : ku == 2 ? combine_fn<2>(es, vec) : ku == 4 ? combine_fn<4>(es, vec)
-                                                                                                 : combine_fn<8>(es, vec);
+  const void* f = ku == 1   ? kernel_of<ForSlots<1>::Combine>(es, ch)
+                  : ku == 2 ? kernel_of<ForSlots<2>::Combine>(es, ch)
+                  : ku == 4 ? kernel_of<ForSlots<4>::Combine>(es, ch)
+                            : kernel_of<ForSlots<8>::Combine>(es, ch);
   *info = LaunchInfo{};
   info->grid = grid.x * grid.y; info->cluster = 1; info->block = kRowThreads;
   info->kernel = "expert_combine_kernel";
@@ -730,15 +751,17 @@ cudaError_t launch_expert_combine(ExpertParams p, int es, int sms, cudaStream_t 
 }
 
 cudaError_t launch_expert_combine_back(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info) {
-  const bool vec = row_aligned(p.in, p.in_pitch) && row_aligned(p.out, p.out_pitch) && row_aligned(p.in2, p.in2_pitch);
-  set_chunks(&p, es, vec);
+  const int ch = chunk_bytes(es, p.in, p.in_pitch, p.out, p.out_pitch, p.in2, p.in2_pitch);
+  set_chunks(&p, es, ch);
   const int ku = slots_unrolled(p.k);
-  const int U = back_chunks(ku, vec);
+  const int U = back_chunks(ku, ch);
   p.lanes = lanes_for(p.nch, U, 32);
   const int per = kRowThreads / p.lanes;
   const dim3 grid((p.T + per - 1) / per);
-  const void* f = ku == 1 ? combine_back_fn<1>(es, vec) : ku == 2 ? combine_back_fn<2>(es, vec)
-                  : ku == 4 ? combine_back_fn<4>(es, vec) : combine_back_fn<8>(es, vec);
+  const void* f = ku == 1   ? kernel_of<ForSlots<1>::Back>(es, ch)
+                  : ku == 2 ? kernel_of<ForSlots<2>::Back>(es, ch)
+                  : ku == 4 ? kernel_of<ForSlots<4>::Back>(es, ch)
+                            : kernel_of<ForSlots<8>::Back>(es, ch);
   *info = LaunchInfo{};
   info->grid = grid.x; info->cluster = 1; info->block = kRowThreads;
   info->kernel = "expert_combine_back_kernel";

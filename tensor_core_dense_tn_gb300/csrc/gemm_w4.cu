@@ -18,21 +18,21 @@
 //
 // Measured (replayed in a graph, weights larger than L2 in rotation, against
 // the time of a copy of the same bytes):
-//    1 token  x 8192 x 8192,  groups of 128                    12.7 us   5.1
-//   16 tokens x 28672 x 4096, groups of 128, zero points       26.3 us   9.2
-//    5 tokens x 5000 x 2000,  groups of 32, fp32 result         8.6 us   0.9
-//    1 token through 8 of 64 experts of 4096 x 2048            13.1 us   5.1
-//   32 tokens, 2 of 16 experts of 8192 x 4096, groups of 64    66.7 us  42.9
+//    1 token  x 8192 x 8192,  groups of 128                    12.5 us   5.1
+//   16 tokens x 28672 x 4096, groups of 128, zero points       27.4 us   9.2
+//    5 tokens x 5000 x 2000,  groups of 32, fp32 result         8.5 us   0.9
+//    1 token through 8 of 64 experts of 4096 x 2048            12.8 us   5.1
+//   32 tokens, 2 of 16 experts of 8192 x 4096, groups of 64    64.3 us  42.9
 // What bounds it is the multiplying warps' instructions, not memory: with the
 // ring alone (nothing multiplied) the same calls take 8.8, 13.7, 6.4, 9.0 and
-// 48.5 us, with two stages instead of four they take as long as with four
-// (the last one 75.7), and with the weights in L2 they gain 1.5 us.  A stage
-// is about 3500 warp instructions, a stage of one warp (four steps) 1250
-// cycles where one CTA has the SM and 1650 where two do.  Removing the
-// unpacking or the mma alone gains 10%, both 45%.  Slower or equal: one CTA
-// per SM with 16 multiplying warps; three CTAs; 96-row tiles; ranges of equal
-// length across tiles joined in memory (24.3 us for 16 tokens, but 13.9 us
-// for one and 76.7 for 32); activations by bulk copies.
+// 48.5 us, with two stages instead of three or four the first four take no
+// longer, and with the weights in L2 they gain 1.5 us.  A stage is about 3500
+// warp instructions; its four steps take a warp 1250 cycles where one CTA has
+// the SM and 1650 where two do.  Removing the unpacking or the mma alone gains
+// 10%, both 45%.  Slower or equal: one CTA per SM with 16 multiplying warps;
+// three CTAs; 96-row tiles; ranges of equal length across tiles, joined in
+// memory (24.3 us for 16 tokens, but 13.9 us for one and 76.7 for 32);
+// activations by bulk copies; a first copy of codes before the scales' loads.
 //
 // mma.sync and not tcgen05.mma: the latter takes at least 27 ns whatever its
 // number of columns up to 64, so that 128 x 256 weights hold the tensor core
@@ -241,7 +241,7 @@ struct RawScales {           // eight groups' scales and zero points of a row, a
 
 // The copying half: keeps the ring ahead of the multiplying warps, across
 // items.
-template <int NT, int FL, bool S_F32>
+template <int NT, int FL, bool SPLIT, bool S_F32>
 __device__ __forceinline__ void w4_copy(const CUtensorMap* tm, const W4Params& p, const W4Block& k) {
   constexpr int kTok = 8 * NT, kFlushes = kSteps / FL, kStages = ring_stages(NT, FL);
   constexpr int kSlab = FL == kSteps ? 1 : FL;            // stages whose scales are loaded together
@@ -348,7 +348,7 @@ __device__ __forceinline__ void w4_copy(const CUtensorMap* tm, const W4Params& p
           }
         }
       }
-      if (p.split > 1) {   // a cluster's barrier counts every thread: these two are the multiplying warps'
+      if constexpr (SPLIT) {   // a cluster's barrier counts every thread: these two are the multiplying warps'
         cluster_sync();
         cluster_sync();
       }
@@ -369,7 +369,7 @@ __device__ __forceinline__ void w4_copy(const CUtensorMap* tm, const W4Params& p
 }
 
 // The multiplying half.
-template <int NT, int FL>
+template <int NT, int FL, bool SPLIT>
 __device__ __forceinline__ void w4_multiply(const W4Params& p, const W4Block& k, int part) {
   constexpr int kTok = 8 * NT, kFlushes = kSteps / FL, kStages = ring_stages(NT, FL);
   constexpr int kSeg = FL < kWarpSteps ? FL : kWarpSteps;   // steps of one scale
@@ -412,7 +412,17 @@ __device__ __forceinline__ void w4_multiply(const W4Params& p, const W4Block& k,
 #pragma unroll
           for (int j = 0; j < 4; ++j) sz[j] = sc[f * kW4TileRows + 8 * j];
           float acc[2][NT][4];
+          // two tiles of tokens: all four steps at once spill registers (28.4 against 27.4 us)
+          constexpr int kUnroll = NT == 2 && kSeg > 2 ? 2 : kSeg;
+          if constexpr (kUnroll < kSeg) {
 #pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+              for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[s][t][j] = 0.0f;
+          }
+#pragma unroll (kUnroll)
           for (int h = 0; h < kSeg; ++h) {
             const int step = f * kSeg + h;
             // 128-byte swizzle: the 16-byte column c of row r sits at c ^ (r % 8)
@@ -432,7 +442,7 @@ __device__ __forceinline__ void w4_multiply(const W4Params& p, const W4Block& k,
               const uint32_t a0[4] = {da[0], db[0], da[1], db[1]}, a1[4] = {da[2], db[2], da[3], db[3]};
 #pragma unroll
               for (int t = 0; t < NT; ++t) {
-                if (h == 0) mma_16816_first(acc[s][t], a0, b[t].x, b[t].y);
+                if (kUnroll == kSeg && h == 0) mma_16816_first(acc[s][t], a0, b[t].x, b[t].y);
                 else mma_16816(acc[s][t], a0, b[t].x, b[t].y);
                 mma_16816(acc[s][t], a1, b[t].z, b[t].w);
               }
@@ -454,8 +464,8 @@ __device__ __forceinline__ void w4_multiply(const W4Params& p, const W4Block& k,
         }
       }
       // The second set's sums go through shared memory to the first, whose
-      // warps hold the same rows; then, with several parts, part j finishes rows
-      // [128 j / split, 128 (j + 1) / split), adding the parts in order.
+      // warps hold the same rows; then, with several parts, each finishes its
+      // share of the tile's elements, adding the parts in order.
       auto each = [&](auto f) {
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -467,38 +477,32 @@ __device__ __forceinline__ void w4_multiply(const W4Params& p, const W4Block& k,
       if (set == 1) each([](float& at, float v) { at = v; });
       named_bar_sync(1, 32 * kWarps);
       if (set == 0) each([](float& at, float v) { at += v; });
-      if (p.split > 1) cluster_sync();
+      if constexpr (SPLIT) cluster_sync();
       else named_bar_sync(1, 32 * kWarps);
-      const int rows = kW4TileRows / p.split, shift = 31 - __clz(rows);
-      constexpr int kMine = kTok * kW4TileRows / (32 * kWarps);
-      float v[kMine];
-#pragma unroll
-      for (int x = 0; x < kMine; ++x) {
-        const int i = tid + x * 32 * kWarps, m = i >> shift, rr = part * rows + (i & (rows - 1));
-        v[x] = 0.0f;
-        if (m >= count) continue;
-        if (p.split > 1) {
+      auto store = [&](int m, int rr, float v) {
+        const long long d = (long long)(m0 + m) * p.ldd + w.n0 + rr;
+        if (p.out_f32) static_cast<float*>(p.D)[d] = v;
+        else static_cast<uint16_t*>(p.D)[d] = (uint16_t)pack_bf16x2(v, 0.0f);
+      };
+      if constexpr (SPLIT) {
+        const int total = count * kW4TileRows, share = (total + p.split - 1) / p.split, end = min(total, (part + 1) * share);
+        for (int i = part * share + tid; i < end; i += 32 * kWarps) {
+          const int m = i / kW4TileRows, rr = i % kW4TileRows;
           const uint32_t at = smem_u32(k.red + m * kRedPitch + rr);
-          float y[kMaxSplit];
+          float y[kMaxSplit], v = 0.0f;
 #pragma unroll
           for (int j = 0; j < kMaxSplit; ++j) y[j] = j < p.split ? ld_cluster_f32(mapa_shared(at, j)) : 0.0f;
 #pragma unroll
-          for (int j = 0; j < kMaxSplit; ++j) v[x] += y[j];
-        } else {
-          v[x] = k.red[m * kRedPitch + rr];
+          for (int j = 0; j < kMaxSplit; ++j) v += y[j];
+          if (w.n0 + rr < p.N) store(m, rr, activate(p.alpha * (kUnit * v), p.act));
         }
-        v[x] *= p.alpha * kUnit;
+      } else {
+        for (int i = tid; i < count * kW4TileRows; i += 32 * kWarps) {
+          const int m = i / kW4TileRows, rr = i % kW4TileRows;
+          if (w.n0 + rr < p.N) store(m, rr, activate(p.alpha * (kUnit * k.red[m * kRedPitch + rr]), p.act));
+        }
       }
-      activate_chunk(v, p.act);
-#pragma unroll
-      for (int x = 0; x < kMine; ++x) {
-        const int i = tid + x * 32 * kWarps, m = i >> shift, n = w.n0 + part * rows + (i & (rows - 1));
-        if (m >= count || n >= p.N) continue;
-        const long long d = (long long)(m0 + m) * p.ldd + n;
-        if (p.out_f32) static_cast<float*>(p.D)[d] = v[x];
-        else static_cast<uint16_t*>(p.D)[d] = (uint16_t)pack_bf16x2(v[x], 0.0f);
-      }
-      if (p.split > 1) cluster_sync();   // the sums are read: no part leaves or writes again before
+      if constexpr (SPLIT) cluster_sync();   // the sums are read: no part leaves or writes again before
       else named_bar_sync(1, 32 * kWarps);
     }
   }
@@ -506,7 +510,9 @@ __device__ __forceinline__ void w4_multiply(const W4Params& p, const W4Block& k,
 }
 
 // NT: token tiles of 8.  FL: steps of 32 k per scale group (8 = whole stage).
-template <int NT, int FL>
+// SPLIT: a tile's k has several parts (apart, because the registers that this
+// takes slow the other form: 72 against 64 us for 32 tokens through experts).
+template <int NT, int FL, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 2) gemm_w4_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ W4Params p) {
   extern __shared__ unsigned char smem_raw[];
   constexpr int kStages = ring_stages(NT, FL);
@@ -528,12 +534,12 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_w4_kernel(const __grid_const
   k.abort_flag = &abort_word;
 
   const int tid = threadIdx.x;
-  const int part = (int)(blockIdx.x % p.split);
+  const int split = SPLIT ? p.split : 1, part = (int)(blockIdx.x % split);
   k.tiles = (p.N + kW4TileRows - 1) / kW4TileRows;
-  k.first = (int)(blockIdx.x / p.split);
-  k.step = (int)(gridDim.x / p.split);
-  k.kb0 = (int)((long long)part * p.num_kb / p.split);
-  k.count_kb = (int)((long long)(part + 1) * p.num_kb / p.split) - k.kb0;
+  k.first = (int)(blockIdx.x / split);
+  k.step = (int)(gridDim.x / split);
+  k.kb0 = (int)((long long)part * p.num_kb / split);
+  k.count_kb = (int)((long long)(part + 1) * p.num_kb / split) - k.kb0;
   if (tid == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(k.full + 8 * s, 1 + kAuxThreads + kAuxThreads / 32);
@@ -565,25 +571,36 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_w4_kernel(const __grid_const
   k.items = k.tiles * k.active;
 
   if (tid >= 32 * kWarps) {
-    if (p.s_f32) w4_copy<NT, FL, true>(&tm, p, k);
-    else w4_copy<NT, FL, false>(&tm, p, k);
+    if (p.s_f32) w4_copy<NT, FL, SPLIT, true>(&tm, p, k);
+    else w4_copy<NT, FL, SPLIT, false>(&tm, p, k);
   } else {
-    w4_multiply<NT, FL>(p, k, part);
+    w4_multiply<NT, FL, SPLIT>(p, k, part);
   }
 }
 
-template <int NT>
-const void* kernel_for(int fl) {
-  return fl == 1 ? (const void*)gemm_w4_kernel<NT, 1> : fl == 2 ? (const void*)gemm_w4_kernel<NT, 2>
-         : fl == 4 ? (const void*)gemm_w4_kernel<NT, 4> : (const void*)gemm_w4_kernel<NT, 8>;
+const void* kernel_for(int nt, int fl, bool split) {
+  static const void* const table[2][4][2] = {
+      {{(const void*)gemm_w4_kernel<1, 1, false>, (const void*)gemm_w4_kernel<1, 1, true>},
+       {(const void*)gemm_w4_kernel<1, 2, false>, (const void*)gemm_w4_kernel<1, 2, true>},
+       {(const void*)gemm_w4_kernel<1, 4, false>, (const void*)gemm_w4_kernel<1, 4, true>},
+       {(const void*)gemm_w4_kernel<1, 8, false>, (const void*)gemm_w4_kernel<1, 8, true>}},
+      {{(const void*)gemm_w4_kernel<2, 1, false>, (const void*)gemm_w4_kernel<2, 1, true>},
+       {(const void*)gemm_w4_kernel<2, 2, false>, (const void*)gemm_w4_kernel<2, 2, true>},
+       {(const void*)gemm_w4_kernel<2, 4, false>, (const void*)gemm_w4_kernel<2, 4, true>},
+       {(const void*)gemm_w4_kernel<2, 8, false>, (const void*)gemm_w4_kernel<2, 8, true>}}};
+  return table[nt - 1][fl == 1 ? 0 : fl == 2 ? 1 : fl == 4 ? 2 : 3][split];
 }
 
 }  // namespace
 
+// The smallest number of parts for which the longest is shortest, as long as
+// all of them run at once.  (1 token x 10157 x 7866, 80 tiles of 31 stages: three
+// parts take 20.1 us, two 25.5.)
 int w4_split(long long items, int num_kb, int sms) {
-  int s = 1;
-  while (s < kMaxSplit && s * 2 <= num_kb && items * s * 2 <= kCtasPerSm * sms) s *= 2;
-  return s;
+  int best = 1;
+  for (int s = 2; s <= kMaxSplit && s <= num_kb && items * s <= kCtasPerSm * sms; ++s)
+    if ((num_kb + s - 1) / s < (num_kb + best - 1) / best) best = s;
+  return best;
 }
 
 cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, int sms, cudaStream_t stream, LaunchInfo* info) {
@@ -596,10 +613,11 @@ cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, int sms, cu
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !configured[dev]) {
-    for (int f = 1; f <= kSteps; f *= 2) {
-      constexpr cudaFuncAttribute kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
-      if ((e = cudaFuncSetAttribute(kernel_for<1>(f), kSmem, smem_for(1, f) + list_bytes(kExpertMax)))) return e;
-      if ((e = cudaFuncSetAttribute(kernel_for<2>(f), kSmem, smem_for(2, f) + list_bytes(kExpertMax)))) return e;
+    for (int i = 0; i < 16; ++i) {
+      const int n = 1 + i / 8, f = 1 << (i / 2 % 4);
+      if ((e = cudaFuncSetAttribute(kernel_for(n, f, i % 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    smem_for(n, f) + list_bytes(kExpertMax))))
+        return e;
     }
     configured[dev] = true;
   }
@@ -633,7 +651,7 @@ cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, int sms, cu
   info->k_parts = p.split;
   info->kernel = p.offsets ? "gemm_w4_kernel<experts>" : "gemm_w4_kernel";
   void* args[2] = {const_cast<CUtensorMap*>(&tm), &p};
-  return cudaLaunchKernelExC(&cfg, nt == 2 ? kernel_for<2>(fl) : kernel_for<1>(fl), args);
+  return cudaLaunchKernelExC(&cfg, kernel_for(nt, fl, p.split > 1), args);
 }
 
 }  // namespace gtn

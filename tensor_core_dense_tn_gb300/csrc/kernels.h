@@ -187,7 +187,7 @@ struct W4Params {
   void* D; long long ldd;
   int out_f32, act;
   float alpha;
-  int split;           // launch: k-parts per tile (cluster size), 1, 2, 4 or 8
+  int split;           // launch: k-parts per tile (cluster size), 1 to 8
   int num_kb;          // ceil(K / kW4StageK)
   uint64_t timeout_ns;
   int* status;
