@@ -19,10 +19,10 @@
 // Measured (replayed in a graph, weights larger than L2 in rotation, against
 // the time of a copy of the same bytes):
 //    1 token  x 8192 x 8192,  groups of 128                    12.5 us   5.1
-//   16 tokens x 28672 x 4096, groups of 128, zero points       27.4 us   9.2
-//    5 tokens x 5000 x 2000,  groups of 32, fp32 result         8.5 us   0.9
-//    1 token through 8 of 64 experts of 4096 x 2048            12.8 us   5.1
-//   32 tokens, 2 of 16 experts of 8192 x 4096, groups of 64    64.3 us  42.9
+//   16 tokens x 28672 x 4096, groups of 128, zero points       27.6 us   9.2
+//    5 tokens x 5000 x 2000,  groups of 32, fp32 result         8.6 us   0.9
+//    1 token through 8 of 64 experts of 4096 x 2048            12.9 us   5.1
+//   32 tokens, 2 of 16 experts of 8192 x 4096, groups of 64    65.6 us  42.9
 // What bounds it is the multiplying warps' instructions, not memory: with the
 // ring alone (nothing multiplied) the same calls take 8.8, 13.7, 6.4, 9.0 and
 // 48.5 us, with two stages instead of three or four the first four take no
@@ -456,6 +456,11 @@ __device__ __forceinline__ void w4_multiply(const W4Params& p, const W4Block& k,
               for (int j = 0; j < 4; ++j)
                 tot[s][t][j] = fmaf(__uint_as_float(sz[2 * s + j / 2].x), acc[s][t][j], tot[s][t][j]);
         }
+        // The stage's codes were read as ordinary memory and are next written by
+        // a TMA copy: without this fence a late read of the last step's words
+        // met the next codes (a few rows in half a million, in calls of
+        // several items per CTA).
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(k.empty + 8 * slot);
         if (++slot == kStages) {

@@ -240,6 +240,32 @@ def test_rows_of_a_foreign_plan_are_checked():
     assert torch.equal(D[:5], good[:5]) and torch.equal(D[6:], good[6:])
 
 
+@pytest.mark.parametrize("T,k,E,N,K,group", [(32, 2, 16, 8192, 4096, 64), (24, 4, 12, 4096, 4096, 128), (40, 8, 10, 4100, 2048, 32)])
+def test_many_tiles_per_block_are_exact_every_time(T, k, E, N, K, group):
+    """Whole numbers, so every sum is exact: a stage that is overwritten before it is read shows at once."""
+    r = gen(N + K)
+    q = torch.randint(0, 16, (E, N, K // 32), generator=r, device="cuda")          # one code per 32 k
+    codes = (q * 17).to(torch.uint8).repeat_interleave(16, dim=2)
+    zeros = torch.randint(0, 16, (E, N, K // group), generator=r, device="cuda")
+    scales = torch.randint(1, 3, (E, N, K // group), generator=r, device="cuda")
+    W = g.W4Matrix(codes, scales.bfloat16(), zeros.to(torch.uint8), K=K, group=group)
+    a = torch.randint(-2, 3, (T, K // 32), generator=r, device="cuda")
+    A = a.bfloat16().repeat_interleave(32, dim=1)
+    ids = torch.rand(T, E, generator=r, device="cuda").topk(k, dim=1).indices
+    plan = g.ExpertPlan(T, k, E, "cuda")
+    g.expert_dispatch(ids, plan)
+    offsets, token = plan.offsets.tolist(), plan.row_token.long()
+    per = group // 32
+    ref = torch.empty(T * k, N, device="cuda", dtype=torch.float64)
+    for e in range(E):
+        w = (32 * scales[e].repeat_interleave(per, dim=1) * (q[e] - zeros[e].repeat_interleave(per, dim=1))).double()
+        ref[offsets[e]:offsets[e + 1]] = a.double()[token[offsets[e]:offsets[e + 1]]] @ w.T
+    for _ in range(30):
+        D = g.gemm_w4_experts(A, W, plan, gather=True, out_dtype=torch.float32)
+        assert torch.equal(D.double(), ref)
+    status()
+
+
 def test_side_stream_and_repeats():
     mat = tuple(t[0] for t in make(1, 1000, 4096, 128, True, "bf16", 1))
     W, A = g.W4Matrix(*mat, K=4096), acts(16, 4096, 2)
