@@ -285,3 +285,40 @@ def test_offsets_past_32_bits():
     assert torch.equal(Xs, X[plan.row_token.long()])
     dX = g.expert_dispatch_backward(plan, Xs)
     assert torch.equal(dX, 2 * X)
+
+
+@pytest.mark.parametrize("T,k,E", [(512, 1, 7), (513, 1, 7), (256, 2, 200), (171, 3, 61), (1024, 4, 128), (4097, 1, 128),
+                                   (2049, 2, 33), (600001, 1, 61), (70000, 9, 1024)])
+def test_plans_of_every_kernel(T, k, E):
+    test_plan_alone(T, k, E)
+
+
+@pytest.mark.parametrize("H,pad,shift", [(34, 0, 0), (33, 1, 0), (262, 2, 2), (1002, 0, 0), (1, 1, 0), (3, 1, 4)])
+@pytest.mark.parametrize("k", [1, 2, 3, 4, 8, 12])
+def test_bf16_rows_at_4_byte_addresses(H, pad, shift, k):
+    T, E = 77, 9
+    plan, slot_row = make_plan(T, k, E, H + k, "dropped")
+    X, Y, dout = (rows_like(n, H, "bf16", 20 + i, pad, shift) for i, n in enumerate((T, T * k, T)))
+    assert X.stride(0) % 2 == 0 or H == 1
+    w = torch.randn(T, k, generator=gen(3), device="cuda")
+    ids = on_gpu(make_ids(T, k, E, H + k, "dropped"))
+    got = rows_like(T * k, H, "bf16", 30, pad, shift)
+    g.expert_dispatch(ids, plan, X, out=got)
+    tok = plan.row_token.long()
+    want = torch.where((tok >= 0)[:, None], X[tok.clamp(min=0)], torch.zeros((), device="cuda", dtype=X.dtype))
+    assert torch.equal(got, want)
+    out = rows_like(T, H, "bf16", 31, pad, shift)
+    g.expert_combine(plan, Y, w, out=out)
+    terms = slot_rows64(Y, slot_row) * w.double()[..., None]
+    ref, mag = terms.sum(1), terms.abs().sum(1)
+    assert torch.all((out.double() - ref).abs() <= k * 2.0 ** -23 * mag + OUT_EPS["bf16"] * ref.abs())
+    dY = rows_like(T * k, H, "bf16", 32, pad, shift)
+    _, dw = g.expert_combine_backward(plan, Y, w, dout, dY=dY)
+    status()
+    want = torch.zeros(T * k, H, device="cuda", dtype=torch.float64)
+    keep = slot_row >= 0
+    want[slot_row[keep]] = (w.double()[..., None] * dout.double()[:, None, :])[keep]
+    assert torch.all((dY.double() - want).abs() <= (2.0 ** -24 + OUT_EPS["bf16"]) * want.abs())
+    terms = slot_rows64(Y, slot_row) * dout.double()[:, None, :]
+    ref, mag = terms.sum(-1), terms.abs().sum(-1)
+    assert torch.all((dw.double() - ref).abs() <= (H / 32 + 32) * 2.0 ** -23 * mag + OUT_EPS["f32"] * ref.abs())

@@ -266,6 +266,29 @@ def test_many_tiles_per_block_are_exact_every_time(T, k, E, N, K, group):
     status()
 
 
+@pytest.mark.parametrize("parts", range(1, 9))
+@pytest.mark.parametrize("M,group", [(3, 64), (13, 128)])
+def test_every_number_of_parts(parts, M, group):
+    """One tile of `parts` stages, dense, and by expert with several blocks of rows per expert."""
+    N, K = 120, 256 * parts
+    mat = make(3, N, K, group, True, "bf16", parts)
+    A = acts(M, K, 8)
+    D = g.gemm_w4(A, g.W4Matrix(*(t[0] for t in mat), K=K, group=group), out_dtype=torch.float32)
+    assert g.last_launch_info()["k_parts"] == parts
+    check(D, A, tuple(t[0] for t in mat), K, group)
+    T = 17 * M
+    ids = torch.randint(0, 3, (T, 1), generator=gen(parts), device="cuda")
+    plan = g.ExpertPlan(T, 1, 3, "cuda")
+    A = acts(T, K, 9)
+    rows = g.expert_dispatch(ids, plan, A)
+    D = g.gemm_w4_experts(rows, g.W4Matrix(*mat, K=K, group=group), plan)
+    status()
+    offsets = plan.offsets.tolist()
+    for e in range(3):
+        lo, hi = offsets[e], offsets[e + 1]
+        check(D[lo:hi], rows[lo:hi], tuple(t[e] for t in mat), K, group)
+
+
 def test_side_stream_and_repeats():
     mat = tuple(t[0] for t in make(1, 1000, 4096, 128, True, "bf16", 1))
     W, A = g.W4Matrix(*mat, K=4096), acts(16, 4096, 2)
