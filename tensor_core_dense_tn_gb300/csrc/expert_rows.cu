@@ -27,8 +27,11 @@ constexpr int kRowThreads = 256;
 
 // ---------------------------------------------------------------- sorting
 __device__ __forceinline__ int load_id(const ExpertParams& p, int s) {
-  const int t = s / p.k, j = s - t * p.k;
-  const long long at = (long long)t * p.ld_ids + j;
+  long long at = s;
+  if (p.ld_ids != p.k) {   // rows apart: no division where they are not
+    const int t = s / p.k;
+    at = (long long)t * p.ld_ids + (s - t * p.k);
+  }
   const long long v = p.ids64 ? static_cast<const long long*>(p.ids)[at] : static_cast<const int*>(p.ids)[at];
   return v >= 0 && v < p.E ? (int)v : p.E;   // E = dropped
 }
@@ -49,43 +52,41 @@ __global__ void __launch_bounds__(1024) expert_hist_kernel(ExpertParams p) {
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.hist[(long long)blockIdx.x * p.E + e] = h[e];
 }
 
-// Exclusive sum over the 32 lanes' values held in shared memory h[0..n), in
-// place, by one block; `carry` has one int per warp.
-__device__ void block_exclusive_scan(int* h, int n, int* carry) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  int base = 0;
-  for (int at = 0; at < n; at += blockDim.x) {
-    const int i = at + threadIdx.x;
-    const int v = i < n ? h[i] : 0;
-    int x = v;
+// Exclusive sum of h[0..n) in shared memory, in place, by the block's first
+// warp (by the whole block it took 2100 cycles for 129 values, most of them
+// its barriers).
+__device__ void exclusive_scan(int* h, int n) {
+  if (threadIdx.x < 32) {
+    const int per = (n + 31) / 32, lo = min(n, (int)threadIdx.x * per), hi = min(n, lo + per);
+    int sum = 0;
+    for (int i = lo; i < hi; ++i) sum += h[i];
+    int x = sum;
 #pragma unroll
     for (int d = 1; d < 32; d *= 2) {
       const int y = __shfl_up_sync(0xFFFFFFFFu, x, d);
-      if (lane >= d) x += y;
+      if (threadIdx.x >= d) x += y;
     }
-    if (lane == 31) carry[warp] = x;
-    __syncthreads();
-    int before = base, total = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) before += carry[w];
-      total += carry[w];
+    x -= sum;
+    for (int i = lo; i < hi; ++i) {
+      const int v = h[i];
+      h[i] = x;
+      x += v;
     }
-    if (i < n) h[i] = before + x - v;
-    base += total;
-    __syncthreads();
   }
+  __syncthreads();
 }
 
-// Ranks of up to kSteps * blockDim.x slots from `base` on among those of the
-// same expert, in slot order: wh[warp][e] = slots of e before the warp's, and
-// count[e] = all of them.  A warp takes kSteps * 32 consecutive slots.
-constexpr int kSteps = 4;
-__device__ __forceinline__ void rank_slots(const int (&id)[kSteps], int (&rank)[kSteps], int E, uint16_t* wh, int* count) {
+// Ranks of up to S * blockDim.x slots from `base` on among those of the same
+// expert, in slot order: wh[warp][e] = slots of e before the warp's, and
+// count[e] = all of them.  A warp takes S * 32 consecutive slots; a step costs
+// about 1000 cycles, most of them the match, so S is as small as it can be.
+template <int S>
+__device__ __forceinline__ void rank_slots(const int (&id)[S], int (&rank)[S], int E, uint16_t* wh, int* count) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   for (int i = tid; i < warps * E; i += blockDim.x) wh[i] = 0;
   __syncthreads();
 #pragma unroll
-  for (int q = 0; q < kSteps; ++q) {
+  for (int q = 0; q < S; ++q) {
     const unsigned same = __match_any_sync(0xFFFFFFFFu, id[q]);
     const int prior = id[q] < E ? wh[warp * E + id[q]] : 0;
     rank[q] = prior + __popc(same & ((1u << lane) - 1));
@@ -96,7 +97,7 @@ __device__ __forceinline__ void rank_slots(const int (&id)[kSteps], int (&rank)[
   __syncthreads();
   for (int e = tid; e < E; e += blockDim.x) {
     int x = 0;
-#pragma unroll 8
+#pragma unroll 16
     for (int w = 0; w < warps; ++w) {
       const int v = wh[w * E + e];
       wh[w * E + e] = (uint16_t)x;
@@ -107,60 +108,67 @@ __device__ __forceinline__ void rank_slots(const int (&id)[kSteps], int (&rank)[
   __syncthreads();
 }
 
-__device__ __forceinline__ void store_rows(const ExpertParams& p, const int (&id)[kSteps], const int (&rank)[kSteps], int base,
-                                           int hi, const int* start, const uint16_t* wh) {
+template <int S>
+__device__ __forceinline__ void load_ids(const ExpertParams& p, int base, int hi, int (&id)[S]) {
+#pragma unroll
+  for (int q = 0; q < S; ++q) {
+    const int s = base + ((int)(threadIdx.x >> 5) * S + q) * 32 + (threadIdx.x & 31);
+    id[q] = s < hi ? load_id(p, s) : p.E;
+  }
+}
+
+// Writes the slots' rows, and the rows' tokens to row_token.
+template <int S>
+__device__ __forceinline__ void store_rows(const ExpertParams& p, const int (&id)[S], const int (&rank)[S], int base, int hi,
+                                           const int* start, const uint16_t* wh, int* row_token) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int q = 0; q < kSteps; ++q) {
-    const int s = base + (warp * kSteps + q) * 32 + lane;
+  for (int q = 0; q < S; ++q) {
+    const int s = base + (warp * S + q) * 32 + lane;
     if (s >= hi) continue;
     int row = -1;
     if (id[q] < p.E) {
       row = start[id[q]] + wh[warp * p.E + id[q]] + rank[q];
-      p.row_token[row] = s / p.k;
+      row_token[row] = s / p.k;
     }
     p.slot_row[s] = row;
   }
 }
 
-__device__ __forceinline__ void load_ids(const ExpertParams& p, int base, int hi, int (&id)[kSteps]) {
-#pragma unroll
-  for (int q = 0; q < kSteps; ++q) {
-    const int s = base + ((int)(threadIdx.x >> 5) * kSteps + q) * 32 + (threadIdx.x & 31);
-    id[q] = s < hi ? load_id(p, s) : p.E;
-  }
-}
-
-// The whole sort of at most kExpertOneBlock slots, in one block.
+// The whole sort of at most S * blockDim.x slots, in one block.  The rows'
+// tokens are put together in shared memory: stored one by one they take a
+// cycle each.
+template <int S>
 __global__ void __launch_bounds__(1024) expert_sort_kernel(ExpertParams p) {
   extern __shared__ int sm[];
-  int* start = sm;                                          // E + 1
-  int* carry = sm + p.E + 1;                                // 32
-  uint16_t* wh = reinterpret_cast<uint16_t*>(carry + 32);   // warps x E
+  int* start = sm;                                           // E + 1
+  int* token = sm + p.E + 1;                                 // n
+  uint16_t* wh = reinterpret_cast<uint16_t*>(token + p.n);   // warps x E
   griddep_wait();
   griddep_launch_dependents();
-  int id[kSteps], rank[kSteps];
+  int id[S], rank[S];
   load_ids(p, 0, p.n, id);
   if (threadIdx.x == 0) start[p.E] = 0;
   rank_slots(id, rank, p.E, wh, start);
-  block_exclusive_scan(start, p.E + 1, carry);
+  exclusive_scan(start, p.E + 1);
   for (int e = threadIdx.x; e <= p.E; e += blockDim.x) p.offsets[e] = start[e];
-  for (int r = start[p.E] + threadIdx.x; r < p.n; r += blockDim.x) p.row_token[r] = -1;
-  store_rows(p, id, rank, 0, p.n, start, wh);
+  store_rows(p, id, rank, 0, p.n, start, wh, token);
+  __syncthreads();
+  for (int r = threadIdx.x; r < p.n; r += blockDim.x) p.row_token[r] = r < start[p.E] ? token[r] : -1;
 }
 
-// Rows of one chunk's slots.  Every block adds up the histograms before its
+// Rows of one chunk's slots, S * blockDim.x at a time.  Every block adds up the histograms before its
 // own chunk (and all of them, for the experts' offsets), ranks its slots in
 // slot order, and writes their rows.
+template <int S>
 __global__ void __launch_bounds__(1024) expert_rank_kernel(ExpertParams p) {
   extern __shared__ int sm[];
   const int E = p.E, tid = threadIdx.x;
   int* start = sm;                                          // E + 1: next row of each expert
   int* total = sm + E + 1;                                  // E + 1
-  int* carry = sm + 2 * (E + 1);                            // 32
-  uint16_t* wh = reinterpret_cast<uint16_t*>(carry + 32);   // warps x E
+  uint16_t* wh = reinterpret_cast<uint16_t*>(total + E + 1);   // warps x E
   const int lo = blockIdx.x * p.chunk, hi = min(p.n, lo + p.chunk);
-  int id[kSteps], rank[kSteps];
+  int id[S], rank[S];
   // The histogram's kernel waited for everything before it, so the ids are
   // there before it has ended.
   load_ids(p, lo, hi, id);
@@ -183,17 +191,17 @@ __global__ void __launch_bounds__(1024) expert_rank_kernel(ExpertParams p) {
     atomicAdd(&total[e], all);
   }
   __syncthreads();
-  block_exclusive_scan(total, E + 1, carry);
+  exclusive_scan(total, E + 1);
   for (int e = tid; e < E; e += blockDim.x) start[e] += total[e];
   const int V = total[E];
   if (blockIdx.x == 0)
     for (int e = tid; e <= E; e += blockDim.x) p.offsets[e] = total[e];
   for (int r = V + blockIdx.x * blockDim.x + tid; r < p.n; r += gridDim.x * blockDim.x) p.row_token[r] = -1;
-  for (int base = lo; base < hi; base += kSteps * (int)blockDim.x) {
+  for (int base = lo; base < hi; base += S * (int)blockDim.x) {
     if (base > lo) load_ids(p, base, hi, id);
     __syncthreads();
     rank_slots(id, rank, E, wh, total);
-    store_rows(p, id, rank, base, hi, start, wh);
+    store_rows(p, id, rank, base, hi, start, wh, p.row_token);
     __syncthreads();
     for (int e = tid; e < E; e += blockDim.x) start[e] += total[e];
   }
@@ -628,8 +636,12 @@ const void* kernel_of(int es, int ch) {
 
 }  // namespace
 
+// Chunks of 1024, 2048 or 4096 slots, at most 64 where that can be: every
+// block of the ranking adds up all of them.  (131072 slots of 256 experts in
+// 128 / 64 / 32 chunks: 11.8 / 9.6 / 12.0 us; 262144 in 128 / 64: 15.4 / 12.7.)
 int expert_chunks(long long n) {
-  const long long c = (n + 1023) / 1024;
+  const int per = n <= 65536 ? 1024 : (n <= 131072 ? 2048 : 4096);
+  const long long c = (n + per - 1) / per;
   return (int)(c < 1 ? 1 : (c > kExpertMaxChunks ? kExpertMaxChunks : c));
 }
 
@@ -664,32 +676,35 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
     info->kernel = "expert_dispatch_small_kernel";
     return launch(f, grid, kRowThreads, smem, stream, p);
   }
-  const size_t rank_smem = (2 * ((size_t)p.E + 1) + 32) * sizeof(int) + (size_t)32 * p.E * sizeof(uint16_t);
-  const size_t sort_smem = ((size_t)p.E + 1 + 32) * sizeof(int) + (size_t)32 * p.E * sizeof(uint16_t);
+  auto rank_bytes = [](int E) { return 2 * ((size_t)E + 1) * sizeof(int) + (size_t)32 * E * sizeof(uint16_t); };
+  auto sort_bytes = [](int E, int n) { return ((size_t)E + 1 + n) * sizeof(int) + (size_t)32 * E * sizeof(uint16_t); };
+  const void* ranks[3] = {(const void*)expert_rank_kernel<1>, (const void*)expert_rank_kernel<2>, (const void*)expert_rank_kernel<4>};
+  const void* sorts[3] = {(const void*)expert_sort_kernel<1>, (const void*)expert_sort_kernel<2>, (const void*)expert_sort_kernel<4>};
   static bool configured[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 64 && !configured[dev]) {
-    e = cudaFuncSetAttribute((const void*)expert_rank_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)((2 * (kExpertMax + 1) + 32) * sizeof(int) + 32 * kExpertMax * sizeof(uint16_t)));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute((const void*)expert_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)((kExpertMax + 1 + 32) * sizeof(int) + 32 * kExpertMax * sizeof(uint16_t)));
+    constexpr cudaFuncAttribute kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    for (const void* f : ranks)
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(f, kSmem, (int)rank_bytes(kExpertMax));
+    for (const void* f : sorts)
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(f, kSmem, (int)sort_bytes(kExpertMax, kExpertOneBlock));
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
   *info = LaunchInfo{};
   if (p.n <= kExpertOneBlock) {
-    if ((e = launch((const void*)expert_sort_kernel, dim3(1), 1024, sort_smem, stream, p))) return e;
-    info->grid = 1; info->cluster = 1; info->block = 1024; info->smem_bytes = (int)sort_smem;
+    const size_t bytes = sort_bytes(p.E, p.n);
+    if ((e = launch(sorts[p.n <= 1024 ? 0 : (p.n <= 2048 ? 1 : 2)], dim3(1), 1024, bytes, stream, p))) return e;
+    info->grid = 1; info->cluster = 1; info->block = 1024; info->smem_bytes = (int)bytes;
     info->kernel = "expert_sort_kernel";
   } else {
     p.chunks = expert_chunks(p.n);
     p.chunk = (int)(((long long)p.n + p.chunks - 1) / p.chunks);
     if ((e = launch((const void*)expert_hist_kernel, dim3(p.chunks), 1024, (size_t)p.E * sizeof(int), stream, p))) return e;
-    if ((e = launch((const void*)expert_rank_kernel, dim3(p.chunks), 1024, rank_smem, stream, p))) return e;
-    info->grid = p.chunks; info->cluster = 1; info->block = 1024; info->smem_bytes = (int)rank_smem;
+    if ((e = launch(ranks[p.chunk <= 1024 ? 0 : (p.chunk <= 2048 ? 1 : 2)], dim3(p.chunks), 1024, rank_bytes(p.E), stream, p))) return e;
+    info->grid = p.chunks; info->cluster = 1; info->block = 1024; info->smem_bytes = (int)rank_bytes(p.E);
     info->kernel = "expert_rank_kernel";
   }
   if (p.H == 0) return cudaSuccess;
