@@ -434,40 +434,50 @@ __global__ void __launch_bounds__(kRowThreads) expert_dispatch_small_kernel(Expe
     }
 }
 
-// out[t] = sum_j w_j in[r_j], slots in blocks of KU with all their loads in flight.
+// Rows and weights of the slots j0 .. j0 + KU - 1 of token t.
+template <int KU>
+__device__ __forceinline__ void load_slots(const ExpertParams& p, int t, int j0, int (&r)[KU], float (&w)[KU]) {
+#pragma unroll
+  for (int j = 0; j < KU; ++j) {
+    r[j] = t < p.T ? load_row(p, t, j0 + j) : -1;
+    w[j] = r[j] >= 0 ? load_weight(p, t, j0 + j) : 0.0f;
+  }
+}
+
+// acc += sum_j w_j in[r_j] over the lane's chunks from c0 on, with all KU U loads in flight.
 template <int ES, int CH, int KU, int U>
-__device__ __forceinline__ void combine_row(const ExpertParams& p, int t, int lane, int lanes) {
-  using R = typename Raw<CH>::T;
+__device__ __forceinline__ void add_rows(const ExpertParams& p, const int (&r)[KU], const float (&w)[KU], int c0, int lanes,
+                                         float (&acc)[U][CH / ES]) {
   constexpr int V = CH / ES;
-  for (int c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += lanes * U * gridDim.y) {
-    float acc[U][V];
+  typename Raw<CH>::T x[KU][U];
+#pragma unroll
+  for (int j = 0; j < KU; ++j)
 #pragma unroll
     for (int u = 0; u < U; ++u)
+      x[j][u] = r[j] >= 0 && c0 + u * lanes < p.nch ? ldc<CH>(p.in, p.in_pitch, r[j], c0 + u * lanes) : zero_raw<CH>();
 #pragma unroll
-      for (int v = 0; v < V; ++v) acc[u][v] = 0.0f;
-    for (int j0 = 0; j0 < p.k; j0 += KU) {
-      int r[KU];
-      float w[KU];
+  for (int j = 0; j < KU; ++j)
 #pragma unroll
-      for (int j = 0; j < KU; ++j) {
-        r[j] = load_row(p, t, j0 + j);
-        w[j] = r[j] >= 0 ? load_weight(p, t, j0 + j) : 0.0f;
-      }
-      R x[KU][U];
+    for (int u = 0; u < U; ++u) {
+      float f[V];
+      unpack<ES, CH>(x[j][u], f);
 #pragma unroll
-      for (int j = 0; j < KU; ++j)
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-          x[j][u] = r[j] >= 0 && c0 + u * lanes < p.nch ? ldc<CH>(p.in, p.in_pitch, r[j], c0 + u * lanes) : zero_raw<CH>();
-#pragma unroll
-      for (int j = 0; j < KU; ++j)
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          float f[V];
-          unpack<ES, CH>(x[j][u], f);
-#pragma unroll
-          for (int v = 0; v < V; ++v) acc[u][v] = fmaf(w[j], f[v], acc[u][v]);
-        }
+      for (int v = 0; v < V; ++v) acc[u][v] = fmaf(w[j], f[v], acc[u][v]);
+    }
+}
+
+// out[t] = sum_j w_j in[r_j].  r, w: the first KU slots.
+template <int ES, int CH, int KU, int U>
+__device__ __forceinline__ void combine_row(const ExpertParams& p, int t, const int (&r)[KU], const float (&w)[KU], int lane,
+                                            int lanes) {
+  for (int c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += lanes * U * gridDim.y) {
+    float acc[U][CH / ES] = {};
+    add_rows<ES, CH, KU, U>(p, r, w, c0, lanes, acc);
+    for (int j0 = KU; j0 < p.k; j0 += KU) {
+      int more[KU];
+      float weight[KU];
+      load_slots<KU>(p, t, j0, more, weight);
+      add_rows<ES, CH, KU, U>(p, more, weight, c0, lanes, acc);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -475,14 +485,38 @@ __device__ __forceinline__ void combine_row(const ExpertParams& p, int t, int la
   }
 }
 
+// The first KU slots are loaded before the walk along the row (8192 x 8 rows of
+// 2048 bf16: 46.2 us, 0.97 of a copy, against 49.6 with the loads inside it).
+// One and two slots: as many blocks as run at once walk over the tokens, each
+// with the next token's rows and weights loaded ahead.  8192 rows of 4096
+// bf16: one slot 24.0 us against 24.9 with a block per token, two slots 32.8
+// against 36.9.  More slots lose by it (4096 tokens of four: 36.2 against 28.6).
+template <int KU> constexpr bool kWalk = KU <= 2;
+
 template <int ES, int CH, int KU, int U>
 __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(ExpertParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lanes = p.lanes, t = blockIdx.x * (kRowThreads / lanes) + threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  if (t >= p.T) return;
-  combine_row<ES, CH, KU, U>(p, t, lane, lanes);
-  if (p.tail) combine_row<ES, ES, KU, 1>(tail_of<ES>(p, CH), t, lane, lanes);
+  const int lanes = p.lanes, per = kRowThreads / lanes, lane = threadIdx.x % lanes;
+  int t = blockIdx.x * per + threadIdx.x / lanes;
+  int r[KU];
+  float w[KU];
+  load_slots<KU>(p, t, 0, r, w);
+  while (t < p.T) {
+    int next_r[KU];
+    float next_w[KU];
+    const int next = t + gridDim.x * per;
+    if constexpr (kWalk<KU>) load_slots<KU>(p, next, 0, next_r, next_w);
+    combine_row<ES, CH, KU, U>(p, t, r, w, lane, lanes);
+    if (p.tail) combine_row<ES, ES, KU, 1>(tail_of<ES>(p, CH), t, r, w, lane, lanes);
+    if constexpr (!kWalk<KU>) break;
+    t = next;
+#pragma unroll
+    for (int j = 0; j < KU; ++j) {
+      r[j] = next_r[j];
+      w[j] = next_w[j];
+    }
+  }
 }
 
 // in = dout, in2 = Y, out = dY.  Adds the lane's part of <dout, Y_j> to dot[j].
@@ -718,7 +752,8 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
 
 namespace {
 
-// Chunks per lane in flight, for KU slots at once.  Measured in us with rows
+// Chunks per lane in flight, for KU slots at once.  Measured in us, a block per
+// token and each slot's row loaded where it is used, with rows
 // of 4096 bf16 in 16-byte chunks and rows of 1002 bf16 in 4-byte ones, 8192
 // tokens of one and two slots, 4096 of four, 2048 of eight:
 //                    16-byte, U = 1 / 2 / 4     4-byte, U = 1 / 2 / 4 / 8
@@ -754,11 +789,25 @@ cudaError_t launch_expert_combine(ExpertParams p, int es, int sms, cudaStream_t 
   const int ku = slots_unrolled(p.k);
   const int U = combine_chunks(ku, ch);
   p.lanes = lanes_for(p.nch, U, 1);
-  const dim3 grid = row_grid(p, U, sms);
+  dim3 grid = row_grid(p, U, sms);
   const void* f = ku == 1   ? kernel_of<ForSlots<1>::Combine>(es, ch)
                   : ku == 2 ? kernel_of<ForSlots<2>::Combine>(es, ch)
                   : ku == 4 ? kernel_of<ForSlots<4>::Combine>(es, ch)
                             : kernel_of<ForSlots<8>::Combine>(es, ch);
+  if (ku <= 2) {
+    static int resident[64][2][5] = {};   // blocks per SM by slots and chunk
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int& blocks = resident[dev][ku - 1][es == 4 ? (ch == 16 ? 0 : 1) : (ch == 16 ? 2 : (ch == 4 ? 3 : 4))];
+    if (blocks == 0) {
+      int got = 0;
+      if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&got, f, kRowThreads, 0))) return e;
+      blocks = got > 0 ? got : 1;
+    }
+    if (grid.x > (unsigned)(blocks * sms)) grid.x = blocks * sms;
+  }
   *info = LaunchInfo{};
   info->grid = grid.x * grid.y; info->cluster = 1; info->block = kRowThreads;
   info->kernel = "expert_combine_kernel";
