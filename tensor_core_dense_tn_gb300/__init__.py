@@ -389,7 +389,7 @@ def _out_code(dtype, what):
 
 
 def _rows_of(t, rows, width, what):
-    """Checks a (rows, width) CUDA matrix with unit column stride; returns its row stride."""
+    """Checks a (rows, width) CUDA matrix with unit column stride and rows that do not overlap; returns its row stride."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] != rows or (width is not None and shape[1] != width) or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA matrix of {rows} x {'H' if width is None else width}, "
@@ -397,7 +397,12 @@ def _rows_of(t, rows, width, what):
     ld, wide = stride[0], shape[1]
     if stride[1] != 1 and wide > 1 and rows > 0:
         raise ValueError(f"{what} must have unit column stride")
-    return ld if ld > wide else wide
+    if ld < wide:
+        if rows > 1:        # a broadcast row, or rows that overlap
+            raise ValueError(f"{what} must have a row stride of at least its row length {wide}, not {ld} "
+                             "(contiguous() makes a copy that has)")
+        ld = wide           # a single row's stride says nothing
+    return ld
 
 
 def _stream_of(t):
