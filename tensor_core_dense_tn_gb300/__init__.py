@@ -388,11 +388,22 @@ def _out_code(dtype, what):
     return code
 
 
-def _rows_of(t, rows, width, what):
-    """Checks a (rows, width) CUDA matrix with unit column stride and rows that do not overlap; returns its row stride."""
+def _gpu_of(index, what):
+    """Checks that `what`, on the GPU `index` (-1: host memory), is where the library launches; returns the index."""
+    if index < 0:
+        raise ValueError(f"{what} must be in GPU memory")
+    current = _torch.cuda.current_device()
+    if index != current:
+        raise ValueError(f"{what} is on GPU {index}, but calls go to the current GPU, which is {current}")
+    return index
+
+
+def _rows_of(t, rows, width, what, gpu):
+    """Checks a (rows, width) matrix on `gpu` with unit column stride and rows that do not overlap; returns its
+    row stride."""
     shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or shape[0] != rows or (width is not None and shape[1] != width) or not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA matrix of {rows} x {'H' if width is None else width}, "
+    if len(shape) != 2 or shape[0] != rows or (width is not None and shape[1] != width) or t.get_device() != gpu:
+        raise ValueError(f"{what} must be a matrix of {rows} x {'H' if width is None else width} on GPU {gpu}, "
                          f"not {tuple(shape)} on {t.device}")
     ld, wide = stride[0], shape[1]
     if stride[1] != 1 and wide > 1 and rows > 0:
@@ -436,6 +447,9 @@ class ExpertPlan:
                 raise ValueError(f"{name} must be a contiguous int32 tensor")
         if slot_row.dim() != 2 or offsets.numel() != experts + 1 or row_token.numel() != slot_row.numel():
             raise ValueError("a plan has experts + 1 offsets, (tokens, slots) slot rows and tokens * slots row tokens")
+        self.gpu = slot_row.get_device()        # -1 in host memory, where no call takes it
+        if offsets.get_device() != self.gpu or row_token.get_device() != self.gpu:
+            raise ValueError("the arrays of a plan must be on one device")
         self.offsets, self.slot_row, self.row_token = offsets, slot_row, row_token
         self.tokens, self.slots = slot_row.shape
         self.experts, self.rows = experts, slot_row.numel()
@@ -460,9 +474,12 @@ class W4Matrix:
         if codes.shape[-1] * 2 < K:
             raise ValueError(f"codes hold {2 * codes.shape[-1]} values a row, fewer than K = {K}")
         want = tuple(codes.shape[:-1]) + (-(-K // group),)
+        self.gpu = codes.get_device()
         for name, t in (("scales", scales), ("zeros", zeros)):
-            if t is not None and (tuple(t.shape) != want or not t.is_cuda or (t.stride(-1) != 1 and want[-1] > 1)):
-                raise ValueError(f"{name} must be a CUDA tensor of {want} with unit stride along the groups")
+            if t is None:
+                continue
+            if tuple(t.shape) != want or t.get_device() != self.gpu or (t.stride(-1) != 1 and want[-1] > 1):
+                raise ValueError(f"{name} must be a tensor of {want} on the codes' GPU with unit stride along the groups")
         if zeros is not None and zeros.dtype != torch.uint8:
             raise ValueError("zeros must be uint8")
         self.codes, self.scales, self.zeros, self.group = codes, scales, zeros, group
@@ -482,17 +499,18 @@ def expert_dispatch(ids, plan: ExpertPlan, X=None, out=None, stream=None):
     wide = ids.dtype == torch.int64
     if not wide and ids.dtype != torch.int32:
         raise ValueError("ids must be int32 or int64")
-    ld_ids = _rows_of(ids, plan.tokens, plan.slots, "ids")
+    gpu = _gpu_of(plan.gpu, "the plan")
+    ld_ids = _rows_of(ids, plan.tokens, plan.slots, "ids", gpu)
     H, x, ldx, o, ldo, code = 0, None, 0, None, 0, OUT_BF16
     if X is not None:
-        code, ldx = _out_code(X.dtype, "X"), _rows_of(X, plan.tokens, None, "X")
+        code, ldx = _out_code(X.dtype, "X"), _rows_of(X, plan.tokens, None, "X", gpu)
         H, x = X.shape[1], X.data_ptr()
         if out is None:
             out, ldo = torch.empty((plan.rows, H), dtype=X.dtype, device=X.device), H
         else:
             if out.dtype != X.dtype:
                 raise ValueError("out must have X's type")
-            ldo = _rows_of(out, plan.rows, H, "out")
+            ldo = _rows_of(out, plan.rows, H, "out", gpu)
         o = out.data_ptr()
     rc = (_lib or load()).gemm_expert_dispatch(plan.info, ids.data_ptr(), ld_ids, wide, H, x, ldx, code, o, ldo,
                                                _stream_of(ids) if stream is None else stream or None)
@@ -513,16 +531,17 @@ def expert_combine(plan: ExpertPlan, Y, weights, out=None, stream=None):
 
 def _combine(plan, Y, weights, out, stream):
     torch = _torch or _t()
-    code, ldy = _out_code(Y.dtype, "rows"), _rows_of(Y, plan.rows, None, "rows")
+    gpu = _gpu_of(plan.gpu, "the plan")
+    code, ldy = _out_code(Y.dtype, "rows"), _rows_of(Y, plan.rows, None, "rows", gpu)
     H = Y.shape[1]
     if weights is not None:
-        wcode, ldw = _out_code(weights.dtype, "weights"), _rows_of(weights, plan.tokens, plan.slots, "weights")
+        wcode, ldw = _out_code(weights.dtype, "weights"), _rows_of(weights, plan.tokens, plan.slots, "weights", gpu)
     if out is None:
         out, ldo = torch.empty((plan.tokens, H), dtype=Y.dtype, device=Y.device), H
     else:
         if out.dtype != Y.dtype:
             raise ValueError("out must have the rows' type")
-        ldo = _rows_of(out, plan.tokens, H, "out")
+        ldo = _rows_of(out, plan.tokens, H, "out", gpu)
     lib, s = _lib or load(), _stream_of(Y) if stream is None else stream or None
     if weights is None:
         rc = lib.gemm_expert_dispatch_backward(plan.info, H, Y.data_ptr(), ldy, code, out.data_ptr(), ldo, s)
@@ -537,12 +556,13 @@ def _combine(plan, Y, weights, out, stream):
 def expert_combine_backward(plan: ExpertPlan, Y, weights, dout, dY=None, dweights=None, stream=None):
     """Gradients of expert_combine: (dY, dweights), in Y's and weights' types."""
     torch = _torch or _t()
-    code, ldy = _out_code(Y.dtype, "Y"), _rows_of(Y, plan.rows, None, "Y")
+    gpu = _gpu_of(plan.gpu, "the plan")
+    code, ldy = _out_code(Y.dtype, "Y"), _rows_of(Y, plan.rows, None, "Y", gpu)
     H = Y.shape[1]
     if dout.dtype != Y.dtype:
         raise ValueError("dout must have Y's type")
-    lddo = _rows_of(dout, plan.tokens, H, "dout")
-    wcode, ldw = _out_code(weights.dtype, "weights"), _rows_of(weights, plan.tokens, plan.slots, "weights")
+    lddo = _rows_of(dout, plan.tokens, H, "dout", gpu)
+    wcode, ldw = _out_code(weights.dtype, "weights"), _rows_of(weights, plan.tokens, plan.slots, "weights", gpu)
     if dY is None:
         dY = torch.empty((plan.rows, H), dtype=Y.dtype, device=Y.device)
     if dweights is None:
@@ -551,8 +571,8 @@ def expert_combine_backward(plan: ExpertPlan, Y, weights, dout, dY=None, dweight
         raise ValueError("dY and dweights must have Y's and weights' types")
     rc = (_lib or load()).gemm_expert_combine_backward(
         plan.info, H, Y.data_ptr(), ldy, dout.data_ptr(), lddo, code, weights.data_ptr(), ldw, wcode, dY.data_ptr(),
-        _rows_of(dY, plan.rows, H, "dY"), dweights.data_ptr(), _rows_of(dweights, plan.tokens, plan.slots, "dweights"),
-        _stream_of(Y) if stream is None else stream or None)
+        _rows_of(dY, plan.rows, H, "dY", gpu), dweights.data_ptr(),
+        _rows_of(dweights, plan.tokens, plan.slots, "dweights", gpu), _stream_of(Y) if stream is None else stream or None)
     if rc:
         _check(rc)
     return dY, dweights
@@ -574,15 +594,18 @@ def _w4(plan, A, W, gather, alpha, activation, out_dtype, out, stream):
     torch = _torch or _t()
     if A.dtype != torch.bfloat16:
         raise ValueError("A must be bf16")
+    gpu = _gpu_of(W.gpu, "W")
+    if plan is not None and plan.gpu != gpu:
+        raise ValueError("the plan and W must be on one GPU")
     rows = A.shape[0] if plan is None else plan.tokens if gather else plan.rows
-    lda = _rows_of(A, rows, W.K, "A")
+    lda = _rows_of(A, rows, W.K, "A", gpu)
     M = rows if plan is None else plan.rows
     if out is None:
         out, ldd = torch.empty((M, W.N), dtype=out_dtype or torch.bfloat16, device=A.device), W.N
     else:
         if out_dtype is not None and out.dtype != out_dtype:
             raise ValueError("out must have out_dtype")
-        ldd = _rows_of(out, M, W.N, "out")
+        ldd = _rows_of(out, M, W.N, "out", gpu)
     code = _out_code(out.dtype, "out")
     lib, s = _lib or load(), _stream_of(A) if stream is None else stream or None
     if plan is None:

@@ -24,7 +24,7 @@ class OnGpu(torch.Tensor):
 
 
 def gpu(t, index=0):
-    t = t.as_subclass(OnGpu)
+    t = t.detach().as_subclass(OnGpu)
     t.index = index
     return t
 
@@ -125,3 +125,66 @@ def test_the_stride_of_a_single_row_does_not_matter(lib):
     g.expert_dispatch(ids, plan, X, stream=1)
     (_, args), = lib.calls
     assert args[2] == K and args[6] == H
+
+
+PLANNED = [name for name in CALLS if name != "w4"]
+
+
+def elsewhere(t):
+    return gpu(t, 1)
+
+
+def in_host_memory(t):
+    return t.as_subclass(torch.Tensor)
+
+
+def moved_plan(how):
+    p = make_plan()
+    return g.ExpertPlan.of(how(p.offsets), how(p.slot_row), how(p.row_token))
+
+
+@pytest.mark.parametrize("name", PLANNED)
+@pytest.mark.parametrize("how", [in_host_memory, elsewhere])
+def test_a_plan_elsewhere_is_refused(lib, name, how):
+    """The kernels read and write the plan's arrays: host memory or another GPU's would fault."""
+    with pytest.raises(ValueError):
+        CALLS[name][0](moved_plan(how), operands(name))
+    assert lib.calls == []
+
+
+@pytest.mark.parametrize("name,what", OPERANDS)
+@pytest.mark.parametrize("how", [in_host_memory, elsewhere])
+def test_an_operand_elsewhere_is_refused(lib, name, what, how):
+    rows, width, dtype = shape_of(name, what)
+    with pytest.raises(ValueError):
+        CALLS[name][0](make_plan(), operands(name, **{what: how(zeros(rows, width, dtype=dtype))}))
+    assert lib.calls == []
+
+
+def test_a_matrix_elsewhere_is_refused(lib):
+    codes, scales = zeros(N, KW // 2, dtype=torch.uint8), zeros(N, KW // 64)
+    W = g.W4Matrix(elsewhere(codes), elsewhere(scales), None, K=KW, group=64)
+    with pytest.raises(ValueError):
+        g.gemm_w4(zeros(T, KW, dtype=BF16), W, stream=1)
+    assert lib.calls == []
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_operands_of_another_gpu_than_the_current_one_are_refused(lib, name, monkeypatch):
+    """The library launches on the current GPU, whatever the tensors' GPU is."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        CALLS[name][0](make_plan(), operands(name))
+    assert lib.calls == []
+
+
+def test_parts_of_a_plan_or_a_matrix_on_different_gpus_are_refused():
+    p = make_plan()
+    for arrays in ((elsewhere(p.offsets), p.slot_row, p.row_token), (p.offsets, elsewhere(p.slot_row), p.row_token),
+                   (p.offsets, p.slot_row, elsewhere(p.row_token))):
+        with pytest.raises(ValueError):
+            g.ExpertPlan.of(*arrays)
+    codes, scales, points = zeros(N, KW // 2, dtype=torch.uint8), zeros(N, KW // 64), zeros(N, KW // 64, dtype=torch.uint8)
+    for parts in ((elsewhere(codes), scales, points), (codes, elsewhere(scales), points), (codes, scales, elsewhere(points))):
+        with pytest.raises(ValueError):
+            g.W4Matrix(*parts, K=KW, group=64)
