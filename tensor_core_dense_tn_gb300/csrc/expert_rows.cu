@@ -606,7 +606,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_back_kernel(Expert
     }
   }
   if (p.out && t < p.T) {
-    const int V = p.offsets[p.E];
+    const int V = min(max(p.offsets[p.E], 0), p.n);   // a caller's own plan may hold anything
     for (long long r = V + t; r < p.n; r += p.T) {
       zero_row<CH>(p, r, lane, lanes);
       if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
