@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(ExpertParams
   if (t >= p.T) return;
   copy_row<CH, U>(p, t, rows + group * p.k, p.k, lane, lanes, x);
   if (p.tail) copy_tail<ES>(tail_of<ES>(p, CH), t, rows + group * p.k, p.k, lane, lanes);
-  for (long long r = V + t; r < p.n; r += p.T) {
+  for (long long r = (long long)V + t; r < p.n; r += p.T) {
     zero_row<CH>(p, r, lane, lanes);
     if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
   }
@@ -428,7 +428,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_dispatch_small_kernel(Expe
   copy_row<CH, U>(p, t, rows + group * p.k, p.k, lane, lanes, x);
   if (p.tail) copy_tail<ES>(tail_of<ES>(p, CH), t, rows + group * p.k, p.k, lane, lanes);
   if (p.nch + p.tail > 0)
-    for (long long r = V + t; r < p.n; r += p.T) {
+    for (long long r = (long long)V + t; r < p.n; r += p.T) {
       zero_row<CH>(p, r, lane, lanes);
       if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
     }
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_back_kernel(Expert
   }
   if (p.out && t < p.T) {
     const int V = min(max(p.offsets[p.E], 0), p.n);   // a caller's own plan may hold anything
-    for (long long r = V + t; r < p.n; r += p.T) {
+    for (long long r = (long long)V + t; r < p.n; r += p.T) {
       zero_row<CH>(p, r, lane, lanes);
       if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
     }
