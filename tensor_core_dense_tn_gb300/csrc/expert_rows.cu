@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(1024) expert_rank_kernel(ExpertParams p) {
   const int V = total[E];
   if (blockIdx.x == 0)
     for (int e = tid; e <= E; e += blockDim.x) p.offsets[e] = total[e];
-  for (int r = V + blockIdx.x * blockDim.x + tid; r < p.n; r += gridDim.x * blockDim.x) p.row_token[r] = -1;
+  for (long long r = (long long)V + blockIdx.x * blockDim.x + tid; r < p.n; r += gridDim.x * blockDim.x) p.row_token[r] = -1;
   for (int base = lo; base < hi; base += S * (int)blockDim.x) {
     if (base > lo) load_ids(p, base, hi, id);
     __syncthreads();

@@ -88,3 +88,23 @@ def test_rows_past_the_last_with_half_of_2_to_the_31_tokens():
     assert equal_in_pieces(dw, X * X)       # one product each, rounded once
     del plan, X, whole, w, dw
     torch.cuda.empty_cache()
+
+
+def test_plan_of_the_most_slots():
+    """The last slots that a plan may have, nearly all of them dropped."""
+    if free_gigabytes() < 60:
+        pytest.skip("needs 60 GB")
+    n, E = (1 << 31) - 4097, 2
+    ids = torch.full((n, 1), -1, dtype=torch.int32, device="cuda")
+    ids[0], ids[n // 2], ids[n - 1] = 1, 1, 0
+    plan = g.ExpertPlan(n, 1, E, "cuda")
+    plan.row_token.fill_(-99)
+    g.expert_dispatch(ids, plan)
+    status()
+    assert plan.offsets.tolist() == [0, 1, 3]
+    assert plan.row_token[:3].tolist() == [n - 1, 0, n // 2]
+    assert [plan.slot_row[t].item() for t in (n - 1, 0, n // 2)] == [0, 1, 2]
+    assert all(bool((part == -1).all()) for part in plan.row_token[3:].split(1 << 28))
+    assert sum(int((part != -1).sum()) for part in plan.slot_row.split(1 << 28)) == 3
+    del plan, ids
+    torch.cuda.empty_cache()
