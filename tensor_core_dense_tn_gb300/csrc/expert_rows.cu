@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(ExpertParam
   while (t < p.T) {
     int next_r[KU];
     float next_w[KU];
-    const int next = t + gridDim.x * per;
+    const int step = gridDim.x * per, next = p.T - t > step ? t + step : p.T;   // t + step may pass 2^31
     if constexpr (kWalk<KU>) load_slots<KU>(p, next, 0, next_r, next_w);
     combine_row<ES, CH, KU, U>(p, t, r, w, lane, lanes);
     if (p.tail) combine_row<ES, ES, KU, 1>(tail_of<ES>(p, CH), t, r, w, lane, lanes);

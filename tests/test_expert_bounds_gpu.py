@@ -108,3 +108,22 @@ def test_plan_of_the_most_slots():
     assert sum(int((part != -1).sum()) for part in plan.slot_row.split(1 << 28)) == 3
     del plan, ids
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+def test_combine_of_the_most_tokens(weighted):
+    """The blocks that walk over the tokens stop at the last one, also where the next step passes 2^31."""
+    if free_gigabytes() < 60:
+        pytest.skip("needs 60 GB")
+    T = (1 << 31) - 4097
+    slot_row = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1)
+    plan = g.ExpertPlan.of(torch.tensor([0, T], dtype=torch.int32, device="cuda"), slot_row, slot_row.view(-1))
+    Y = ramp(T, torch.bfloat16).view(T, 1)
+    if weighted:
+        out = g.expert_combine(plan, Y, torch.ones(T, 1, dtype=torch.bfloat16, device="cuda"))
+    else:
+        out = g.expert_dispatch_backward(plan, Y)
+    status()
+    assert equal_in_pieces(out, Y)
+    del plan, slot_row, Y, out
+    torch.cuda.empty_cache()
