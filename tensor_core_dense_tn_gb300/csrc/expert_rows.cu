@@ -259,21 +259,22 @@ __device__ __forceinline__ typename Raw<CH>::T pack(const float (&x)[CH / ES]) {
   }
 }
 
+// Chunks are counted without a sign: a row has fewer than 2^31, but a step past its end may pass that.
 template <int CH>
-__device__ __forceinline__ typename Raw<CH>::T ldc(const void* base, long long row_bytes, long long row, int c) {
+__device__ __forceinline__ typename Raw<CH>::T ldc(const void* base, long long row_bytes, long long row, unsigned c) {
   return reinterpret_cast<const typename Raw<CH>::T*>(static_cast<const char*>(base) + row * row_bytes)[c];
 }
 template <int CH>
-__device__ __forceinline__ void stc(void* base, long long row_bytes, long long row, int c, typename Raw<CH>::T v) {
+__device__ __forceinline__ void stc(void* base, long long row_bytes, long long row, unsigned c, typename Raw<CH>::T v) {
   reinterpret_cast<typename Raw<CH>::T*>(static_cast<char*>(base) + row * row_bytes)[c] = v;
 }
 // The same, marked as not used again soon.
 template <int CH>
-__device__ __forceinline__ typename Raw<CH>::T ldc_stream(const void* base, long long row_bytes, long long row, int c) {
+__device__ __forceinline__ typename Raw<CH>::T ldc_stream(const void* base, long long row_bytes, long long row, unsigned c) {
   return __ldcs(reinterpret_cast<const typename Raw<CH>::T*>(static_cast<const char*>(base) + row * row_bytes) + c);
 }
 template <int CH>
-__device__ __forceinline__ void stc_stream(void* base, long long row_bytes, long long row, int c, typename Raw<CH>::T v) {
+__device__ __forceinline__ void stc_stream(void* base, long long row_bytes, long long row, unsigned c, typename Raw<CH>::T v) {
   __stcs(reinterpret_cast<typename Raw<CH>::T*>(static_cast<char*>(base) + row * row_bytes) + c, v);
 }
 
@@ -293,7 +294,7 @@ __device__ __forceinline__ int load_row(const ExpertParams& p, int t, int j) {
 
 // Chunks c0, c0 + lanes, ... of token t's row.
 template <int CH, int U>
-__device__ __forceinline__ void load_chunks(const ExpertParams& p, int t, int c0, int lanes, typename Raw<CH>::T (&x)[U]) {
+__device__ __forceinline__ void load_chunks(const ExpertParams& p, int t, unsigned c0, unsigned lanes, typename Raw<CH>::T (&x)[U]) {
 #pragma unroll
   for (int u = 0; u < U; ++u)
     if (c0 + u * lanes < p.nch) x[u] = ldc<CH>(p.in, p.in_pitch, t, c0 + u * lanes);
@@ -302,10 +303,10 @@ __device__ __forceinline__ void load_chunks(const ExpertParams& p, int t, int c0
 // Copies token t's row to the rows r[0..count), from the chunks in x on; U
 // chunks per lane in flight.
 template <int CH, int U>
-__device__ __forceinline__ void copy_row(const ExpertParams& p, int t, const int* r, int count, int lane, int lanes,
+__device__ __forceinline__ void copy_row(const ExpertParams& p, int t, const int* r, int count, unsigned lane, unsigned lanes,
                                          typename Raw<CH>::T (&x)[U]) {
-  const int step = lanes * U * gridDim.y;
-  for (int c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += step) {
+  const unsigned step = lanes * U * gridDim.y;
+  for (unsigned c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += step) {
     for (int j = 0; j < count; ++j) {
       if (r[j] < 0) continue;
 #pragma unroll
@@ -318,8 +319,8 @@ __device__ __forceinline__ void copy_row(const ExpertParams& p, int t, const int
 
 // Zeroes row r of p.out, by `lanes` threads of each of the gridDim.y blocks.
 template <int CH>
-__device__ __forceinline__ void zero_row(const ExpertParams& p, long long r, int lane, int lanes) {
-  for (int c = lane + lanes * blockIdx.y; c < p.nch; c += lanes * gridDim.y) stc<CH>(p.out, p.out_pitch, r, c, zero_raw<CH>());
+__device__ __forceinline__ void zero_row(const ExpertParams& p, long long r, unsigned lane, unsigned lanes) {
+  for (unsigned c = lane + lanes * blockIdx.y; c < p.nch; c += lanes * gridDim.y) stc<CH>(p.out, p.out_pitch, r, c, zero_raw<CH>());
 }
 
 // Rows past 16-byte chunks: the last H % (16 / ES) elements of each row go
@@ -337,7 +338,7 @@ __device__ __forceinline__ ExpertParams tail_of(ExpertParams p, int ch) {
 
 // The elements past the last whole chunk, where there are some.
 template <int ES>
-__device__ __forceinline__ void copy_tail(const ExpertParams& tail, int t, const int* r, int count, int lane, int lanes) {
+__device__ __forceinline__ void copy_tail(const ExpertParams& tail, int t, const int* r, int count, unsigned lane, unsigned lanes) {
   typename Raw<ES>::T x[1];
   load_chunks<ES, 1>(tail, t, lane + lanes * blockIdx.y, lanes, x);
   copy_row<ES, 1>(tail, t, r, count, lane, lanes, x);
@@ -446,7 +447,7 @@ __device__ __forceinline__ void load_slots(const ExpertParams& p, int t, int j0,
 
 // acc += sum_j w_j in[r_j] over the lane's chunks from c0 on, with all KU U loads in flight.
 template <int ES, int CH, int KU, int U>
-__device__ __forceinline__ void add_rows(const ExpertParams& p, const int (&r)[KU], const float (&w)[KU], int c0, int lanes,
+__device__ __forceinline__ void add_rows(const ExpertParams& p, const int (&r)[KU], const float (&w)[KU], unsigned c0, unsigned lanes,
                                          float (&acc)[U][CH / ES]) {
   constexpr int V = CH / ES;
   typename Raw<CH>::T x[KU][U];
@@ -468,9 +469,9 @@ __device__ __forceinline__ void add_rows(const ExpertParams& p, const int (&r)[K
 
 // out[t] = sum_j w_j in[r_j].  r, w: the first KU slots.
 template <int ES, int CH, int KU, int U>
-__device__ __forceinline__ void combine_row(const ExpertParams& p, int t, const int (&r)[KU], const float (&w)[KU], int lane,
-                                            int lanes) {
-  for (int c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += lanes * U * gridDim.y) {
+__device__ __forceinline__ void combine_row(const ExpertParams& p, int t, const int (&r)[KU], const float (&w)[KU], unsigned lane,
+                                            unsigned lanes) {
+  for (unsigned c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += lanes * U * gridDim.y) {
     float acc[U][CH / ES] = {};
     add_rows<ES, CH, KU, U>(p, r, w, c0, lanes, acc);
     for (int j0 = KU; j0 < p.k; j0 += KU) {
@@ -525,10 +526,10 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(ExpertParam
 // The other kernels do not gain (combine loses 7%).
 template <int ES, int CH, int KU, int U>
 __device__ __forceinline__ void combine_back_row(const ExpertParams& p, int t, const int (&r)[KU], const float (&w)[KU],
-                                                 float (&dot)[KU], int lane, int lanes) {
+                                                 float (&dot)[KU], unsigned lane, unsigned lanes) {
   using R = typename Raw<CH>::T;
   constexpr int V = CH / ES;
-  for (int c0 = lane; c0 < p.nch; c0 += lanes * U) {
+  for (unsigned c0 = lane; c0 < p.nch; c0 += lanes * U) {
     R d[U], y[KU][U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -658,7 +659,7 @@ int chunk_bytes(int es, const void* a, long long pitch_a, const void* b, long lo
 }
 
 void set_chunks(ExpertParams* p, int es, int ch) {
-  p->nch = (int)(p->H * es / ch);
+  p->nch = (unsigned)(p->H * es / ch);
   p->tail = (int)(p->H - (long long)p->nch * ch / es);
 }
 

@@ -158,7 +158,8 @@ struct ExpertParams {
   void* out; long long out_pitch;          // rows written: Xs, out, dX or dY
   int* hist;           // chunks x E
   int chunks, chunk;   // chunks of a large sort, slots per chunk
-  int nch, tail;       // launch: chunks per row, elements after them
+  unsigned nch;        // launch: chunks per row
+  int tail;            // launch: elements after them
   int lanes;           // launch: threads per token
 };
 

@@ -127,3 +127,36 @@ def test_combine_of_the_most_tokens(weighted):
     assert equal_in_pieces(out, Y)
     del plan, slot_row, Y, out
     torch.cuda.empty_cache()
+
+
+def test_the_longest_rows():
+    """One row of nearly 2^31 elements, moved one at a time (an odd pitch) and in 16-byte chunks with a tail."""
+    if free_gigabytes() < 60:
+        pytest.skip("needs 60 GB")
+    H = (1 << 31) - 5
+    ids = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    w = torch.ones(1, 1, device="cuda")
+    X = ramp(H, torch.bfloat16, 2)                # 0 1 0 1 ..: sums of fewer than 2^24 products are exact
+    for pitch in (H, H + 5):
+        plan = g.ExpertPlan(1, 1, 1, "cuda")
+        matrix = lambda t: t.as_strided((1, H), (pitch, 1))  # noqa: E731
+        row = torch.empty(pitch, dtype=torch.bfloat16, device="cuda")
+        row[:H] = X
+        out = torch.full((pitch,), float("nan"), dtype=torch.bfloat16, device="cuda")
+        g.expert_dispatch(ids, plan, matrix(row), out=matrix(out))
+        status()
+        assert equal_in_pieces(out[:H], X) and bool(out[H:].isnan().all())
+        out.fill_(float("nan"))
+        g.expert_combine(plan, matrix(row), w, out=matrix(out))
+        status()
+        assert equal_in_pieces(out[:H], X) and bool(out[H:].isnan().all())
+        out.fill_(float("nan"))
+        _, dw = g.expert_combine_backward(plan, matrix(row), w, matrix(row), dY=matrix(out))
+        status()
+        assert equal_in_pieces(out[:H], X) and bool(out[H:].isnan().all())
+        # 256 lanes add fewer than 2^23 ones each, which is exact, then 8 + 8 rounded joins
+        ones = H // 2
+        assert abs(dw.item() - ones) <= 16 * 2.0 ** -24 * ones
+        del row, out
+    del X
+    torch.cuda.empty_cache()
