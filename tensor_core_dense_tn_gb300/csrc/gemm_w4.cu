@@ -202,7 +202,9 @@ __device__ __forceinline__ W4Item item_of(const W4Params& p, const W4Block& k, i
   return w;
 }
 
-// Lists the matrices that have rows; returns their number.
+// Lists the matrices that have rows; returns their number.  The rows of the
+// y-th are lo[y] .. lo[y + 1]: offsets[e] .. offsets[e + 1] of a plan in order,
+// and for offsets that decrease up to the next one's first, which may be none.
 __device__ int list_experts(const W4Params& p, int* lo, uint16_t* id) {
   __shared__ int warp_count[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -226,7 +228,9 @@ __device__ int list_experts(const W4Params& p, int* lo, uint16_t* id) {
       at += __popc(some & ((1u << lane) - 1));
       id[at] = (uint16_t)e;
       lo[at] = a;
-      lo[at + 1] = b;      // the next one's lo, if there is one, is the same row
+      // One writer per entry: in a caller's own plan the next one's lo may be another row than b, and the
+      // CTAs of a cluster have to come to the same list (they meet once for each block of its rows).
+      if (at + 1 == before) lo[at + 1] = b;
     }
     __syncthreads();
   }

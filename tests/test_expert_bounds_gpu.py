@@ -160,3 +160,26 @@ def test_the_longest_rows():
         del row, out
     del X
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("K,parts", [(256, 1), (2048, 8)])
+@pytest.mark.parametrize("offsets,used", [([0, 40, 8, 8, 60], [(0, 8, 0), (8, 60, 3)]),
+                                          ([30, 20, 20, 44, 60], [(20, 44, 2), (44, 60, 3)]),
+                                          ([0, 20, 60, 8, 60], [(0, 8, 0), (20, 60, 3)])])
+def test_products_of_decreasing_offsets(K, parts, offsets, used):
+    """Offsets that no dispatch makes: every part of a split product takes the same rows, an expert's up to the next
+    one's first, and nothing outside the result is written."""
+    rows, N, E = 60, 100, 4
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = g.ExpertPlan.of(torch.tensor(offsets, **i32), torch.zeros(rows, 1, **i32), torch.arange(rows, **i32))
+    codes = torch.randint(0, 256, (E, N, K // 2), device="cuda", dtype=torch.uint8)
+    A = torch.randint(-2, 3, (rows, K), device="cuda").bfloat16()
+    W = g.W4Matrix(codes, torch.ones(E, N, K // 128, device="cuda"), K=K, group=128)
+    D, whole = guarded(rows, N, torch.float32, 64)
+    g.gemm_w4_experts(A, W, plan, out=D)
+    assert g.last_launch_info()["k_parts"] == parts
+    status()
+    assert untouched(whole, 64)
+    q = torch.stack([codes & 15, codes >> 4], dim=-1).view(E, N, K).double() - 8      # whole numbers: exact sums
+    for lo, hi, e in used:       # rows of one expert alone
+        assert torch.equal(D[lo:hi].double(), A[lo:hi].double() @ q[e].T)
