@@ -205,6 +205,7 @@ __device__ __forceinline__ W4Item item_of(const W4Params& p, const W4Block& k, i
 // Lists the matrices that have rows; returns their number.  The rows of the
 // y-th are lo[y] .. lo[y + 1]: offsets[e] .. offsets[e + 1] of a plan in order,
 // and for offsets that decrease up to the next one's first, which may be none.
+// The last one's end at offsets[E], where the rows of zeros begin.
 __device__ int list_experts(const W4Params& p, int* lo, uint16_t* id) {
   __shared__ int warp_count[kThreads / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -224,13 +225,13 @@ __device__ int list_experts(const W4Params& p, int* lo, uint16_t* id) {
       if (w < warp) at += warp_count[w];
       before += warp_count[w];
     }
+    // One writer per entry: in a caller's own plan the next one's lo may be another row than b, and the
+    // CTAs of a cluster have to come to the same list (they meet once for each block of its rows).
+    if (tid == 0) lo[before] = min(max(p.offsets[p.E], 0), p.M);
     if (b > a) {
       at += __popc(some & ((1u << lane) - 1));
       id[at] = (uint16_t)e;
       lo[at] = a;
-      // One writer per entry: in a caller's own plan the next one's lo may be another row than b, and the
-      // CTAs of a cluster have to come to the same list (they meet once for each block of its rows).
-      if (at + 1 == before) lo[at + 1] = b;
     }
     __syncthreads();
   }

@@ -165,7 +165,8 @@ def test_the_longest_rows():
 @pytest.mark.parametrize("K,parts", [(256, 1), (2048, 8)])
 @pytest.mark.parametrize("offsets,used", [([0, 40, 8, 8, 60], [(0, 8, 0), (8, 60, 3)]),
                                           ([30, 20, 20, 44, 60], [(20, 44, 2), (44, 60, 3)]),
-                                          ([0, 20, 60, 8, 60], [(0, 8, 0), (20, 60, 3)])])
+                                          ([0, 20, 60, 8, 60], [(0, 8, 0), (20, 60, 3)]),
+                                          ([0, 8, 8, 50, 44], [(0, 8, 0), (8, 44, 2), (44, 60, None)])])
 def test_products_of_decreasing_offsets(K, parts, offsets, used):
     """Offsets that no dispatch makes: every part of a split product takes the same rows, an expert's up to the next
     one's first, and nothing outside the result is written."""
@@ -181,5 +182,6 @@ def test_products_of_decreasing_offsets(K, parts, offsets, used):
     status()
     assert untouched(whole, 64)
     q = torch.stack([codes & 15, codes >> 4], dim=-1).view(E, N, K).double() - 8      # whole numbers: exact sums
-    for lo, hi, e in used:       # rows of one expert alone
-        assert torch.equal(D[lo:hi].double(), A[lo:hi].double() @ q[e].T)
+    for lo, hi, e in used:       # rows of one expert alone, or past the last (which are zero)
+        want = torch.zeros(1, 1, device="cuda") if e is None else A[lo:hi].double() @ q[e].T
+        assert torch.equal(D[lo:hi].double(), want.double().expand(hi - lo, N))
