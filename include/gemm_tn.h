@@ -499,10 +499,8 @@ int gemm_bf16_tn_skinny_noalloc(int64_t M, int64_t N, int64_t K,
  * The plan's arrays are device memory owned by the caller; dispatch writes
  * them and the other calls read them, checking every row against [0, T*k).
  * All calls are asynchronous on `stream` with programmatic stream
- * serialisation, like the GEMM kernels.  Sorting more than 4096 slots uses
- * the library's workspace of the stream; where it would have to be allocated
- * or grown during stream capture, the call returns
- * GEMM_ERR_INVALID_VALUE. */
+ * serialisation, like the GEMM kernels.  They use no memory but the caller's,
+ * so any of them may be captured and replayed on any stream. */
 typedef struct gemm_expert_plan {
   int64_t tokens;      /* T; T*k below 2^31 */
   int slots;           /* k, 1..64 */

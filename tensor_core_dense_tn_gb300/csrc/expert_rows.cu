@@ -117,10 +117,10 @@ __device__ __forceinline__ void load_ids(const ExpertParams& p, int base, int hi
   }
 }
 
-// Writes the slots' rows, and the rows' tokens to row_token.
+// Writes the slots' rows, and the rows' tokens to row_token where it is given.
 template <int S>
 __device__ __forceinline__ void store_rows(const ExpertParams& p, const int (&id)[S], const int (&rank)[S], int base, int hi,
-                                           const int* start, const uint16_t* wh, int* row_token) {
+                                           const int* start, const uint16_t* wh, int* row_token = nullptr) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int q = 0; q < S; ++q) {
@@ -129,7 +129,7 @@ __device__ __forceinline__ void store_rows(const ExpertParams& p, const int (&id
     int row = -1;
     if (id[q] < p.E) {
       row = start[id[q]] + wh[warp * p.E + id[q]] + rank[q];
-      row_token[row] = s / p.k;
+      if (row_token) row_token[row] = s / p.k;
     }
     p.slot_row[s] = row;
   }
@@ -159,7 +159,8 @@ __global__ void __launch_bounds__(1024) expert_sort_kernel(ExpertParams p) {
 
 // Rows of one chunk's slots, S * blockDim.x at a time.  Every block adds up the histograms before its
 // own chunk (and all of them, for the experts' offsets), ranks its slots in
-// slot order, and writes their rows.
+// slot order, and writes their rows.  The histograms lie in row_token, which
+// other blocks may still be reading, so the next kernel fills that.
 template <int S>
 __global__ void __launch_bounds__(1024) expert_rank_kernel(ExpertParams p) {
   extern __shared__ int sm[];
@@ -193,17 +194,35 @@ __global__ void __launch_bounds__(1024) expert_rank_kernel(ExpertParams p) {
   __syncthreads();
   exclusive_scan(total, E + 1);
   for (int e = tid; e < E; e += blockDim.x) start[e] += total[e];
-  const int V = total[E];
   if (blockIdx.x == 0)
     for (int e = tid; e <= E; e += blockDim.x) p.offsets[e] = total[e];
-  for (long long r = (long long)V + blockIdx.x * blockDim.x + tid; r < p.n; r += gridDim.x * blockDim.x) p.row_token[r] = -1;
   for (int base = lo; base < hi; base += S * (int)blockDim.x) {
     if (base > lo) load_ids(p, base, hi, id);
     __syncthreads();
     rank_slots(id, rank, E, wh, total);
-    store_rows(p, id, rank, base, hi, start, wh, p.row_token);
+    store_rows(p, id, rank, base, hi, start, wh);
     __syncthreads();
     for (int e = tid; e < E; e += blockDim.x) start[e] += total[e];
+  }
+}
+
+// Number of rows that slots fill.
+__device__ __forceinline__ int rows_filled(const ExpertParams& p) { return min(max(p.offsets[p.E], 0), p.n); }
+
+// The rows' tokens, from the slots' rows (a plan of many slots without rows to copy).
+constexpr int kTokenSlots = 4;   // per thread
+__global__ void __launch_bounds__(kRowThreads) expert_token_kernel(ExpertParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int V = rows_filled(p), s0 = blockIdx.x * (kTokenSlots * kRowThreads) + threadIdx.x;   // below 2^31: n ends 4096 before
+  int r[kTokenSlots];
+#pragma unroll
+  for (int q = 0; q < kTokenSlots; ++q) r[q] = s0 + q * kRowThreads < p.n ? p.slot_row[s0 + q * kRowThreads] : -1;
+#pragma unroll
+  for (int q = 0; q < kTokenSlots; ++q) {
+    const int s = s0 + q * kRowThreads;
+    if (r[q] >= 0 && r[q] < p.n) p.row_token[r[q]] = s / p.k;
+    if (s >= V && s < p.n) p.row_token[s] = -1;
   }
 }
 
@@ -357,16 +376,19 @@ __global__ void __launch_bounds__(kRowThreads) expert_gather_kernel(ExpertParams
   if (t < p.T) load_chunks<CH, U>(p, t, lane + lanes * U * blockIdx.y, lanes, x);
   griddep_wait();
   griddep_launch_dependents();
+  const bool fill = p.tokens_left && blockIdx.y == 0;
   for (int i = threadIdx.x; i < per * p.k; i += kRowThreads) {
     const int t = t0 + i / p.k;
     rows[i] = t < p.T ? load_row(p, t, i % p.k) : -1;
+    if (fill && rows[i] >= 0) p.row_token[rows[i]] = t;
   }
-  const int V = p.offsets[p.E];
+  const int V = rows_filled(p);
   __syncthreads();
   if (t >= p.T) return;
   copy_row<CH, U>(p, t, rows + group * p.k, p.k, lane, lanes, x);
   if (p.tail) copy_tail<ES>(tail_of<ES>(p, CH), t, rows + group * p.k, p.k, lane, lanes);
   for (long long r = (long long)V + t; r < p.n; r += p.T) {
+    if (fill && lane == 0) p.row_token[r] = -1;
     zero_row<CH>(p, r, lane, lanes);
     if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
   }
@@ -607,7 +629,7 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_back_kernel(Expert
     }
   }
   if (p.out && t < p.T) {
-    const int V = min(max(p.offsets[p.E], 0), p.n);   // a caller's own plan may hold anything
+    const int V = rows_filled(p);
     for (long long r = (long long)V + t; r < p.n; r += p.T) {
       zero_row<CH>(p, r, lane, lanes);
       if (p.tail) zero_row<ES>(tail_of<ES>(p, CH), r, lane, lanes);
@@ -671,16 +693,19 @@ const void* kernel_of(int es, int ch) {
 
 }  // namespace
 
+namespace {
+
 // Chunks of 1024, 2048 or 4096 slots, at most 64 where that can be: every
 // block of the ranking adds up all of them.  (131072 slots of 256 experts in
 // 128 / 64 / 32 chunks: 11.8 / 9.6 / 12.0 us; 262144 in 128 / 64: 15.4 / 12.7.)
-int expert_chunks(long long n) {
+// Their histograms have to fit n integers.
+int expert_chunks(long long n, int experts) {
   const int per = n <= 65536 ? 1024 : (n <= 131072 ? 2048 : 4096);
-  const long long c = (n + per - 1) / per;
-  return (int)(c < 1 ? 1 : (c > kExpertMaxChunks ? kExpertMaxChunks : c));
+  long long c = (n + per - 1) / per;
+  if (c > kExpertMaxChunks) c = kExpertMaxChunks;
+  if (c > n / experts) c = n / experts;
+  return (int)c;
 }
-
-namespace {
 
 // 8192 rows of 1002 bf16, one slot each: 15.2 / 12.6 us with 4 / 8 chunks of 4
 // bytes; of 1001, 24.3 / 23.6 / 18.8 us with 2 / 4 / 8 elements.
@@ -735,14 +760,20 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
     info->grid = 1; info->cluster = 1; info->block = 1024; info->smem_bytes = (int)bytes;
     info->kernel = "expert_sort_kernel";
   } else {
-    p.chunks = expert_chunks(p.n);
+    p.chunks = expert_chunks(p.n, p.E);
+    p.hist = p.row_token;
+    p.tokens_left = 1;
     p.chunk = (int)(((long long)p.n + p.chunks - 1) / p.chunks);
     if ((e = launch((const void*)expert_hist_kernel, dim3(p.chunks), 1024, (size_t)p.E * sizeof(int), stream, p))) return e;
     if ((e = launch(ranks[p.chunk <= 1024 ? 0 : (p.chunk <= 2048 ? 1 : 2)], dim3(p.chunks), 1024, rank_bytes(p.E), stream, p))) return e;
     info->grid = p.chunks; info->cluster = 1; info->block = 1024; info->smem_bytes = (int)rank_bytes(p.E);
     info->kernel = "expert_rank_kernel";
   }
-  if (p.H == 0) return cudaSuccess;
+  if (p.H == 0 && !p.tokens_left) return cudaSuccess;
+  if (p.H == 0) {
+    const int per = kTokenSlots * kRowThreads;
+    return launch((const void*)expert_token_kernel, dim3((p.n + per - 1) / per), kRowThreads, 0, stream, p);
+  }
   const dim3 grid = row_grid(p, U, sms);
   const size_t smem = (size_t)(kRowThreads / p.lanes) * p.k * sizeof(int);
   const void* f = kernel_of<Gather>(es, ch);

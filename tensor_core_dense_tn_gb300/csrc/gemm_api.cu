@@ -857,11 +857,6 @@ int run_expert_dispatch(const gemm_expert_plan* plan, const void* ids, int64_t l
   DeviceState* st = nullptr;
   if ((rc = init_device(&dev, &st))) return rc;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-  if (p.n > kExpertOneBlock) {
-    Workspace* w = nullptr;
-    if ((rc = get_workspace(dev, stream, (size_t)expert_chunks(p.n) * p.E, 0, &w))) return rc;
-    p.hist = reinterpret_cast<int*>(w->partials);
-  }
   LaunchInfo li = {};
   return finish_launch(launch_expert_dispatch(p, es, st->sms, stream, &li), li);
 }

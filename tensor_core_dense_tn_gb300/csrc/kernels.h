@@ -156,16 +156,16 @@ struct ExpertParams {
   const void* in; long long in_pitch;      // rows read (bytes): X, Y or dout
   const void* in2; long long in2_pitch;    // combine backward: Y
   void* out; long long out_pitch;          // rows written: Xs, out, dX or dY
-  int* hist;           // chunks x E
-  int chunks, chunk;   // chunks of a large sort, slots per chunk
+  int* hist;           // launch: chunks x E, in row_token until that is written
+  int chunks, chunk;   // launch: chunks of a large sort, slots per chunk
+  int tokens_left;     // launch: row_token is written after the ranks
   unsigned nch;        // launch: chunks per row
   int tail;            // launch: elements after them
   int lanes;           // launch: threads per token
 };
 
 struct LaunchInfo;
-// es: bytes per element (2 = bf16, 4 = fp32).  p.hist is needed where p.n > kExpertOneBlock.
-int expert_chunks(long long n);
+// es: bytes per element (2 = bf16, 4 = fp32).
 cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info);
 cudaError_t launch_expert_combine(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info);
 cudaError_t launch_expert_combine_back(ExpertParams p, int es, int sms, cudaStream_t stream, LaunchInfo* info);

@@ -185,3 +185,75 @@ def test_products_of_decreasing_offsets(K, parts, offsets, used):
     for lo, hi, e in used:       # rows of one expert alone, or past the last (which are zero)
         want = torch.zeros(1, 1, device="cuda") if e is None else A[lo:hi].double() @ q[e].T
         assert torch.equal(D[lo:hi].double(), want.double().expand(hi - lo, N))
+
+
+def sorted_plan(ids, E):
+    key = ids.reshape(-1).long()
+    order = torch.sort(key, stable=True).indices
+    slot_row = torch.empty_like(order)
+    slot_row[order] = torch.arange(key.numel(), device="cuda")
+    offsets = torch.searchsorted(key[order], torch.arange(E + 1, device="cuda"))
+    return offsets.int(), slot_row.int().view(ids.shape), (order // ids.shape[1]).int()
+
+
+def holds(plan, want):
+    return all(torch.equal(a, b) for a, b in zip((plan.offsets, plan.slot_row, plan.row_token), want))
+
+
+@pytest.mark.parametrize("with_rows", [False, True])
+def test_a_captured_sort_owns_its_memory(with_rows):
+    """A dispatch of many slots captured on a stream that has seen none, replayed on another stream while larger ones
+    run on the first: every plan comes out right, so the two share nothing."""
+    T, k, E, H = 40000, 2, 61, 24
+    ids = torch.randint(0, E, (T, k), device="cuda")
+    X = torch.randn(T, H, device="cuda") if with_rows else None
+    more = torch.randint(0, 1024, (500000, 4), device="cuda", dtype=torch.int32)
+    plan, larger = g.ExpertPlan(T, k, E, "cuda"), g.ExpertPlan(500000, 4, 1024, "cuda")
+    out = torch.empty(T * k, H, device="cuda") if with_rows else None
+    want, want_larger = sorted_plan(ids, E), sorted_plan(more, 1024)
+    torch.cuda.synchronize()
+    captured, replayed = torch.cuda.Stream(), torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=captured):
+        g.expert_dispatch(ids, plan, X, out=out)
+    for _ in range(5):
+        for t in (plan.offsets, plan.slot_row, plan.row_token, larger.offsets, larger.slot_row, larger.row_token):
+            t.fill_(-99)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(captured):
+            for _ in range(4):
+                g.expert_dispatch(more, larger)
+        with torch.cuda.stream(replayed):
+            for _ in range(8):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert holds(plan, want) and holds(larger, want_larger)
+        if with_rows:
+            assert torch.equal(out, X[want[2].long()])
+    status()
+
+
+@pytest.mark.parametrize("T,k,E", [(4097, 1, 1024), (5000, 1, 1024), (1366, 3, 1000), (70000, 9, 1024), (66000, 1, 7)])
+@pytest.mark.parametrize("H", [0, 8])
+def test_histograms_fit_the_plan(T, k, E, H):
+    """Sorts whose histograms are nearly as large as the plan's arrays, with and without rows; dropped slots."""
+    ids = torch.randint(-E // 4, E, (T, k), device="cuda")
+    whole = torch.full((E + 1 + 2 * T * k + 128,), -99, dtype=torch.int32, device="cuda")
+    n = T * k
+    parts = whole[32:32 + n].view(T, k), whole[64 + n:64 + 2 * n], whole[96 + 2 * n:97 + 2 * n + E]
+    plan = g.ExpertPlan.of(parts[2], parts[0], parts[1])
+    X = torch.randn(T, H, device="cuda")
+    Xs = g.expert_dispatch(ids, plan, X if H else None)
+    status()
+    key = torch.where(ids < 0, torch.full_like(ids, E), ids).reshape(-1)
+    by, order = torch.sort(key, stable=True)
+    V = int((by < E).sum())
+    assert torch.equal(plan.offsets.long(), torch.searchsorted(by, torch.arange(E + 1, device="cuda")))
+    assert torch.equal(plan.row_token[:V].long(), order[:V] // k) and bool((plan.row_token[V:] == -1).all())
+    rows = torch.full((n,), -1, device="cuda")
+    rows[order[:V]] = torch.arange(V, device="cuda")
+    assert torch.equal(plan.slot_row.view(-1).long(), rows)
+    for lo, hi in ((0, 32), (32 + n, 64 + n), (64 + 2 * n, 96 + 2 * n), (97 + 2 * n + E, len(whole))):
+        assert bool((whole[lo:hi] == -99).all())
+    if H:
+        assert torch.equal(Xs[:V], X[order[:V] // k]) and bool((Xs[V:] == 0).all())
