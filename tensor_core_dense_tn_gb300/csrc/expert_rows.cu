@@ -41,7 +41,9 @@ __global__ void __launch_bounds__(1024) expert_hist_kernel(ExpertParams p) {
   extern __shared__ int h[];
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) h[e] = 0;
   griddep_wait();
-  griddep_launch_dependents();
+  // More blocks than this hold so many SMs that the ranking's, let in now, settle
+  // two on one: 500000 x 4 slots of 1024 experts 87 us, 65 if they come at the end.
+  if (gridDim.x <= 64) griddep_launch_dependents();
   __syncthreads();
   const int lo = blockIdx.x * p.chunk, hi = min(p.n, lo + p.chunk);
   for (int s = lo + threadIdx.x; s < hi; s += blockDim.x) {
@@ -771,6 +773,7 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
   }
   if (p.H == 0 && !p.tokens_left) return cudaSuccess;
   if (p.H == 0) {
+    // 8192 x 8 slots of 128 experts: 7.6 us with this launch, 65536 x 4 of 256: 13.5.
     const int per = kTokenSlots * kRowThreads;
     return launch((const void*)expert_token_kernel, dim3((p.n + per - 1) / per), kRowThreads, 0, stream, p);
   }
