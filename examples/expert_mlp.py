@@ -42,16 +42,18 @@ def grouped(A, bounds, B):
 
 
 class Dispatch(torch.autograd.Function):
-    """The tokens' rows in expert order; fills the plan."""
+    """The tokens' rows in expert order; fills the plan.  Its arrays are saved, so that autograd raises where the
+    plan was filled again before the gradients were taken."""
 
     @staticmethod
     def forward(ctx, X, ids, plan):
-        ctx.plan = plan
-        return g.expert_dispatch(ids, plan, X)
+        rows = g.expert_dispatch(ids, plan, X)
+        ctx.save_for_backward(plan.offsets, plan.slot_row, plan.row_token)
+        return rows
 
     @staticmethod
     def backward(ctx, dXs):
-        return g.expert_dispatch_backward(ctx.plan, dXs.contiguous()), None, None
+        return g.expert_dispatch_backward(g.ExpertPlan.of(*ctx.saved_tensors), dXs.contiguous()), None, None
 
 
 class Combine(torch.autograd.Function):
@@ -59,13 +61,13 @@ class Combine(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, Y, weights, plan):
-        ctx.plan = plan
-        ctx.save_for_backward(Y, weights)
+        ctx.save_for_backward(Y, weights, plan.offsets, plan.slot_row, plan.row_token)
         return g.expert_combine(plan, Y, weights)
 
     @staticmethod
     def backward(ctx, dout):
-        dY, dweights = g.expert_combine_backward(ctx.plan, *ctx.saved_tensors, dout.contiguous())
+        Y, weights, *arrays = ctx.saved_tensors
+        dY, dweights = g.expert_combine_backward(g.ExpertPlan.of(*arrays), Y, weights, dout.contiguous())
         return dY, dweights, None
 
 

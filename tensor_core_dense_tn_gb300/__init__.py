@@ -425,13 +425,18 @@ def _stream_of(t):
 class ExpertPlan:
     """A dispatch plan: int32 CUDA tensors offsets (E + 1), slot_row (T, k) and
     row_token (T * k), filled by expert_dispatch() and read by the other calls.
-    A program keeps one per shape and fills it again at every step."""
+    A serving program keeps one per shape and fills it again at every step; for
+    training every layer of every step needs its own until its gradients are
+    taken, which read the same arrays.  Filling a plan counts as an in-place
+    change of them, so a backward pass that saved them for autograd and finds
+    them filled again raises."""
 
     def __init__(self, tokens: int, slots: int, experts: int, device):
         torch = _t()
         buf = torch.empty(experts + 1 + 2 * tokens * slots, dtype=torch.int32, device=device)
         n = tokens * slots
         self._set(buf[2 * n:], buf[:n].view(tokens, slots), buf[n:2 * n], experts)
+        self._versioned = self._versioned[:1]       # views of one tensor share its version
 
     @classmethod
     def of(cls, offsets, slot_row, row_token, experts: int | None = None):
@@ -451,6 +456,7 @@ class ExpertPlan:
         if offsets.get_device() != self.gpu or row_token.get_device() != self.gpu:
             raise ValueError("the arrays of a plan must be on one device")
         self.offsets, self.slot_row, self.row_token = offsets, slot_row, row_token
+        self._versioned = tuple(t for t in (offsets, slot_row, row_token) if not t.is_inference())
         self.tokens, self.slots = slot_row.shape
         self.experts, self.rows = experts, slot_row.numel()
         self.info = ExpertPlanInfo(self.tokens, self.slots, experts, offsets.data_ptr(), slot_row.data_ptr(),
@@ -494,7 +500,9 @@ class W4Matrix:
 def expert_dispatch(ids, plan: ExpertPlan, X=None, out=None, stream=None):
     """Fills `plan` from ids (tokens, slots), int32 or int64 with ids outside
     [0, experts) dropped, and returns X's rows in expert order (None without X):
-    Xs[plan.slot_row[t, j]] = X[t], zeros past plan.offsets[experts]."""
+    Xs[plan.slot_row[t, j]] = X[t], zeros past plan.offsets[experts].  Like every
+    call here it returns a tensor without an autograd graph; the gradient is
+    expert_dispatch_backward()."""
     torch = _torch or _t()
     wide = ids.dtype == torch.int64
     if not wide and ids.dtype != torch.int32:
@@ -516,6 +524,7 @@ def expert_dispatch(ids, plan: ExpertPlan, X=None, out=None, stream=None):
                                                _stream_of(ids) if stream is None else stream or None)
     if rc:
         _check(rc)
+    torch.autograd.graph.increment_version(plan._versioned)
     return out if X is not None else None
 
 
@@ -525,7 +534,8 @@ def expert_dispatch_backward(plan: ExpertPlan, dXs, out=None, stream=None):
 
 
 def expert_combine(plan: ExpertPlan, Y, weights, out=None, stream=None):
-    """out[t] = sum_j weights[t, j] * Y[slot_row[t, j]] (weights: (tokens, slots) bf16 or fp32)."""
+    """out[t] = sum_j weights[t, j] * Y[slot_row[t, j]] (weights: (tokens, slots) bf16 or fp32); without an
+    autograd graph, the gradients are expert_combine_backward()."""
     return _combine(plan, Y, weights, out, stream)
 
 

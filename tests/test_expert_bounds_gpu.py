@@ -257,3 +257,24 @@ def test_histograms_fit_the_plan(T, k, E, H):
         assert bool((whole[lo:hi] == -99).all())
     if H:
         assert torch.equal(Xs[:V], X[order[:V] // k]) and bool((Xs[V:] == 0).all())
+
+
+def test_gradients_of_a_plan_filled_again_raise():
+    """Two layers with one plan, forward twice before backward: the first layer's gradients would be wrong."""
+    from test_expert_example import example, setup
+    ex = example()
+    T, k, E, H = 20, 2, 4, 64
+    _, _, _, x, dout = setup(T, k, E, H, 32)
+    x.requires_grad_()
+    plan, w = g.ExpertPlan(T, k, E, "cuda"), torch.rand(T, k, device="cuda", requires_grad=True)
+    ids = [torch.randint(0, E, (T, k), device="cuda") for _ in range(2)]
+    rows = ex.Dispatch.apply(x, ids[0], plan)
+    y = ex.Combine.apply(rows, w, plan)
+    y.backward(dout, retain_graph=True)
+    want = 0.5 * x.grad
+    g.expert_dispatch(ids[1], plan)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward(dout)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        rows.backward(torch.ones_like(rows))
+    assert torch.equal(0.5 * x.grad, want)

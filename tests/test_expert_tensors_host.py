@@ -188,3 +188,27 @@ def test_parts_of_a_plan_or_a_matrix_on_different_gpus_are_refused():
     for parts in ((elsewhere(codes), scales, points), (codes, elsewhere(scales), points), (codes, scales, elsewhere(points))):
         with pytest.raises(ValueError):
             g.W4Matrix(*parts, K=KW, group=64)
+
+
+@pytest.mark.parametrize("apart", [True, False])
+def test_filling_a_plan_counts_as_changing_its_arrays(lib, apart):
+    """The library writes them through their addresses, which autograd does not see."""
+    p = make_plan()
+    if not apart:
+        p = g.ExpertPlan(T, K, E, "cpu")
+        p.gpu = 0
+    before = [t._version for t in (p.offsets, p.slot_row, p.row_token)]
+    CALLS["dispatch"][0](p, operands("dispatch"))
+    assert all(t._version > v for t, v in zip((p.offsets, p.slot_row, p.row_token), before))
+    after = [t._version for t in (p.offsets, p.slot_row, p.row_token)]
+    for name in PLANNED[1:]:
+        CALLS[name][0](p, operands(name))
+    assert [t._version for t in (p.offsets, p.slot_row, p.row_token)] == after
+
+
+def test_plans_of_inference_mode_can_be_filled_outside_it(lib):
+    with torch.inference_mode():
+        p = make_plan()
+        CALLS["dispatch"][0](p, operands("dispatch"))
+    CALLS["dispatch"][0](p, operands("dispatch"))
+    assert len(lib.calls) == 2
