@@ -39,7 +39,11 @@
  * grown) on the first call for a (device, stream) pair that needs them and
  * kept until gemm_shutdown().  A skinny call that would allocate or grow it
  * during stream capture returns an error; a tiled call runs unsplit
- * instead.  Calls on different streams use different workspaces.
+ * instead.  Calls on different streams use different workspaces.  A graph
+ * keeps the workspace of the stream that its calls were captured on, also
+ * after a later call made that stream a larger one, until gemm_shutdown().
+ * So replays of graphs captured on one stream, and other calls on that
+ * stream, must not overlap, whatever streams the graphs are launched on.
  *
  * Launch: kernels are launched with programmatic stream serialisation, so
  * their set-up (barrier initialisation, Tensor Memory allocation) may overlap

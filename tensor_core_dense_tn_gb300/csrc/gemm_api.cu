@@ -20,6 +20,7 @@
 #include <mutex>
 #include <string>
 #include <utility>
+#include <vector>
 
 #include "../../include/gemm_tn.h"
 #include "kernels.h"
@@ -63,8 +64,10 @@ struct Workspace {
   size_t partial_floats = 0;
   int* counters = nullptr;
   size_t counter_ints = 0;
+  bool captured = false;   // a captured call holds its addresses
 };
 std::map<std::pair<int, uintptr_t>, Workspace> g_ws;
+std::vector<std::pair<int, Workspace>> g_kept;   // device, buffers that were replaced but may be replayed into
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -159,9 +162,9 @@ int get_workspace(int dev, cudaStream_t stream, size_t partial_floats, size_t co
   std::lock_guard<std::mutex> lk(g_mu);
   *out = nullptr;
   Workspace& w = g_ws[{dev, reinterpret_cast<uintptr_t>(stream)}];
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  cudaStreamIsCapturing(stream, &cs);
   if (w.partial_floats < partial_floats || w.counter_ints < counter_ints) {
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    cudaStreamIsCapturing(stream, &cs);
     if (cs != cudaStreamCaptureStatusNone) {
       if (optional) return GEMM_OK;
       return fail(GEMM_ERR_INVALID_VALUE, "split-K workspace must be created outside stream capture");
@@ -169,8 +172,12 @@ int get_workspace(int dev, cudaStream_t stream, size_t partial_floats, size_t co
     // Work already queued may still use the old buffers.
     cudaError_t e = cudaStreamSynchronize(stream);
     if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaStreamSynchronize: %s", cudaGetErrorString(e));
-    if (w.partials) cudaFree(w.partials);
-    if (w.counters) cudaFree(w.counters);
+    if (w.captured) {
+      g_kept.push_back({dev, w});
+    } else {
+      if (w.partials) cudaFree(w.partials);
+      if (w.counters) cudaFree(w.counters);
+    }
     w = Workspace{};
     size_t pf = partial_floats < (1u << 16) ? (1u << 16) : partial_floats;
     size_t ci = counter_ints < 4096 ? 4096 : counter_ints;
@@ -188,6 +195,7 @@ int get_workspace(int dev, cudaStream_t stream, size_t partial_floats, size_t co
     w.partial_floats = pf;
     w.counter_ints = ci;
   }
+  if (cs != cudaStreamCaptureStatusNone) w.captured = true;
   *out = &w;
   return GEMM_OK;
 }
@@ -1224,6 +1232,8 @@ int gemm_get_status(void* stream) {
     for (auto& kv : g_ws)
       if (kv.first.first == dev && kv.second.counters)
         cudaMemset(kv.second.counters, 0, kv.second.counter_ints * sizeof(int));
+    for (auto& kept : g_kept)
+      if (kept.first == dev) cudaMemset(kept.second.counters, 0, kept.second.counter_ints * sizeof(int));
   }
   cudaDeviceSynchronize();
   t_last_detail = h[1];
@@ -1251,6 +1261,12 @@ void gemm_shutdown(void) {
     if (kv.second.counters) cudaFree(kv.second.counters);
   }
   g_ws.clear();
+  for (auto& kept : g_kept) {
+    cudaSetDevice(kept.first);
+    cudaFree(kept.second.partials);
+    cudaFree(kept.second.counters);
+  }
+  g_kept.clear();
   cudaSetDevice(cur);
 }
 
