@@ -491,14 +491,14 @@ __device__ __forceinline__ void add_rows(const ExpertParams& p, const int (&r)[K
     }
 }
 
-// out[t] = sum_j w_j in[r_j].  r, w: the first KU slots.
-template <int ES, int CH, int KU, int U>
+// out[t] = sum_j w_j in[r_j].  AHEAD: r, w hold the first KU slots.
+template <int ES, int CH, int KU, int U, bool AHEAD>
 __device__ __forceinline__ void combine_row(const ExpertParams& p, int t, const int (&r)[KU], const float (&w)[KU], unsigned lane,
                                             unsigned lanes) {
   for (unsigned c0 = lane + lanes * U * blockIdx.y; c0 < p.nch; c0 += lanes * U * gridDim.y) {
     float acc[U][CH / ES] = {};
-    add_rows<ES, CH, KU, U>(p, r, w, c0, lanes, acc);
-    for (int j0 = KU; j0 < p.k; j0 += KU) {
+    if constexpr (AHEAD) add_rows<ES, CH, KU, U>(p, r, w, c0, lanes, acc);
+    for (int j0 = AHEAD ? KU : 0; j0 < p.k; j0 += KU) {
       int more[KU];
       float weight[KU];
       load_slots<KU>(p, t, j0, more, weight);
@@ -516,7 +516,13 @@ __device__ __forceinline__ void combine_row(const ExpertParams& p, int t, const 
 // with the next token's rows and weights loaded ahead.  8192 rows of 4096
 // bf16: one slot 24.0 us against 24.9 with a block per token, two slots 32.8
 // against 36.9.  More slots lose by it (4096 tokens of four: 36.2 against 28.6).
-template <int KU> constexpr bool kWalk = KU <= 2;
+// bf16 in smaller chunks loses by all of it, so its slots are loaded inside the
+// walk along the row, a block per token: rows of 1001 with one, two, four and
+// eight slots 14.9 / 31.0 / 24.7 / 23.9 us against 26.1 / 45.4 / 34.8 / 43.5, of
+// 1002 8.7 / 14.4 / 12.2 / 10.5 against 9.2 / 14.5 / 13.9 / 12.5.  (Rows of 1001
+// fp32 at two slots: 30.6 inside, 22.1 ahead, the others alike.)
+template <int ES, int CH> constexpr bool kAhead = CH == 16 || ES == 4;
+template <int ES, int CH, int KU> constexpr bool kWalk = kAhead<ES, CH> && KU <= 2;
 
 template <int ES, int CH, int KU, int U>
 __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(ExpertParams p) {
@@ -526,15 +532,15 @@ __global__ void __launch_bounds__(kRowThreads) expert_combine_kernel(ExpertParam
   int t = blockIdx.x * per + threadIdx.x / lanes;
   int r[KU];
   float w[KU];
-  load_slots<KU>(p, t, 0, r, w);
+  if constexpr (kAhead<ES, CH>) load_slots<KU>(p, t, 0, r, w);
   while (t < p.T) {
     int next_r[KU];
     float next_w[KU];
     const int step = gridDim.x * per, next = p.T - t > step ? t + step : p.T;   // t + step may pass 2^31
-    if constexpr (kWalk<KU>) load_slots<KU>(p, next, 0, next_r, next_w);
-    combine_row<ES, CH, KU, U>(p, t, r, w, lane, lanes);
-    if (p.tail) combine_row<ES, ES, KU, 1>(tail_of<ES>(p, CH), t, r, w, lane, lanes);
-    if constexpr (!kWalk<KU>) break;
+    if constexpr (kWalk<ES, CH, KU>) load_slots<KU>(p, next, 0, next_r, next_w);
+    combine_row<ES, CH, KU, U, kAhead<ES, CH>>(p, t, r, w, lane, lanes);
+    if (p.tail) combine_row<ES, ES, KU, 1, kAhead<ES, CH>>(tail_of<ES>(p, CH), t, r, w, lane, lanes);
+    if constexpr (!kWalk<ES, CH, KU>) break;
     t = next;
 #pragma unroll
     for (int j = 0; j < KU; ++j) {
@@ -829,13 +835,13 @@ cudaError_t launch_expert_combine(ExpertParams p, int es, int sms, cudaStream_t 
                   : ku == 2 ? kernel_of<ForSlots<2>::Combine>(es, ch)
                   : ku == 4 ? kernel_of<ForSlots<4>::Combine>(es, ch)
                             : kernel_of<ForSlots<8>::Combine>(es, ch);
-  if (ku <= 2) {
-    static int resident[64][2][5] = {};   // blocks per SM by slots and chunk
+  if (ku <= 2 && (ch == 16 || es == 4)) {
+    static int resident[64][2][3] = {};   // blocks per SM by slots and chunk
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    int& blocks = resident[dev][ku - 1][es == 4 ? (ch == 16 ? 0 : 1) : (ch == 16 ? 2 : (ch == 4 ? 3 : 4))];
+    int& blocks = resident[dev][ku - 1][es == 2 ? 0 : (ch == 16 ? 1 : 2)];
     if (blocks == 0) {
       int got = 0;
       if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&got, f, kRowThreads, 0))) return e;

@@ -110,21 +110,22 @@ def test_plan_of_the_most_slots():
     torch.cuda.empty_cache()
 
 
-@pytest.mark.parametrize("weighted", [False, True])
-def test_combine_of_the_most_tokens(weighted):
-    """The blocks that walk over the tokens stop at the last one, also where the next step passes 2^31."""
-    if free_gigabytes() < 60:
-        pytest.skip("needs 60 GB")
+@pytest.mark.parametrize("H,weighted", [(1, False), (1, True), (8, False), (8, True)])
+def test_combine_of_the_most_tokens(H, weighted):
+    """The blocks that walk over the tokens (of rows in 16-byte chunks) stop at the last one, also where the next step
+    passes 2^31."""
+    if free_gigabytes() < 50 + 10 * H:
+        pytest.skip("needs 60 or 130 GB")
     T = (1 << 31) - 4097
     slot_row = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1)
     plan = g.ExpertPlan.of(torch.tensor([0, T], dtype=torch.int32, device="cuda"), slot_row, slot_row.view(-1))
-    Y = ramp(T, torch.bfloat16).view(T, 1)
+    Y = ramp(T * H, torch.bfloat16).view(T, H)
     if weighted:
         out = g.expert_combine(plan, Y, torch.ones(T, 1, dtype=torch.bfloat16, device="cuda"))
     else:
         out = g.expert_dispatch_backward(plan, Y)
     status()
-    assert equal_in_pieces(out, Y)
+    assert equal_in_pieces(out, Y, 1 << 26)
     del plan, slot_row, Y, out
     torch.cuda.empty_cache()
 
