@@ -48,6 +48,8 @@ class Recorder:
 def lib(monkeypatch):
     recorder = Recorder()
     monkeypatch.setattr(g, "_lib", recorder)
+    g._t()
+    monkeypatch.setattr(g, "_several_gpus", True)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     return recorder
 
@@ -159,6 +161,20 @@ def test_an_operand_elsewhere_is_refused(lib, name, what, how):
     with pytest.raises(ValueError):
         CALLS[name][0](make_plan(), operands(name, **{what: how(zeros(rows, width, dtype=dtype))}))
     assert lib.calls == []
+
+
+def test_host_memory_is_refused_where_there_is_one_gpu(lib, monkeypatch):
+    monkeypatch.setattr(g, "_several_gpus", False)
+    for name in PLANNED:
+        with pytest.raises(ValueError):
+            CALLS[name][0](moved_plan(in_host_memory), operands(name))
+    for name, what in OPERANDS:
+        rows, width, dtype = shape_of(name, what)
+        with pytest.raises(ValueError):
+            CALLS[name][0](make_plan(), operands(name, **{what: in_host_memory(zeros(rows, width, dtype=dtype))}))
+    assert lib.calls == []
+    CALLS["combine"][0](make_plan(), operands("combine"))
+    assert len(lib.calls) == 1
 
 
 def test_a_matrix_elsewhere_is_refused(lib):
