@@ -49,9 +49,12 @@
  * their set-up (barrier initialisation, Tensor Memory allocation) may overlap
  * the tail of the previous kernel on the stream.  Each kernel waits for the
  * previous kernel's completion (griddepcontrol.wait) before its first global
- * memory access, so stream order is preserved for inputs and outputs.  The
- * one exception is opt-in: with gemm_tn_config.b_static the skinny kernel
- * loads its first ring of B before that wait.
+ * memory access, so stream order is preserved for inputs and outputs.  Two
+ * kernels load earlier.  With gemm_tn_config.b_static (opt-in) the skinny
+ * kernel loads its first ring of B before that wait.  In gemm_expert_dispatch
+ * the second and third kernel of a call load ids and rows of X before theirs:
+ * the call's first kernel has waited for whatever wrote those, and it lets the
+ * next one in only then.
  *
  * Thread safety: calls may come from several host threads; the last-error
  * string is per thread.
@@ -501,7 +504,11 @@ int gemm_bf16_tn_skinny_noalloc(int64_t M, int64_t N, int64_t K,
  * same from run to run.
  *
  * The plan's arrays are device memory owned by the caller; dispatch writes
- * them and the other calls read them, checking every row against [0, T*k).
+ * them (row_token holds its histograms meanwhile) and the other calls read
+ * them, checking every row, token and offset against its range: with arrays
+ * that no dispatch filled, results are unspecified, but nothing outside the
+ * matrices is read or written.  The gradients read the plan of their forward
+ * call, so a plan that is filled again before them gives wrong ones.
  * All calls are asynchronous on `stream` with programmatic stream
  * serialisation, like the GEMM kernels.  They use no memory but the caller's,
  * so any of them may be captured and replayed on any stream. */
@@ -578,10 +585,10 @@ typedef struct gemm_w4_matrix {
  * multiple of 8); D is aligned to its element size, ldd >= N.  activation is
  * a gemm_activation.  The differences q - zero are exact in the tensor-core
  * product, and the scales multiply fp32 sums of a group: the weights are not
- * rounded.  Any M is computed; the weights are read once for every 16 tokens,
- * so the call is meant for decode batches and for larger M a bf16 GEMM is
- * the faster choice.  M or N = 0 returns GEMM_OK with no launch; K = 0 gives
- * act(0). */
+ * rounded.  Any M is computed, but the weights are read and unpacked again for
+ * every 16 tokens: the call is meant for decode batches, and for hundreds of
+ * tokens a bf16 GEMM on unpacked weights is faster where there is room for
+ * them.  M or N = 0 returns GEMM_OK with no launch; K = 0 gives act(0). */
 int gemm_w4_tn(int64_t M, const void *A, int64_t lda, const gemm_w4_matrix *W, void *D, int64_t ldd,
                float alpha, int out_dtype, int activation, void *stream);
 

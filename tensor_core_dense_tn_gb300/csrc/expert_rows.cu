@@ -9,7 +9,8 @@
 //
 // All of them are bound by memory.  Every kernel works token by token, so
 // that the token's row is read (or written) once and only the k expert rows
-// move per slot; walking the expert rows instead would read X k times.  Sums
+// move per slot; walking the expert rows instead would read X k times.  (The
+// combine's gradient reads dout's row once for every eight slots.)  Sums
 // run over j in order in fp32 and are rounded once, with no atomics on data,
 // so results do not change from run to run.  Rows that no slot fills (dropped
 // slots) are set to zero by the token loop, T rows apart.
@@ -705,7 +706,7 @@ namespace {
 
 // Chunks of 1024, 2048 or 4096 slots, at most 64 where that can be: every
 // block of the ranking adds up all of them.  (131072 slots of 256 experts in
-// 128 / 64 / 32 chunks: 11.8 / 9.6 / 12.0 us; 262144 in 128 / 64: 15.4 / 12.7.)
+// 128 / 64 / 32 chunks: 11.8 / 10.4 / 12.2 us; 262144 in 128 / 64: 14.1 / 13.9.)
 // Their histograms have to fit n integers.
 int expert_chunks(long long n, int experts) {
   const int per = n <= 65536 ? 1024 : (n <= 131072 ? 2048 : 4096);
@@ -793,22 +794,22 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
 
 namespace {
 
-// Chunks per lane in flight, for KU slots at once.  Measured in us, a block per
-// token and each slot's row loaded where it is used, with rows
-// of 4096 bf16 in 16-byte chunks and rows of 1002 bf16 in 4-byte ones, 8192
-// tokens of one and two slots, 4096 of four, 2048 of eight:
-//                    16-byte, U = 1 / 2 / 4     4-byte, U = 1 / 2 / 4 / 8
-//   combine, KU = 1   29.5 / 27.0 / 24.9         - / - / 9.5 / 6.6
-//            KU = 2   36.4 / 36.9 / 39.4         - / 17.2 / 13.2 / -
-//            KU = 4   28.6 / 36.5 / -           15.1 / 11.4 / - / -
-//            KU = 8   26.0 / - / -              11.9 / 10.3 / - / -
-//   gradient KU = 1   35.7 / 33.3 / -            - / - / 13.3 / 12.3
-//            KU = 2   54.5 / 52.8 / -            - / - / 18.3 / 16.0
-//            KU = 4   46.9 / - / -               - / 18.9 / 15.3 / -
-//            KU = 8   47.3 / - / -               - / 22.7 / 18.1 / -
-// (KU = 2 with rows of 1000 bf16: 10.7 / 9.8 / 11.0, so U = 2.  With rows of 1001
-// bf16, one element at a time, these calls take 12.2, 30.4, 22.3 and 22.3 us
-// and for the gradient 20.7, 27.4, 26.7 and 30.9.)
+// Chunks per lane in flight, for KU slots at once.  Measured in us with rows of
+// 4096 bf16 in 16-byte chunks and of 1002 and 1001 bf16 in 4- and 2-byte ones,
+// 400 MB of them in rotation, 8192 tokens of one and two slots, 4096 of four,
+// 2048 of eight, for U = 1 / 2 / 4 / 8:
+//                    16-byte                      4-byte                       2-byte
+//   combine, KU = 1   26.4 / 29.4 / 24.6 / 24.7    19.1 / 14.9 /  9.9 /  8.6    29.2 / 25.6 / 23.8 / 14.9
+//            KU = 2   32.3 / 32.6 / 33.2 / 44.3    21.0 / 17.5 / 14.4 / 17.3    32.2 / 23.5 / 31.0 / 31.2
+//            KU = 4   27.4 / 30.9 / 46.7 / 38.0    15.9 / 12.2 / 11.2 / 13.5    24.3 / 24.7 / 25.7 / 34.1
+//            KU = 8   24.5 / 29.2 / 34.6 /  187    12.6 / 10.6 / 11.6 / 11.3    28.4 / 23.9 / 34.7 / 43.0
+//   gradient KU = 1   36.1 / 34.3 / 32.5 / 33.8    22.1 / 18.9 / 14.2 / 13.2    29.7 / 27.2 / 26.4 / 21.9
+//            KU = 2   54.6 / 53.4 / 55.5 / 64.4    30.8 / 26.2 / 19.8 / 18.3    43.1 / 39.6 / 36.3 / 29.2
+//            KU = 4   47.5 / 52.2 / 47.5 / 54.8    26.1 / 19.9 / 17.1 / 20.4    40.2 / 30.3 / 28.1 / 32.7
+//            KU = 8   47.9 / 45.6 / 52.3 / 89.3    28.9 / 24.6 / 19.6 / 19.6    41.6 / 38.4 / 32.4 / 31.4
+// Both small chunks share a rule.  Not the best here: combine's KU = 2 in 2-byte
+// chunks and KU = 4 in 4-byte ones, and the gradient's 16-byte chunks with one
+// and eight slots, which earlier measurements with less in rotation preferred.
 constexpr int combine_chunks(int ku, int ch) { return ch == 16 ? (ku >= 4 ? 1 : 4 / ku) : (ku >= 4 ? 2 : 8 / ku); }
 constexpr int back_chunks(int ku, int ch) { return ch == 16 ? (ku >= 4 ? 1 : 2) : (ku >= 4 ? 4 : 8); }
 

@@ -23,16 +23,22 @@
 //    5 tokens x 5000 x 2000,  groups of 32, fp32 result         8.6 us   0.9
 //    1 token through 8 of 64 experts of 4096 x 2048            12.9 us   5.1
 //   32 tokens, 2 of 16 experts of 8192 x 4096, groups of 64    65.6 us  42.9
-// What bounds it is the multiplying warps' instructions, not memory: with the
-// ring alone (nothing multiplied) the same calls take 8.8, 13.7, 6.4, 9.0 and
-// 48.5 us, with two stages instead of three or four the first four take no
-// longer, and with the weights in L2 they gain 1.5 us.  A stage is about 3500
-// warp instructions; its four steps take a warp 1250 cycles where one CTA has
-// the SM and 1650 where two do.  Removing the unpacking or the mma alone gains
-// 10%, both 45%.  Slower or equal: one CTA per SM with 16 multiplying warps;
+// What bounds it is the multiplying warps' dependent chain (code word, unpacking,
+// two mma into the same sums) with four of them per scheduler, more than memory:
+// with the ring alone (nothing multiplied) the same calls take 8.8, 13.7, 6.4,
+// 9.0 and 48.5 us, with two stages instead of three or four the first four take
+// no longer, and with the weights in L2 they gain 1.5 us.  Nor is it the issue
+// of instructions or the tensor pipe: counters show 38-52% of the issue slots
+// and 11-18% of the pipe in use, and unpacking without the fma took longer.  A
+// stage is about 3500 warp instructions; its four steps take a warp 1250 cycles
+// where one CTA has the SM and 1650 where two do.  Removing the unpacking or the
+// mma alone gains 10%, both 45%.  The ring alone is short of the copy too: its
+// thread 0 asks for a stage's codes only after its warp has stored the scales of
+// the one before.  Slower or equal: one CTA per SM with 16 multiplying warps;
 // three CTAs; 96-row tiles; ranges of equal length across tiles, joined in
-// memory (24.3 us for 16 tokens, but 13.9 us for one and 76.7 for 32);
-// activations by bulk copies; a first copy of codes before the scales' loads.
+// memory (24.3 us for 16 tokens, but 13.9 us for one and 76.7 for 32; no rule
+// chooses between the two); activations by bulk copies; a first copy of codes
+// before the scales' loads.
 //
 // mma.sync and not tcgen05.mma: the latter takes at least 27 ns whatever its
 // number of columns up to 64, so that 128 x 256 weights hold the tensor core

@@ -131,10 +131,10 @@ constexpr int kExpertMax = 1024;          // experts
 constexpr int kExpertMaxSlots = 64;       // slots per token
 // Slots that one launch sorts and copies.  Every block counts against all ids,
 // so its time grows with n: 2048 slots of 128 experts take it 9.7 us without
-// the rows, the separate sort 4.9.
+// the rows, the separate sort 4.8.
 constexpr int kExpertSmallSlots = 512;
-// Slots that one block sorts.  2056 slots of 128 experts: 5.2 us in one block,
-// and one launch less for the host; 9003 of 61 take two kernels 5.7.
+// Slots that one block sorts.  2056 slots of 128 experts: 5.1 us in one block;
+// 9003 of 61 take three kernels 6.6, two where rows are copied.
 constexpr int kExpertOneBlock = 4096;
 constexpr int kExpertMaxChunks = 128;     // chunks of slots of a larger sort
 
