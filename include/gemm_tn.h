@@ -603,6 +603,52 @@ int gemm_w4_tn(int64_t M, const void *A, int64_t lda, const gemm_w4_matrix *W, v
 int gemm_w4_tn_experts(const gemm_expert_plan *plan, const void *A, int64_t lda, int gather, const gemm_w4_matrix *W,
                        void *D, int64_t ldd, float alpha, int out_dtype, int activation, void *stream);
 
+/* ------------------------------------------------------------------------
+ * bf16 products by expert, for rows in a dispatch plan's order, and their
+ * gradients.  With R = T*k rows, W_e an N x K matrix and the rows r of expert e
+ * (offsets[e] <= r < offsets[e+1]):
+ *
+ *     D[r]  = act(alpha * A[r] * W_e^T)                  gemm_bf16_tn_experts
+ *     dA[r] = alpha * dD[r] * W_e                        ..._backward_a
+ *     dW_e  = alpha * dD_e^T * A_e + beta * C_e          ..._backward_w
+ *
+ * D and dA have zeros in the rows from offsets[E] on; those rows of A and dD
+ * are not used.  An expert without rows has dW_e = beta * C_e (zeros for
+ * beta = 0, where C is not read and may be NULL).  The offsets are read on the
+ * device: no call needs them on the host or waits for them.
+ *
+ *   A, dA   R x K, row-major, leading dimension at least K
+ *   D, dD   R x N
+ *   W, C, dW  E matrices of N x K; stride_* elements from one to the next, at
+ *           least N times the leading dimension (not used for one expert).
+ *           dW may be C (with the same strides), to add to what it holds
+ *
+ * A, dD and W are bf16 and 16-byte aligned with leading dimensions and strides
+ * that are multiples of 8 (GEMM_ERR_MISALIGNED otherwise).  D, dA, dW and C
+ * are bf16 or fp32 (out_dtype) and may have any alignment to their element
+ * size; with addresses, pitches, strides and row lengths of whole 16 bytes they
+ * are written by TMA, which is faster.  Outputs must not overlap operands other than C.
+ * Sums are fp32 and rounded once; their order does not change from run to run.
+ * activation is a gemm_activation; the gradients are those of the product
+ * without it.
+ *
+ * No memory but the caller's is used, so any of these calls may be captured
+ * and replayed on any stream.  As for the calls above, a plan that no dispatch
+ * filled gives unspecified results, but nothing outside the matrices is read
+ * or written. */
+int gemm_bf16_tn_experts(const gemm_expert_plan *plan, int64_t N, int64_t K, const void *A, int64_t lda,
+                         const void *W, int64_t ldw, int64_t stride_w, void *D, int64_t ldd,
+                         float alpha, int out_dtype, int activation, void *stream);
+
+int gemm_bf16_tn_experts_backward_a(const gemm_expert_plan *plan, int64_t N, int64_t K, const void *dD, int64_t lddd,
+                                    const void *W, int64_t ldw, int64_t stride_w, void *dA, int64_t ldda,
+                                    float alpha, int out_dtype, void *stream);
+
+int gemm_bf16_tn_experts_backward_w(const gemm_expert_plan *plan, int64_t N, int64_t K, const void *dD, int64_t lddd,
+                                    const void *A, int64_t lda, const void *C, int64_t ldc, int64_t stride_c,
+                                    void *dW, int64_t lddw, int64_t stride_dw, float alpha, float beta,
+                                    int out_dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

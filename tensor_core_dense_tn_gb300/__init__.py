@@ -40,7 +40,8 @@ EXPORTED = ["gemm_bf16_tn", "gemm_bf16_tn_ex", "gemm_get_status", "gemm_get_stat
             "gemm_bf16_tn_skinny_noalloc", "gemm_bf16_tn_bias_act", "gemm_fp8_tn", "gemm_fp8_tn_ex",
             "gemm_bf16_tn_grouped", "gemm_bf16_tn_batched", "gemm_plan", "gemm_stream_read",
             "gemm_mma_rate", "gemm_fp8_tn_bias_act", "gemm_expert_dispatch", "gemm_expert_dispatch_backward",
-            "gemm_expert_combine", "gemm_expert_combine_backward", "gemm_w4_tn", "gemm_w4_tn_experts"]
+            "gemm_expert_combine", "gemm_expert_combine_backward", "gemm_w4_tn", "gemm_w4_tn_experts",
+            "gemm_bf16_tn_experts", "gemm_bf16_tn_experts_backward_a", "gemm_bf16_tn_experts_backward_w"]
 
 FP8_E4M3, FP8_E5M2 = 0, 1
 SCHED_DEFAULT, SCHED_STATIC, SCHED_CLC = 0, 1, 2
@@ -162,6 +163,13 @@ def load(path: str = LIB_PATH):
         lib.gemm_w4_tn.restype = i32
         lib.gemm_w4_tn_experts.argtypes = [plan, vp, i64, i32, w4, vp, i64, f32, i32, i32, vp]
         lib.gemm_w4_tn_experts.restype = i32
+        lib.gemm_bf16_tn_experts.argtypes = [plan, i64, i64, vp, i64, vp, i64, i64, vp, i64, f32, i32, i32, vp]
+        lib.gemm_bf16_tn_experts.restype = i32
+        lib.gemm_bf16_tn_experts_backward_a.argtypes = [plan, i64, i64, vp, i64, vp, i64, i64, vp, i64, f32, i32, vp]
+        lib.gemm_bf16_tn_experts_backward_a.restype = i32
+        lib.gemm_bf16_tn_experts_backward_w.argtypes = [plan, i64, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64,
+                                                        f32, f32, i32, vp]
+        lib.gemm_bf16_tn_experts_backward_w.restype = i32
         lib.gemm_get_status.argtypes = [vp]
         lib.gemm_get_status.restype = i32
         lib.gemm_get_status_detail.restype = i32
@@ -364,6 +372,25 @@ def gemm_w4_tn_experts(plan, A, lda, gather, W, D, ldd, alpha, out_dtype, activa
     """Raw C-ABI call: gemm_w4_tn with each expert's matrix for its rows of the plan."""
     return load().gemm_w4_tn_experts(plan, A or None, lda, gather, W, D or None, ldd, alpha, out_dtype, activation,
                                      stream or None)
+
+
+def gemm_bf16_tn_experts(plan, N, K, A, lda, W, ldw, stride_w, D, ldd, alpha, out_dtype, activation, stream) -> int:
+    """Raw C-ABI call: D[r] = act(alpha * A[r] * W_e^T) for the rows r of expert e."""
+    return load().gemm_bf16_tn_experts(plan, N, K, A or None, lda, W or None, ldw, stride_w, D or None, ldd, alpha,
+                                       out_dtype, activation, stream or None)
+
+
+def gemm_bf16_tn_experts_backward_a(plan, N, K, dD, lddd, W, ldw, stride_w, dA, ldda, alpha, out_dtype, stream) -> int:
+    """Raw C-ABI call: dA[r] = alpha * dD[r] * W_e."""
+    return load().gemm_bf16_tn_experts_backward_a(plan, N, K, dD or None, lddd, W or None, ldw, stride_w, dA or None,
+                                                  ldda, alpha, out_dtype, stream or None)
+
+
+def gemm_bf16_tn_experts_backward_w(plan, N, K, dD, lddd, A, lda, C, ldc, stride_c, dW, lddw, stride_dw, alpha, beta,
+                                    out_dtype, stream) -> int:
+    """Raw C-ABI call: dW_e = alpha * dD_e^T * A_e + beta * C_e."""
+    return load().gemm_bf16_tn_experts_backward_w(plan, N, K, dD or None, lddd, A or None, lda, C or None, ldc, stride_c,
+                                                  dW or None, lddw, stride_dw, alpha, beta, out_dtype, stream or None)
 
 
 _torch = None
@@ -632,6 +659,104 @@ def _w4(plan, A, W, gather, alpha, activation, out_dtype, out, stream):
     else:
         rc = lib.gemm_w4_tn_experts(plan.info, A.data_ptr(), lda, gather, W.info, out.data_ptr(), ldd, alpha, code,
                                     activation, s)
+    if rc:
+        _check(rc)
+    return out
+
+
+def _matrices_of(t, count, N, K, what, gpu):
+    """Checks `count` N x K matrices on `gpu` with unit column stride, none overlapping another; returns their row
+    stride and the stride from one to the next."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape != (count, N, K) or t.get_device() != gpu:
+        raise ValueError(f"{what} must be {count} matrices of {N} x {K} on GPU {gpu}, not {tuple(shape)} on {t.device}")
+    apart, ld = stride[0], stride[1]
+    if stride[2] != 1 and K > 1 and N > 0:
+        raise ValueError(f"{what} must have unit column stride")
+    if ld < K:
+        if N > 1:
+            raise ValueError(f"{what} must have a row stride of at least its row length {K}, not {ld}")
+        ld = K
+    if apart < N * ld:
+        if count > 1:       # one matrix for all experts, or matrices that overlap
+            raise ValueError(f"{what} must have a stride of at least {N * ld} from one expert's matrix to the next, not "
+                             f"{apart} (contiguous() makes a copy that has)")
+        apart = N * ld
+    return ld, apart
+
+
+def gemm_experts(A, W, plan: ExpertPlan, alpha: float = 1.0, activation: int = ACT_NONE, out_dtype=None, out=None,
+                 stream=None):
+    """D[r] = act(alpha * A[r] @ W[e].T) for the rows r of expert e in `plan`: A (plan.rows, K) bf16 in expert order,
+    W (experts, N, K) bf16; zeros in the rows past plan.offsets[experts].  Nothing waits for the row counts.  Without
+    an autograd graph: the gradients of the product without an activation are gemm_experts_backward_a() and _w()."""
+    return _experts_rows(False, A, W, plan, alpha, activation, out_dtype, out, stream)
+
+
+def gemm_experts_backward_a(dD, W, plan: ExpertPlan, alpha: float = 1.0, out_dtype=None, out=None, stream=None):
+    """Gradient of gemm_experts' rows: dA[r] = alpha * dD[r] @ W[e], zeros past plan.offsets[experts]."""
+    return _experts_rows(True, dD, W, plan, alpha, ACT_NONE, out_dtype, out, stream)
+
+
+def _experts_rows(backward, X, W, plan, alpha, activation, out_dtype, out, stream):
+    torch = _torch or _t()
+    if X.dtype != torch.bfloat16 or W.dtype != torch.bfloat16 or W.dim() != 3:
+        raise ValueError(f"{'dD' if backward else 'A'} and W must be bf16, W one matrix per expert")
+    gpu = plan.gpu
+    if gpu or _several_gpus:
+        _gpu_of(gpu, "the plan")
+    _, N, K = W.shape
+    ldw, apart = _matrices_of(W, plan.experts, N, K, "W", gpu)
+    ldx = _rows_of(X, plan.rows, N if backward else K, "dD" if backward else "A", gpu)
+    width = K if backward else N
+    if out is None:
+        out, ldo = torch.empty((plan.rows, width), dtype=out_dtype or torch.bfloat16, device=X.device), width
+    else:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out must have out_dtype")
+        ldo = _rows_of(out, plan.rows, width, "out", gpu)
+    code = _out_code(out.dtype, "out")
+    lib, s = _lib or load(), _stream_of(X) if stream is None else stream or None
+    if backward:
+        rc = lib.gemm_bf16_tn_experts_backward_a(plan.info, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw, apart,
+                                                 out.data_ptr(), ldo, alpha, code, s)
+    else:
+        rc = lib.gemm_bf16_tn_experts(plan.info, N, K, X.data_ptr(), ldx, W.data_ptr(), ldw, apart, out.data_ptr(), ldo,
+                                      alpha, code, activation, s)
+    if rc:
+        _check(rc)
+    return out
+
+
+def gemm_experts_backward_w(dD, A, plan: ExpertPlan, alpha: float = 1.0, beta: float = 0.0, C=None, out_dtype=None,
+                            out=None, stream=None):
+    """Gradients of gemm_experts' matrices: dW[e] = alpha * dD_e.T @ A_e (+ beta * C[e]) over e's rows of dD
+    (plan.rows, N) and A (plan.rows, K), both bf16; (experts, N, K) of out_dtype, by default bf16.  C has out's type
+    and may be out itself, to add to what it holds."""
+    torch = _torch or _t()
+    if dD.dtype != torch.bfloat16 or A.dtype != torch.bfloat16:
+        raise ValueError("dD and A must be bf16")
+    gpu = plan.gpu
+    if gpu or _several_gpus:
+        _gpu_of(gpu, "the plan")
+    lddd, lda = _rows_of(dD, plan.rows, None, "dD", gpu), _rows_of(A, plan.rows, None, "A", gpu)
+    N, K, E = dD.shape[1], A.shape[1], plan.experts
+    if out is None:
+        dtype = out_dtype or (torch.bfloat16 if C is None or beta == 0.0 else C.dtype)
+        out = torch.empty((E, N, K), dtype=dtype, device=A.device)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out must have out_dtype")
+    code = _out_code(out.dtype, "out")
+    ldo, apart = _matrices_of(out, E, N, K, "out", gpu)
+    c, ldc, apart_c = None, 0, 0
+    if beta != 0.0:
+        if C is None or C.dtype != out.dtype:
+            raise ValueError("beta != 0 needs C of out's type")
+        ldc, apart_c = _matrices_of(C, E, N, K, "C", gpu)
+        c = C.data_ptr()
+    rc = (_lib or load()).gemm_bf16_tn_experts_backward_w(
+        plan.info, N, K, dD.data_ptr(), lddd, A.data_ptr(), lda, c, ldc, apart_c, out.data_ptr(), ldo, apart, alpha,
+        beta, code, _stream_of(A) if stream is None else stream or None)
     if rc:
         _check(rc)
     return out

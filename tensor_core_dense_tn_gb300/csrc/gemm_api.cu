@@ -1025,6 +1025,123 @@ int run_w4(int64_t M, const gemm_expert_plan* plan, int gather, const void* A, i
   return finish_launch(launch_w4(tm, p, active, st->sms, static_cast<cudaStream_t>(stream_v), &li), li);
 }
 
+// ---------------------------------------------------------------- products by expert
+// A matrix argument of TMA loads: on 16 bytes with a pitch of whole 16 bytes.
+int check_tma_rows(const char* what, const void* base, int64_t ld, int64_t width) {
+  const int rc = check_rows(what, base, ld, width, 2);
+  if (rc) return rc;
+  if (!aligned16(base) || ld % 8)
+    return fail(GEMM_ERR_MISALIGNED, "%s must be 16-byte aligned with a leading dimension that is a multiple of 8", what);
+  return GEMM_OK;
+}
+
+// Matrices of rows x ld elements, one per expert, that do not overlap.
+int check_stride(const char* what, int64_t E, int64_t rows, int64_t ld, int64_t stride) {
+  if (E > 1 && stride < rows * ld)
+    return fail(GEMM_ERR_INVALID_VALUE, "stride from one matrix of %s to the next (%lld) below their size (%lld)", what,
+                (long long)stride, (long long)(rows * ld));
+  return GEMM_OK;
+}
+
+// op: kExpertsForward (X = A), kExpertsRows (X = dD) with out = R rows, or
+// kExpertsWeights (X = dD, Y = A) with out = E matrices of N x K.
+int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, const void* X, int64_t ldx, const void* Y,
+                int64_t ldy, int64_t stride_y, const void* C, int64_t ldc, int64_t stride_c, void* D, int64_t ldd,
+                int64_t stride_d, float alpha, float beta, int out_dtype, int activation, void* stream_v) {
+  t_error.clear();
+  ExpertParams ep;
+  int rc = check_plan(plan, 0, &ep);
+  if (rc || (rc = check_dtype("out_dtype", out_dtype))) return rc;
+  if (activation < GEMM_ACT_NONE || activation > GEMM_ACT_SILU)
+    return fail(GEMM_ERR_INVALID_VALUE, "unknown activation %d", activation);
+  const int64_t kMaxDim = (int64_t)1 << 31;
+  if (N < 0 || K < 0 || N >= kMaxDim - 4096 || K >= kMaxDim - 4096)
+    return fail(GEMM_ERR_INVALID_VALUE, "sizes must be in [0, 2^31 - 4096): N=%lld K=%lld", (long long)N, (long long)K);
+  const bool weights = op == kExpertsWeights;
+  const int64_t R = ep.n, E = ep.E;
+  const int64_t cols = op == kExpertsForward ? N : K, sum = weights ? R : op == kExpertsForward ? K : N;
+  if (cols == 0 || (weights ? N : R) == 0) return GEMM_OK;
+  const int esize = dtype_bytes(out_dtype);
+  const char* dname = weights ? "dW" : op == kExpertsRows ? "dA" : "D";
+  if ((rc = check_rows(dname, D, ldd, cols, esize))) return rc;
+  ExpertsParams p = {};
+  p.has_c = weights && beta != 0.0f;
+  if (weights && (rc = check_stride(dname, E, N, ldd, stride_d))) return rc;
+  if (p.has_c && ((rc = check_rows("C", C, ldc, cols, esize)) || (rc = check_stride("C", E, N, ldc, stride_c)))) return rc;
+  if (E == 1) {       // the strides are not used; give the maps valid ones
+    stride_y = N * ldy;
+    stride_d = N * ldd;
+    stride_c = N * ldc;
+  }
+  p.has_ab = sum > 0;
+  if (p.has_ab) {
+    if ((rc = check_tma_rows(op == kExpertsForward ? "A" : "dD", X, ldx, op == kExpertsForward ? K : N)) ||
+        (rc = check_tma_rows(weights ? "A" : "W", Y, ldy, K)))
+      return rc;
+    if (!weights) {
+      if ((rc = check_stride("W", E, N, ldy, stride_y))) return rc;
+      if (stride_y % 8) return fail(GEMM_ERR_MISALIGNED, "the stride from one matrix of W to the next must be a multiple of 8");
+    }
+  }
+  int dev = 0;
+  DeviceState* st = nullptr;
+  if ((rc = init_device(&dev, &st))) return rc;
+  p.op = op;
+  p.R = (int)R;
+  p.E = (int)E;
+  p.offsets = ep.offsets;
+  p.S = weights ? 0 : (int)sum;
+  p.rows_out = (int)N;
+  p.cols_out = (int)cols;
+  p.D = D;
+  p.ldd = ldd;
+  p.stride_d = stride_d;
+  p.C = C;
+  p.ldc = ldc;
+  p.stride_c = stride_c;
+  p.out_f32 = out_dtype == GEMM_OUT_F32;
+  p.act = activation;
+  p.alpha = alpha;
+  p.beta = beta;
+  auto on16 = [&](const void* base, int64_t ld, int64_t stride) {
+    return aligned16(base) && ld * esize % 16 == 0 && (!weights || stride * esize % 16 == 0);
+  };
+  // A TMA store clips a row's end to whole 16 bytes only: it would write into
+  // the padding behind rows that end inside them.
+  p.direct = cols * esize % 16 || !on16(D, ldd, stride_d) || (p.has_c && !on16(C, ldc, stride_c));
+  p.timeout_ns = timeout_ns(nullptr);
+  p.status = st->status;
+  experts_geometry(&p, st->sms);
+  const int64_t tile_rows = 128 * p.cg;
+  const int64_t tiles_n = (cols + p.bn - 1) / p.bn;
+  const int64_t blocks = weights ? E * ((N + tile_rows - 1) / tile_rows) : R / tile_rows + E + 1;
+  if (tiles_n * blocks >= kMaxDim - 4096) return fail(GEMM_ERR_INVALID_VALUE, "too many tiles");
+  p.tiles_n = (int)tiles_n;
+  p.tiles_m = weights ? (int)((N + tile_rows - 1) / tile_rows) : 0;
+  p.strip = weights ? 8 : raster_group_for((int)tile_rows, sum, 2, 16);
+  CUtensorMap tA, tB, tC, tD;
+  memset(&tA, 0, sizeof tA);
+  tB = tC = tD = tA;
+  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (p.has_ab) {
+    if ((rc = encode_2d(&tA, bf16, 2, X, op == kExpertsForward ? K : N, R, ldx, 64, p.a_rows, sw, "rows"))) return rc;
+    if (weights) rc = encode_2d(&tB, bf16, 2, Y, K, R, ldy, 64, 64, sw, "A");
+    else rc = encode_3d(&tB, bf16, 2, Y, K, N, E, ldy, stride_y, 64, op == kExpertsForward ? p.bn / p.cg : 64, sw, "W");
+    if (rc) return rc;
+  }
+  if (!p.direct) {
+    const CUtensorMapDataType dt = p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf16;
+    const CUtensorMapSwizzle so = CU_TENSOR_MAP_SWIZZLE_64B;
+    if (!weights) rc = encode_2d(&tD, dt, esize, D, cols, R, ldd, 64 / esize, 32, so, dname);
+    else rc = encode_3d(&tD, dt, esize, D, cols, N, E, ldd, stride_d, 64 / esize, 32, so, dname);
+    if (!rc && p.has_c) rc = encode_3d(&tC, dt, esize, C, cols, N, E, ldc, stride_c, 64 / esize, 32, so, "C");
+    if (rc) return rc;
+  }
+  LaunchInfo li = {};
+  return finish_launch(launch_experts(tA, tB, tC, tD, p, st->sms, static_cast<cudaStream_t>(stream_v), &li), li);
+}
+
 }  // namespace
 
 // Sets the text gemm_last_error_string returns on this thread, for entry
@@ -1159,6 +1276,28 @@ int gemm_w4_tn_experts(const gemm_expert_plan* plan, const void* A, int64_t lda,
                        void* D, int64_t ldd, float alpha, int out_dtype, int activation, void* stream) {
   if (!plan) return gtn::fail(GEMM_ERR_INVALID_VALUE, "plan is NULL");
   return gtn::run_w4(0, plan, gather, A, lda, W, D, ldd, alpha, out_dtype, activation, stream);
+}
+
+int gemm_bf16_tn_experts(const gemm_expert_plan* plan, int64_t N, int64_t K, const void* A, int64_t lda, const void* W,
+                         int64_t ldw, int64_t stride_w, void* D, int64_t ldd, float alpha, int out_dtype,
+                         int activation, void* stream) {
+  return gtn::run_experts(gtn::kExpertsForward, plan, N, K, A, lda, W, ldw, stride_w, nullptr, 0, 0, D, ldd, 0, alpha,
+                          0.0f, out_dtype, activation, stream);
+}
+
+int gemm_bf16_tn_experts_backward_a(const gemm_expert_plan* plan, int64_t N, int64_t K, const void* dD, int64_t lddd,
+                                    const void* W, int64_t ldw, int64_t stride_w, void* dA, int64_t ldda, float alpha,
+                                    int out_dtype, void* stream) {
+  return gtn::run_experts(gtn::kExpertsRows, plan, N, K, dD, lddd, W, ldw, stride_w, nullptr, 0, 0, dA, ldda, 0, alpha,
+                          0.0f, out_dtype, GEMM_ACT_NONE, stream);
+}
+
+int gemm_bf16_tn_experts_backward_w(const gemm_expert_plan* plan, int64_t N, int64_t K, const void* dD, int64_t lddd,
+                                    const void* A, int64_t lda, const void* C, int64_t ldc, int64_t stride_c, void* dW,
+                                    int64_t lddw, int64_t stride_dw, float alpha, float beta, int out_dtype,
+                                    void* stream) {
+  return gtn::run_experts(gtn::kExpertsWeights, plan, N, K, dD, lddd, A, lda, 0, C, ldc, stride_c, dW, lddw, stride_dw,
+                          alpha, beta, out_dtype, GEMM_ACT_NONE, stream);
 }
 
 int gemm_plan(int64_t M, int64_t N, int64_t K, int fp8_inputs, int num_sms, const gemm_tn_config* cfg,

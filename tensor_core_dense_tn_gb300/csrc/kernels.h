@@ -200,6 +200,40 @@ int w4_split(long long items, int num_kb, int sms);
 // active: matrices that can have rows (1 for the dense form).
 cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, int sms, cudaStream_t stream, LaunchInfo* info);
 
+// bf16 products by expert and their gradients (gemm_experts.cu).
+constexpr int kExpertsForward = 0, kExpertsRows = 1, kExpertsWeights = 2;
+constexpr int kExpertsMaxBoxes = 8;       // staged boxes per epilogue warp
+
+struct ExpertsParams {
+  int op;              // kExperts*
+  int R, E;            // rows of the plan, experts
+  const int* offsets;  // E + 1
+  int S;               // forward, rows: length of the sum (K or N)
+  int rows_out;        // weights: rows of one output matrix (N)
+  int cols_out;        // columns of the output
+  int has_ab;          // the operands' tensor maps are filled (the sum is not empty)
+  void* D; long long ldd, stride_d;        // elements
+  const void* C; long long ldc, stride_c;  // weights: read where has_c
+  int has_c, out_f32, act;
+  int direct;          // D or C is not on 16 bytes: no TMA for them
+  float alpha, beta;
+  int cg, bn, a_rows;  // CTAs per tile, columns per tile, rows of A per TMA box
+  int a_bytes, b_bytes, stages, boxes;     // ring stage per CTA, stages, staged boxes per epilogue warp
+  int tiles_m, tiles_n;                    // weights: per expert; else tiles_n alone
+  int strip;           // row blocks per strip of the tile order
+  uint64_t timeout_ns;
+  int* status;
+};
+
+// Chooses the tile shape (cg, bn, a_rows, stages, boxes) from op, R, E, the
+// output's columns and has_c.
+void experts_geometry(ExpertsParams* p, int sms);
+// tmA: rows of the first operand {columns, rows}, 64 x a_rows boxes (weights:
+// 64 x 64), tmB: the second, boxes of 64 x bn / cg (forward) or 64 x 64; 128-byte
+// swizzle.  tmC, tmD: the output, 64 bytes x 32 rows, 64-byte swizzle, 3D for weights.
+cudaError_t launch_experts(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC, const CUtensorMap& tmD,
+                           ExpertsParams p, int sms, cudaStream_t stream, LaunchInfo* info);
+
 struct LaunchInfo {
   int path;            // 1 = 1-SM tiled, 2 = 2-SM tiled, 3 = skinny
   int grid, cluster, block;

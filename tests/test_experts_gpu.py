@@ -1,0 +1,273 @@
+"""GPU parity of the bf16 products by expert and their gradients.
+
+The expected values are loops over the experts in 64 bits.  Whole numbers
+whose sums stay below 2^24 have to come out exactly (rounded once to bf16
+where the result is bf16).  Other values are held to bounds that follow from
+the arithmetic: an fp32 sum of n products in any order, each addition rounded
+or cut off, is within n 2^-23 of the sum of the magnitudes; the factors and
+beta * C add 2^-23 of theirs each; the result's rounding is half a step,
+2^-8 of the value for bf16 and 2^-24 for fp32.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+g = pytest.importorskip("tensor_core_dense_tn_gb300")
+
+BF16, F32 = torch.bfloat16, torch.float32
+EPS = {BF16: 2.0 ** -8, F32: 2.0 ** -24}
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def plan_of(counts, lost):
+    """A plan with counts[e] rows of expert e and `lost` rows of nobody behind them."""
+    i32 = dict(dtype=torch.int32, device="cuda")
+    offsets = torch.tensor([sum(counts[:e]) for e in range(len(counts) + 1)], **i32)
+    rows = sum(counts) + lost
+    return g.ExpertPlan.of(offsets, torch.zeros(rows, 1, **i32), torch.zeros(rows, **i32))
+
+
+def values(shape, seed, whole, pad=None):
+    """bf16 values; whole numbers in [-3, 3], or normal ones.  Rows start on 16 bytes, `pad` elements apart from
+    their end (by default as few as that takes), and the padding holds NaN."""
+    wide = -(-shape[-1] // 8) * 8 + (pad or 0)
+    buf = torch.full((*shape[:-1], wide), float("nan"), device="cuda", dtype=BF16)
+    t = torch.randint(-3, 4, shape, generator=gen(seed), device="cuda").float() if whole else \
+        torch.randn(shape, generator=gen(seed), device="cuda")
+    buf[..., :shape[-1]] = t
+    return buf[..., :shape[-1]]
+
+
+def bounds_of(plan):
+    return plan.offsets.tolist()
+
+
+def forward64(A, W, plan):
+    """The product and the sum of its terms' magnitudes."""
+    ref = torch.zeros(A.shape[0], W.shape[1], dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(ref)
+    b = bounds_of(plan)
+    for e, (lo, hi) in enumerate(zip(b, b[1:])):
+        a, w = A[lo:hi].double(), W[e].double()
+        ref[lo:hi], mag[lo:hi] = a @ w.T, a.abs() @ w.abs().T
+    return ref, mag
+
+
+def weights64(dD, A, plan):
+    b = bounds_of(plan)
+    pairs = [(dD[lo:hi].double(), A[lo:hi].double()) for lo, hi in zip(b, b[1:])]
+    return torch.stack([d.T @ a for d, a in pairs]), torch.stack([d.abs().T @ a.abs() for d, a in pairs])
+
+
+def status():
+    assert g.gemm_get_status(torch.cuda.current_stream().cuda_stream) == 0
+
+
+def check(got, ref, mag, terms, whole):
+    assert not torch.isnan(got).any()
+    if whole:
+        assert torch.equal(got, ref.to(F32).to(got.dtype))
+    else:
+        bound = (terms + 2) * 2.0 ** -23 * mag + EPS[got.dtype] * 1.01 * ref.abs()
+        assert torch.all((got.double() - ref).abs() <= bound)
+
+
+def canvas(shape, dtype, pad):
+    """An output of `shape` inside a larger buffer of sevens, `pad` elements behind each row."""
+    buf = torch.full((*shape[:-1], shape[-1] + pad), 7.0, device="cuda", dtype=dtype)
+    return buf, buf[..., :shape[-1]]
+
+
+CASES = [  # rows of each expert, rows of nobody, N, K
+    ([1], 0, 8, 8), ([0, 1, 0, 0], 0, 256, 64), ([2], 3, 1, 1), ([5, 0, 130, 64, 1], 17, 72, 136),
+    ([256, 255, 257, 1, 0, 128], 0, 264, 200), ([700], 1, 520, 1000), ([3] * 61, 5, 1000, 2000),
+    ([300, 513, 90], 300, 768, 512), ([33, 16, 15, 17], 0, 33, 77), ([0, 0, 0], 40, 64, 64),
+    ([16] * 7 + [128] * 3, 0, 512, 320), ([129, 127, 640], 2, 2048, 72), ([1] * 1024, 8, 64, 128),
+]
+
+
+@pytest.mark.parametrize("counts,lost,N,K", CASES)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("whole", [True, False])
+def test_rows(counts, lost, N, K, dtype, whole):
+    plan = plan_of(counts, lost)
+    W = values((len(counts), N, K), 1, whole)
+    for call, S, width, right in ((g.gemm_experts, K, N, W), (g.gemm_experts_backward_a, N, K, W.transpose(1, 2))):
+        X = values((plan.rows, S), 2, whole)
+        X[sum(counts):] = float("nan")          # nobody's rows are not used
+        ref, mag = forward64(X, right, plan)
+        check(call(X, W, plan, out_dtype=dtype), ref, mag, S, whole)
+        buf, out = canvas((plan.rows, width), dtype, 3 if N % 16 else 8)
+        assert call(X, W, plan, alpha=0.5, out=out) is out
+        status()
+        check(out, 0.5 * ref, mag, S, whole and dtype == F32)
+        assert torch.all(buf[:, width:] == 7)
+
+
+@pytest.mark.parametrize("counts,lost,N,K", CASES)
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("whole", [True, False])
+def test_weights(counts, lost, N, K, dtype, whole):
+    plan = plan_of(counts, lost)
+    dD, A = values((plan.rows, N), 3, whole), values((plan.rows, K), 4, whole, pad=8)
+    dD[sum(counts):] = float("nan")
+    A[sum(counts):] = float("nan")
+    ref, mag = weights64(dD, A, plan)
+    check(g.gemm_experts_backward_w(dD, A, plan, out_dtype=dtype), ref, mag, max(counts), whole)
+    status()
+    # added to what is there, in place, in a padded buffer
+    buf, out = canvas((len(counts), N, K), dtype, 3 if K % 16 else 8)
+    start = torch.randint(-8, 9, out.shape, generator=gen(5), device="cuda").to(dtype)
+    out.copy_(start)
+    g.gemm_experts_backward_w(dD, A, plan, beta=2.0, C=out, out=out)
+    status()
+    check(out, ref + 2 * start.double(), mag + 2 * start.double().abs(), max(counts), whole)
+    assert torch.all(buf[..., K:] == 7)
+    # and from another buffer, with a factor
+    C = start.clone()
+    got = g.gemm_experts_backward_w(dD, A, plan, alpha=0.5, beta=-1.0, C=C)
+    assert got.dtype == dtype and torch.equal(C, start)
+    check(got, 0.5 * ref - start.double(), mag + start.double().abs(), max(counts), whole and dtype == F32)
+
+
+@pytest.mark.parametrize("act", [g.ACT_RELU, g.ACT_GELU, g.ACT_GELU_TANH, g.ACT_SILU])
+@pytest.mark.parametrize("counts", [[5, 0, 40], [300, 200, 77]])
+def test_activation(act, counts):
+    """The activations' slopes lie in [-0.13, 1.13]; their own error is a few fp32 steps of the value (2^-20)."""
+    plan = plan_of(counts, 9)
+    A, W = values((plan.rows, 200), 1, False), values((3, 136, 200), 2, False) * 200 ** -0.5
+    ref, mag = forward64(A, W, plan)
+    fn = {g.ACT_RELU: torch.relu, g.ACT_GELU: torch.nn.functional.gelu, g.ACT_SILU: torch.nn.functional.silu,
+          g.ACT_GELU_TANH: lambda t: torch.nn.functional.gelu(t, approximate="tanh")}[act]
+    for dtype in (BF16, F32):
+        got = g.gemm_experts(A, W, plan, activation=act, out_dtype=dtype)
+        status()
+        bound = 1.2 * 202 * 2.0 ** -23 * mag + 2.0 ** -20 * ref.abs() + EPS[dtype] * 1.01 * fn(ref).abs()
+        assert torch.all((got.double() - fn(ref)).abs() <= bound)
+        assert torch.all(got[sum(counts):] == 0)
+
+
+@pytest.mark.parametrize("counts", [[5, 7, 3, 11], [200, 130, 61, 300]])
+def test_what_is_not_finite_stays_in_its_expert(counts):
+    plan = plan_of(counts, 0)
+    b = bounds_of(plan)
+    for bad in (float("nan"), float("inf")):
+        A, dD, W = values((plan.rows, 96), 1, True), values((plan.rows, 80), 2, True), values((4, 80, 96), 3, True)
+        clean = g.gemm_experts(A, W, plan), g.gemm_experts_backward_a(dD, W, plan), g.gemm_experts_backward_w(dD, A, plan)
+        A[b[1]:b[2]] = bad
+        dD[b[2]:b[3], 5] = bad
+        D, dA, dW = g.gemm_experts(A, W, plan), g.gemm_experts_backward_a(dD, W, plan), g.gemm_experts_backward_w(dD, A, plan)
+        status()
+        keep = torch.ones(plan.rows, dtype=torch.bool, device="cuda")
+        keep[b[1]:b[2]] = False
+        assert torch.equal(D[keep], clean[0][keep]) and not torch.isfinite(D[~keep]).any()
+        keep[:] = True
+        keep[b[2]:b[3]] = False
+        assert torch.equal(dA[keep], clean[1][keep])
+        assert torch.equal(dW[0], clean[2][0]) and torch.equal(dW[3], clean[2][3])
+        assert torch.equal(dW[2, :5], clean[2][2, :5]) and torch.equal(dW[2, 6:], clean[2][2, 6:])
+
+
+def test_gradients_against_differences():
+    """d<out, D>/dA and /dW against differences of the product with fp32 results, on whole numbers: the product is
+    linear in each, so the difference of one step is the gradient, and all sums are exact."""
+    plan = plan_of([6, 0, 19], 2)
+    A, W, out = values((plan.rows, 40), 1, True), values((3, 24, 40), 2, True), values((plan.rows, 24), 3, True)
+    dA = g.gemm_experts_backward_a(out, W, plan, out_dtype=F32)
+    dW = g.gemm_experts_backward_w(out, A, plan, out_dtype=F32)
+    at = lambda: (out[:25].double() * g.gemm_experts(A, W, plan, out_dtype=F32)[:25].double()).sum()  # noqa: E731
+    base = at()
+    for t, grad, places in ((A, dA, [(0, 0), (5, 39), (6, 1), (24, 7)]), (W, dW, [(0, 0, 0), (2, 23, 39), (2, 4, 5), (1, 3, 3)])):
+        for where in places:
+            t[where] += 1
+            assert at() - base == grad[where].double()
+            t[where] -= 1
+    assert torch.all(dA[25:] == 0)
+
+
+@pytest.mark.parametrize("N,K", [(512, 256), (40, 72)])
+def test_a_captured_step_follows_the_offsets(N, K):
+    """One graph of all three calls, replayed after the plan, the rows and the matrices changed, beside eager calls."""
+    T, k, E = 300, 2, 8
+    plan = g.ExpertPlan(T, k, E, "cuda")
+    ids = torch.zeros(T, k, dtype=torch.int64, device="cuda")
+    X, W, dD = values((T, K), 1, True), values((E, N, K), 2, True), values((T * k, N), 3, True)
+
+    def step():
+        rows = g.expert_dispatch(ids, plan, X)
+        return (g.gemm_experts(rows, W, plan, out_dtype=F32), g.gemm_experts_backward_a(dD, W, plan, out_dtype=F32),
+                g.gemm_experts_backward_w(dD, rows, plan, out_dtype=F32))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            held = step()
+    torch.cuda.current_stream().wait_stream(side)
+    for seed in range(3):
+        ids.copy_(torch.randint(-1, E if seed else 2, (T, k), generator=gen(seed), device="cuda"))
+        X.copy_(values((T, K), 10 + seed, True))
+        W.copy_(values((E, N, K), 20 + seed, True))
+        graph.replay()
+        got = [t.clone() for t in held]
+        rows = g.expert_dispatch(ids, plan, X)
+        status()
+        for a, b in zip(got, (forward64(rows, W, plan)[0], forward64(dD, W.transpose(1, 2), plan)[0],
+                              weights64(dD, rows, plan)[0])):
+            assert torch.equal(a.double(), b)
+
+
+@pytest.mark.parametrize("offsets", [[5, 3, 9, 1], [-7, 40, 90, 10 ** 9], [2 ** 31 - 1] * 4, [-2 ** 31] * 4, [0, 0, 0, 0]])
+def test_plans_that_no_dispatch_filled(offsets):
+    """Nothing outside the outputs is written; for offsets out of order the experts' rows are those up to the largest
+    offset so far."""
+    rows = 64
+    i32 = dict(dtype=torch.int32, device="cuda")
+    plan = g.ExpertPlan.of(torch.tensor(offsets, **i32), torch.zeros(rows, 1, **i32), torch.zeros(rows, **i32))
+    A, dD, W = values((rows, 72), 1, True), values((rows, 40), 2, True), values((3, 40, 72), 3, True)
+    big = torch.full((rows + 64, 40), 7.0, device="cuda")
+    g.gemm_experts(A, W, plan, out=big[32:32 + rows])
+    g.gemm_experts_backward_a(dD, W, plan)
+    g.gemm_experts_backward_w(dD, A, plan)
+    status()
+    assert torch.all(big[:32] == 7) and torch.all(big[32 + rows:] == 7)
+    top = 0
+    row = [top := max(top, min(max(o, 0), rows)) for o in offsets]
+    want = torch.zeros(rows, 40, dtype=torch.float64, device="cuda")
+    for e in range(3):
+        want[row[e]:row[e + 1]] = A[row[e]:row[e + 1]].double() @ W[e].double().T
+    assert torch.equal(big[32 + row[0]:32 + rows].double(), want[row[0]:])
+
+
+def test_another_stream():
+    plan = plan_of([100, 40], 3)
+    A, W = values((plan.rows, 512), 1, True), values((2, 264, 512), 2, True)
+    ref = g.gemm_experts(A, W, plan)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = g.gemm_experts(A, W, plan, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(got, ref)
+
+
+def test_empty_calls():
+    plan = plan_of([0, 0], 0)
+    A, dD, W = values((0, 64), 1, True), values((0, 32), 2, True), values((2, 32, 64), 3, True)
+    assert g.gemm_experts(A, W, plan).shape == (0, 32)
+    assert g.gemm_experts_backward_a(dD, W, plan).shape == (0, 64)
+    out = torch.full((2, 32, 64), 3.0, device="cuda")
+    assert torch.all(g.gemm_experts_backward_w(dD, A, plan, beta=2.0, C=out.clone(), out=out) == 6)
+    assert torch.all(g.gemm_experts_backward_w(dD, A, plan, out=out) == 0)
+    plan = plan_of([4, 5], 1)
+    none = torch.empty(10, 0, device="cuda", dtype=BF16)
+    assert torch.all(g.gemm_experts(none, torch.empty(2, 32, 0, device="cuda", dtype=BF16), plan) == 0)
+    assert torch.all(g.gemm_experts_backward_a(none, torch.empty(2, 0, 32, device="cuda", dtype=BF16), plan) == 0)
+    assert g.gemm_experts_backward_w(none, none, plan).shape == (2, 0, 0)
+    status()
