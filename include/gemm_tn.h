@@ -626,8 +626,7 @@ int gemm_w4_tn_experts(const gemm_expert_plan *plan, const void *A, int64_t lda,
  * A, dD and W are bf16 and 16-byte aligned with leading dimensions and strides
  * that are multiples of 8 (GEMM_ERR_MISALIGNED otherwise).  D, dA, dW and C
  * are bf16 or fp32 (out_dtype) and may have any alignment to their element
- * size; with addresses, pitches, strides and row lengths of whole 16 bytes they
- * are written by TMA, which is faster.  Outputs must not overlap operands other than C.
+ * size (bf16 with odd pitches or row lengths is slower).  Outputs must not overlap operands other than C.
  * Sums are fp32 and rounded once; their order does not change from run to run.
  * activation is a gemm_activation; the gradients are those of the product
  * without it.

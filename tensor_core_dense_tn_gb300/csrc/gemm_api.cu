@@ -1043,6 +1043,31 @@ int check_stride(const char* what, int64_t E, int64_t rows, int64_t ld, int64_t 
   return GEMM_OK;
 }
 
+// Map of an MN-major operand: a matrix of rows x cols (stride = 0), or `count`
+// of them with the expert as its last coordinate; boxes of 64 columns x box_rows rows.  With
+// chunks > 0 the columns are split into {64, cols / 64} (which takes whole
+// chunks: the view has no end inside one), and a box holds that many chunks.
+int encode_chunks(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t count, int64_t ld, int64_t stride,
+                  int box_rows, int chunks, const char* what) {
+  cuuint64_t dims[4], strides[3];
+  cuuint32_t box[4], estr[4] = {1, 1, 1, 1};
+  int n = 0;
+  auto dim = [&](int64_t size, int64_t step, int in_box) {
+    dims[n] = (cuuint64_t)size;
+    if (n) strides[n - 1] = (cuuint64_t)step * 2;
+    box[n++] = (cuuint32_t)in_box;
+  };
+  dim(chunks ? 64 : cols, 1, 64);
+  dim(rows, ld, box_rows);
+  if (chunks) dim(cols / 64, 64, chunks);
+  if (stride) dim(count, stride, 1);
+  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(GEMM_ERR_LAUNCH, "cuTensorMapEncodeTiled(%s) failed with %d", what, (int)r);
+  return GEMM_OK;
+}
+
 // op: kExpertsForward (X = A), kExpertsRows (X = dD) with out = R rows, or
 // kExpertsWeights (X = dD, Y = A) with out = E matrices of N x K.
 int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, const void* X, int64_t ldx, const void* Y,
@@ -1103,43 +1128,46 @@ int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, cons
   p.act = activation;
   p.alpha = alpha;
   p.beta = beta;
-  auto on16 = [&](const void* base, int64_t ld, int64_t stride) {
-    return aligned16(base) && ld * esize % 16 == 0 && (!weights || stride * esize % 16 == 0);
+  auto even = [&](const void* base, int64_t ld, int64_t stride) {
+    return aligned_to(base, 4) && ld % 2 == 0 && (!weights || stride % 2 == 0);
   };
-  // A TMA store clips a row's end to whole 16 bytes only: it would write into
-  // the padding behind rows that end inside them.
-  p.direct = cols * esize % 16 || !on16(D, ldd, stride_d) || (p.has_c && !on16(C, ldc, stride_c));
+  p.pairs = cols % 2 == 0 && even(D, ldd, stride_d) && (!p.has_c || even(C, ldc, stride_c));
   p.timeout_ns = timeout_ns(nullptr);
   p.status = st->status;
   experts_geometry(&p, st->sms);
-  const int64_t tile_rows = 128 * p.cg;
-  const int64_t tiles_n = (cols + p.bn - 1) / p.bn;
-  const int64_t blocks = weights ? E * ((N + tile_rows - 1) / tile_rows) : R / tile_rows + E + 1;
-  if (tiles_n * blocks >= kMaxDim - 4096) return fail(GEMM_ERR_INVALID_VALUE, "too many tiles");
-  p.tiles_n = (int)tiles_n;
-  p.tiles_m = weights ? (int)((N + tile_rows - 1) / tile_rows) : 0;
-  p.strip = weights ? 8 : raster_group_for((int)tile_rows, sum, 2, 16);
-  CUtensorMap tA, tB, tC, tD;
-  memset(&tA, 0, sizeof tA);
-  tB = tC = tD = tA;
-  const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+  const int64_t col_blocks = (cols + 128 * p.cg - 1) / (128 * p.cg);
+  const int64_t row_blocks = (N + p.tile_rows - 1) / p.tile_rows;     // of the weights' gradient
+  const int64_t most = weights ? E * row_blocks : R / p.tile_rows + E + 1;
+  if (col_blocks * most >= kMaxDim - 4096) return fail(GEMM_ERR_INVALID_VALUE, "too many tiles");
+  p.col_blocks = (int)col_blocks;
+  p.row_blocks = weights ? (int)row_blocks : 0;
+  p.strip = weights ? 8 : raster_group_for(p.tile_rows, sum, 2, 16);
+  ExpertsMaps maps;
+  memset(&maps, 0, sizeof maps);
   if (p.has_ab) {
-    if ((rc = encode_2d(&tA, bf16, 2, X, op == kExpertsForward ? K : N, R, ldx, 64, p.a_rows, sw, "rows"))) return rc;
-    if (weights) rc = encode_2d(&tB, bf16, 2, Y, K, R, ldy, 64, 64, sw, "A");
-    else rc = encode_3d(&tB, bf16, 2, Y, K, N, E, ldy, stride_y, 64, op == kExpertsForward ? p.bn / p.cg : 64, sw, "W");
-    if (rc) return rc;
-  }
-  if (!p.direct) {
-    const CUtensorMapDataType dt = p.out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : bf16;
-    const CUtensorMapSwizzle so = CU_TENSOR_MAP_SWIZZLE_64B;
-    if (!weights) rc = encode_2d(&tD, dt, esize, D, cols, R, ldd, 64 / esize, 32, so, dname);
-    else rc = encode_3d(&tD, dt, esize, D, cols, N, E, ldd, stride_d, 64 / esize, 32, so, dname);
-    if (!rc && p.has_c) rc = encode_3d(&tC, dt, esize, C, cols, N, E, ldc, stride_c, 64 / esize, 32, so, "C");
-    if (rc) return rc;
+    const CUtensorMapDataType bf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
+    if (weights) {
+      p.wide_cols = K % 64 == 0;
+      p.wide_rows = N % (64 * p.cg) == 0;
+      const int chunks = p.tile_rows / p.cg / 64;
+      if ((rc = encode_chunks(&maps.cols, Y, K, R, 1, ldy, 0, 64, p.wide_cols ? 2 : 0, "A")) ||
+          (rc = encode_chunks(&maps.cols_part, Y, K, R, 1, ldy, 0, 16, p.wide_cols ? 2 : 0, "A")) ||
+          (rc = encode_chunks(&maps.rows, X, N, R, 1, ldx, 0, 64, p.wide_rows ? chunks : 0, "dD")) ||
+          (rc = encode_chunks(&maps.rows_part, X, N, R, 1, ldx, 0, 16, p.wide_rows ? chunks : 0, "dD")))
+        return rc;
+    } else {
+      const int64_t S = p.S;
+      p.wide_cols = op == kExpertsRows && K % 64 == 0;
+      if (op == kExpertsForward) rc = encode_3d(&maps.cols, bf16, 2, Y, K, N, E, ldy, stride_y, 64, 128, sw, "W");
+      else rc = encode_chunks(&maps.cols, Y, K, N, E, ldy, stride_y, 64, p.wide_cols ? 2 : 0, "W");
+      if (rc || (rc = encode_2d(&maps.rows, bf16, 2, X, S, R, ldx, 64, p.row_box, sw, "rows")) ||
+          (rc = encode_2d(&maps.rows_part, bf16, 2, X, S, R, ldx, 64, p.row_box / 2, sw, "rows")))
+        return rc;
+    }
   }
   LaunchInfo li = {};
-  return finish_launch(launch_experts(tA, tB, tC, tD, p, st->sms, static_cast<cudaStream_t>(stream_v), &li), li);
+  return finish_launch(launch_experts(maps, p, st->sms, static_cast<cudaStream_t>(stream_v), &li), li);
 }
 
 }  // namespace

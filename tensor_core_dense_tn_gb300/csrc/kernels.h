@@ -202,7 +202,14 @@ cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, int sms, cu
 
 // bf16 products by expert and their gradients (gemm_experts.cu).
 constexpr int kExpertsForward = 0, kExpertsRows = 1, kExpertsWeights = 2;
-constexpr int kExpertsMaxBoxes = 8;       // staged boxes per epilogue warp
+
+// n / d for 0 <= n < 2^31 as (n * mul) >> (32 + shift): with 2^s >= d the
+// multiplier is ceil(2^(31 + s) / d), shift s - 1; its excess over the exact
+// quotient times n stays below one part in d.  mul = 0 for d = 1.
+struct FastDiv {
+  uint32_t mul, shift;
+};
+FastDiv fast_div(uint32_t d);
 
 struct ExpertsParams {
   int op;              // kExperts*
@@ -215,24 +222,33 @@ struct ExpertsParams {
   void* D; long long ldd, stride_d;        // elements
   const void* C; long long ldc, stride_c;  // weights: read where has_c
   int has_c, out_f32, act;
-  int direct;          // D or C is not on 16 bytes: no TMA for them
+  int pairs;           // bf16 D and C: even pitches and row lengths on 4 bytes, moved two columns at a time
   float alpha, beta;
-  int cg, bn, a_rows;  // CTAs per tile, columns per tile, rows of A per TMA box
-  int a_bytes, b_bytes, stages, boxes;     // ring stage per CTA, stages, staged boxes per epilogue warp
-  int tiles_m, tiles_n;                    // weights: per expert; else tiles_n alone
+  int cg, tile_rows;   // CTAs per tile (of 128 columns each), most rows per tile
+  int row_box;         // forward, rows: rows of their operand per TMA box (a CTA's share of a tile)
+  int wide_cols, wide_rows;                // MN-major operands: one box for all of a CTA's columns (or rows) of a stage
+  int row_bytes;       // rows' operand in a ring stage of a CTA
+  int stages, acc_cols;                    // ring stages, columns of one accumulator
+  int row_blocks, col_blocks;              // weights: tiles of a matrix; else col_blocks alone
   int strip;           // row blocks per strip of the tile order
+  FastDiv by_cols, by_tiles, by_strip, by_strip_tiles;   // launch: col_blocks, tiles of a matrix, strip, strip * col_blocks
   uint64_t timeout_ns;
   int* status;
 };
 
-// Chooses the tile shape (cg, bn, a_rows, stages, boxes) from op, R, E, the
-// output's columns and has_c.
+// Chooses the tile shape (cg, tile_rows and what follows from them) from op, R and E.
 void experts_geometry(ExpertsParams* p, int sms);
-// tmA: rows of the first operand {columns, rows}, 64 x a_rows boxes (weights:
-// 64 x 64), tmB: the second, boxes of 64 x bn / cg (forward) or 64 x 64; 128-byte
-// swizzle.  tmC, tmD: the output, 64 bytes x 32 rows, 64-byte swizzle, 3D for weights.
-cudaError_t launch_experts(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmC, const CUtensorMap& tmD,
-                           ExpertsParams p, int sms, cudaStream_t stream, LaunchInfo* info);
+// The operands' tensor maps (128-byte swizzle):
+// cols  the operand of the output's columns: forward, W in boxes of 64 x 128;
+//       rows, W, and weights, A, in boxes of 64 columns x 64 rows, with
+//       wide_cols as {64, row, chunk of 64 columns (, expert)} and two chunks
+// rows  that of its rows: 64 x row_box; weights, dD as `cols`, with wide_rows
+//       tile_rows / cg / 64 chunks
+// part  weights: the same with 16 rows; else rows in boxes half as high
+struct ExpertsMaps {
+  CUtensorMap cols, rows, cols_part, rows_part;
+};
+cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cudaStream_t stream, LaunchInfo* info);
 
 struct LaunchInfo {
   int path;            // 1 = 1-SM tiled, 2 = 2-SM tiled, 3 = skinny
