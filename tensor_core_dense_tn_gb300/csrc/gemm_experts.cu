@@ -60,7 +60,7 @@ constexpr int kBlockK = 64;                // summation indices per ring stage
 constexpr int kChunkBytes = 64 * 128;      // 64 rows of 64 bf16: a chunk of an MN-major operand
 constexpr int kPartBytes = 16 * 128;       // 16 rows of it: a chunk of a sum's last, shorter block
 constexpr int kColBytes = 128 * 128;       // a stage of the columns' operand: 128 of them per CTA
-constexpr int kEpiWarps = 8;               // two for each quarter of Tensor Memory's lanes
+constexpr int kEpiWarps = 8;               // four for each accumulator, one for each quarter of its lanes
 constexpr int kErrTimeout = -5;            // GEMM_ERR_TIMEOUT
 constexpr int kMaxStages = 16;
 
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), kEpiWarps * CG);
+      mbar_init(acce_bar(b), kEpiWarps / 2 * CG);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -500,35 +500,47 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
         if (!wait_bar<kPair>(acce_bar(acc), acc_phase ^ 1, ab)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * p.acc_cols);
-        for (int kb = 0; kb < r.num_kb; ++kb) {
-          ok = wait_bar<kPair>(full_bar(stage), phase, ab);
-          if (ok && ragged(r) && kb + 1 == r.num_kb) {
-            ok = wait_bar<kPair>(ready_bar(stage), (ready_phase >> stage) & 1u, ab);
-            ready_phase ^= 1u << stage;
-          }
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t c = sC + stage * kColBytes, b = sR + stage * p.row_bytes;
-          const int left = r.k_end - r.k0 - kb * kBlockK;
-          const bool part = S_::kWeights && left < kBlockK;
-          const int chunk = part ? kPartBytes : kChunkBytes;
-          const uint64_t c0 = S_::kMnCols ? desc_mn(c, chunk) : smem_desc_sw128(c);
-          const uint64_t b0 = S_::kMnRows ? desc_mn(b, chunk) : smem_desc_sw128(b);
-          // 16 summation indices are 32 bytes of a K-major operand's rows, 16 rows of each chunk of an MN-major one
-          // (the chunks of a part lie together)
-          const uint32_t step_c = !S_::kMnCols ? 2 : part ? kColBytes / 4 / 16 : kPartBytes / 16;
-          const uint32_t step_b = !S_::kMnRows ? 2 : part ? p.row_bytes / 4 / 16 : kPartBytes / 16;
-          const int steps = part ? (left + 15) / 16 : 4;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (i < steps)
-              mma_issue<CG, kKindF16>(d_tmem, c0 + step_c * i, b0 + step_b * i, idesc, (kb != 0 || i != 0) ? 1u : 0u);
+        auto hand_back = [&] {
           if constexpr (kPair) mma_commit_pair(empty_bar(stage), 0x3);
           else mma_commit(empty_bar(stage));
           if (++stage == p.stages) {
             stage = 0;
             phase ^= 1;
           }
+        };
+        // Whole blocks; the last, shorter one apart: with the two in one loop,
+        // and so its steps and strides in registers, the MMAs came with pauses
+        // (2048 rows for each of 8 matrices of 8192 x 4096: 747 us, apart 625).
+        const int whole = S_::kWeights ? (r.k_end - r.k0) / kBlockK : r.num_kb;
+        for (int kb = 0; kb < whole; ++kb) {
+          ok = wait_bar<kPair>(full_bar(stage), phase, ab);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t c = sC + stage * kColBytes, b = sR + stage * p.row_bytes;
+          const uint64_t c0 = S_::kMnCols ? desc_mn(c, kChunkBytes) : smem_desc_sw128(c);
+          const uint64_t b0 = S_::kMnRows ? desc_mn(b, kChunkBytes) : smem_desc_sw128(b);
+          // 16 summation indices are 32 bytes of a K-major operand's rows, 16 rows of each chunk of an MN-major one
+          constexpr uint64_t kStepC = S_::kMnCols ? kPartBytes / 16 : 2, kStepR = S_::kMnRows ? kPartBytes / 16 : 2;
+#pragma unroll
+          for (int i = 0; i < kBlockK / 16; ++i)
+            mma_issue<CG, kKindF16>(d_tmem, c0 + kStepC * i, b0 + kStepR * i, idesc, (kb != 0 || i != 0) ? 1u : 0u);
+          hand_back();
+        }
+        if (S_::kWeights && ok && whole < r.num_kb) {
+          ok = wait_bar<kPair>(full_bar(stage), phase, ab);
+          if (ok && ragged(r)) {
+            ok = wait_bar<kPair>(ready_bar(stage), (ready_phase >> stage) & 1u, ab);
+            ready_phase ^= 1u << stage;
+          }
+          if (!ok) break;
+          tc_fence_after();
+          // parts of 16 rows, each with its chunks together
+          const int parts = (r.k_end - r.k0 - whole * kBlockK + 15) / 16;
+          for (int i = 0; i < parts; ++i)
+            mma_issue<CG, kKindF16>(d_tmem, desc_mn(sC + stage * kColBytes + i * (kColBytes / 4), kPartBytes),
+                                    desc_mn(sR + stage * p.row_bytes + i * (p.row_bytes / 4), kPartBytes), idesc,
+                                    (whole != 0 || i != 0) ? 1u : 0u);
+          hand_back();
         }
         if (!ok) break;
         if constexpr (kPair) mma_commit_pair(accf_bar(acc), 0x3);
@@ -545,14 +557,15 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
   } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
-    const int c_first = (warp - 2) / 4 * 32;  // of every 64 rows the first or the second 32
+    // Four warps take the tiles of one accumulator, four those of the other:
+    // while some store, the others wait for sums, read and convert.
+    const int acc = (warp - 2) / 4;
     Abort ab{abort_flag, p.timeout_ns, p.status, kRoleEpilogue};
     const bool f32 = p.out_f32, pairs = p.pairs;
     const int esize = f32 ? 4 : 2;
-    int acc = 0;
     uint32_t acc_phase = 0;
-    const uint32_t acce_target = kPair ? mapa_shared(acce_bar(0), 0) : acce_bar(0);
-    for (int t = first_tile; t < num_tiles; t += step) {
+    const uint32_t acce_target = kPair ? mapa_shared(acce_bar(acc), 0) : acce_bar(acc);
+    for (int t = first_tile + acc * step; t < num_tiles; t += 2 * step) {
       const Tile r = tile_of<CG, OP>(t, p, tb);
       const int col = r.col0 + (int)rank * 128 + q * 32 + lane;
       const bool mine = col < p.cols_out;
@@ -563,12 +576,12 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
       [[maybe_unused]] uint32_t xc[32];
       if constexpr (OP == kExpertsWeights)
         if (p.has_c)
-          load_c(element(p.C, p.ldc, p.stride_c, r.row0 + c_first), p.ldc, r.rows - c_first, mine, f32, pairs, xc);
+          load_c(element(p.C, p.ldc, p.stride_c, r.row0), p.ldc, r.rows, mine, f32, pairs, xc);
       // (the whole warp leaves, or none of it: what follows is warp-wide)
       if (!__all_sync(0xffffffffu, wait_bar<kPair>(accf_bar(acc), acc_phase, ab))) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int c = c_first; c < r.rows; c += 64) {
+      for (int c = 0; c < r.rows; c += 32) {
         float v[32];
         if (r.num_kb > 0) {
           uint32_t x[32];
@@ -584,8 +597,8 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
         if constexpr (OP == kExpertsWeights) {
           if (p.has_c) {
             add_c(xc, p.beta, f32, pairs, v);
-            if (c + 64 < r.rows)      // the next rows of C are on their way while these are stored
-              load_c(element(p.C, p.ldc, p.stride_c, r.row0 + c + 64), p.ldc, r.rows - c - 64, mine, f32, pairs, xc);
+            if (c + 32 < r.rows)      // the next rows of C are on their way while these are stored
+              load_c(element(p.C, p.ldc, p.stride_c, r.row0 + c + 32), p.ldc, r.rows - c - 32, mine, f32, pairs, xc);
           }
         }
         uint8_t* to = element(p.D, p.ldd, p.stride_d, r.row0 + c);
@@ -596,12 +609,11 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (kPair) mbar_arrive_cluster(acce_target + 8u * acc);
+        if constexpr (kPair) mbar_arrive_cluster(acce_target);
         else mbar_arrive(acce_bar(acc));
       }
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1;
+      acc_phase ^= 1;
     }
   } else if constexpr (S_::kWeights) {
     // ------------------------------------------------------------ ragged blocks
