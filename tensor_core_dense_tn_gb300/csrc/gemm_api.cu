@@ -1135,7 +1135,7 @@ int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, cons
   p.timeout_ns = timeout_ns(nullptr);
   p.status = st->status;
   experts_geometry(&p, st->sms);
-  const int64_t col_blocks = (cols + 128 * p.cg - 1) / (128 * p.cg);
+  const int64_t col_blocks = (cols + p.col_tile * p.cg - 1) / (p.col_tile * p.cg);
   const int64_t row_blocks = (N + p.tile_rows - 1) / p.tile_rows;     // of the weights' gradient
   const int64_t most = weights ? E * row_blocks : R / p.tile_rows + E + 1;
   if (col_blocks * most >= kMaxDim - 4096) return fail(GEMM_ERR_INVALID_VALUE, "too many tiles");
@@ -1154,16 +1154,16 @@ int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, cons
       if ((rc = encode_chunks(&maps.cols, Y, K, R, 1, ldy, 0, 64, p.wide_cols ? 2 : 0, "A")) ||
           (rc = encode_chunks(&maps.cols_part, Y, K, R, 1, ldy, 0, 16, p.wide_cols ? 2 : 0, "A")) ||
           (rc = encode_chunks(&maps.rows, X, N, R, 1, ldx, 0, 64, p.wide_rows ? chunks : 0, "dD")) ||
-          (rc = encode_chunks(&maps.rows_part, X, N, R, 1, ldx, 0, 16, p.wide_rows ? chunks : 0, "dD")))
+          (rc = encode_chunks(&maps.rows_part[0], X, N, R, 1, ldx, 0, 16, p.wide_rows ? chunks : 0, "dD")))
         return rc;
     } else {
       const int64_t S = p.S;
       p.wide_cols = op == kExpertsRows && K % 64 == 0;
-      if (op == kExpertsForward) rc = encode_3d(&maps.cols, bf16, 2, Y, K, N, E, ldy, stride_y, 64, 128, sw, "W");
+      if (op == kExpertsForward) rc = encode_3d(&maps.cols, bf16, 2, Y, K, N, E, ldy, stride_y, 64, p.col_tile, sw, "W");
       else rc = encode_chunks(&maps.cols, Y, K, N, E, ldy, stride_y, 64, p.wide_cols ? 2 : 0, "W");
-      if (rc || (rc = encode_2d(&maps.rows, bf16, 2, X, S, R, ldx, 64, p.row_box, sw, "rows")) ||
-          (rc = encode_2d(&maps.rows_part, bf16, 2, X, S, R, ldx, 64, p.row_box / 2, sw, "rows")))
-        return rc;
+      if (rc || (rc = encode_2d(&maps.rows, bf16, 2, X, S, R, ldx, 64, p.row_box, sw, "rows"))) return rc;
+      for (int i = 0; i < 3 && p.row_box >= 64; ++i)
+        if ((rc = encode_2d(&maps.rows_part[i], bf16, 2, X, S, R, ldx, 64, (i + 1) * (p.row_box / 4), sw, "rows"))) return rc;
     }
   }
   LaunchInfo li = {};

@@ -60,7 +60,6 @@ constexpr int kBlockK = 64;                // summation indices per ring stage
 constexpr int kChunkBytes = 64 * 128;      // 64 rows of 64 bf16: a chunk of an MN-major operand
 constexpr int kPartBytes = 16 * 128;       // 16 rows of it: a chunk of a sum's last, shorter block
 constexpr int kColBytes = 128 * 128;       // a stage of the columns' operand: 128 of them per CTA
-constexpr int kEpiWarps = 8;               // four for each accumulator, one for each quarter of its lanes
 constexpr int kErrTimeout = -5;            // GEMM_ERR_TIMEOUT
 constexpr int kMaxStages = 16;
 
@@ -68,6 +67,12 @@ template <int OP>
 struct Shape {
   static constexpr bool kWeights = OP == kExpertsWeights;
   static constexpr bool kMnCols = OP != kExpertsForward, kMnRows = kWeights;   // operands that are MN-major
+  // Storing warps, half of them for each accumulator, and the rows that one
+  // takes at a time.  With more of them more of C is on its way (64 matrices of
+  // 2048 x 2048 fp32 with C: 16 warps 404 us, 8 424); a product's long sums hide
+  // the stores of 8 (one prompt through 128 experts: 818 us, with 16 840).
+  static constexpr int kEpiWarps = kWeights ? 16 : 8;
+  static constexpr int kRowsAtOnce = kWeights ? 16 : 32;
   static constexpr int kThreads = 32 * (2 + kEpiWarps + (kWeights ? 1 : 0));
 };
 
@@ -228,7 +233,7 @@ __device__ __forceinline__ Tile tile_of(int t, const ExpertsParams& p, const Tab
     cb = sh == p.strip ? div_by(in, p.by_strip) : in / sh;
     rb = s0 + in - cb * sh;
   }
-  r.col0 = cb * (128 * CG);
+  r.col0 = cb * (p.col_tile * CG);
   r.row0 = first + rb * each;
   r.rows = min(each, high - rb * each);
   r.n = (r.rows + kStep - 1) / kStep * kStep;
@@ -284,25 +289,47 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* m, bo
 }
 
 // ---------------------------------------------------------------- epilogue
-// Values of 32 rows of one column per lane, lane l on column `col` + l, to or
+// The logistic activations for a result that is rounded to bf16: __expf, whose
+// error grows with its argument (2^-22 of the value for each unit of it, below
+// 2^-15 up to the cap of 80), instead of expf.  Far below the rounding's 2^-9, and
+// less work beside the MMAs.
+template <int NR>
+__device__ __forceinline__ void logistic_rows(float (&v)[NR], bool gelu) {
+#pragma unroll
+  for (int j = 0; j < NR; ++j) {
+    const float t = gelu ? -1.5957691216057308f * fmaf(0.044715f * v[j], v[j] * v[j], v[j]) : -v[j];
+    v[j] = __fdividef(v[j], 1.0f + __expf(fminf(t, 80.0f)));
+  }
+}
+
+template <int NR>
+__device__ __forceinline__ void activate_rows(float (&v)[NR], int act, bool f32) {
+  if (!f32 && act == kActSilu) logistic_rows(v, false);
+  else if (!f32 && act == kActGeluTanh) logistic_rows(v, true);
+  else activate_chunk(v, act);
+}
+
+// Values of NR rows of one column per lane, lane l on column `col` + l, to or
 // from a row-major matrix at `base` (its element (first row, col)).  fp32 rows
 // are 128 contiguous bytes of a warp.  bf16: in pairs, where the addresses
 // allow: an even lane moves both columns of its pair in one row, the odd lane
 // in the next, so that a step moves two rows of 64 bytes.
-__device__ __forceinline__ void store_rows_f32(float* at, long long ld, int rows, bool mine, const float (&v)[32]) {
+template <int NR>
+__device__ __forceinline__ void store_rows_f32(float* at, long long ld, int rows, bool mine, const float (&v)[NR]) {
   if (!mine) return;
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
+  for (int j = 0; j < NR; ++j)
     if (j < rows) at[j * ld] = v[j];
 }
 
+template <int NR>
 __device__ __forceinline__ void store_rows_bf16(uint16_t* at, long long ld, int rows, bool mine, bool pairs,
-                                                const float (&v)[32]) {
+                                                const float (&v)[NR]) {
   const int odd = threadIdx.x & 1;
   if (pairs) {
     uint32_t* to = reinterpret_cast<uint32_t*>(at - odd + odd * ld);
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
+    for (int j = 0; j < NR; j += 2) {
       const float give = odd ? v[j] : v[j + 1];
       const float got = __shfl_xor_sync(0xffffffffu, give, 1);
       const uint32_t w = odd ? pack_bf16x2(got, v[j + 1]) : pack_bf16x2(v[j], got);
@@ -310,38 +337,43 @@ __device__ __forceinline__ void store_rows_bf16(uint16_t* at, long long ld, int 
     }
   } else if (mine) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
+    for (int j = 0; j < NR; ++j)
       if (j < rows) at[j * ld] = (uint16_t)(pack_bf16x2(v[j], 0.0f) & 0xFFFFu);
   }
 }
 
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&x)[32]) { tmem_ld_32x32b_x32(taddr, x); }
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&x)[16]) { tmem_ld_32x32b_x16(taddr, x); }
+
 // C's raw words as store_rows_* would write them; unpack_c turns them into values.
+template <int NR>
 __device__ __forceinline__ void load_c(const void* base, long long ld, int rows, bool mine, bool f32, bool pairs,
-                                       uint32_t (&x)[32]) {
+                                       uint32_t (&x)[NR]) {
   const int odd = threadIdx.x & 1;
   if (f32) {
     const uint32_t* at = static_cast<const uint32_t*>(base);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = mine && j < rows ? at[j * ld] : 0;
+    for (int j = 0; j < NR; ++j) x[j] = mine && j < rows ? at[j * ld] : 0;
   } else if (pairs) {
     const uint32_t* at = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) - odd + odd * ld);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] = mine && 2 * j + odd < rows ? at[j * ld] : 0;
+    for (int j = 0; j < NR / 2; ++j) x[j] = mine && 2 * j + odd < rows ? at[j * ld] : 0;
   } else {
     const uint16_t* at = static_cast<const uint16_t*>(base);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = mine && j < rows ? at[j * ld] : 0;
+    for (int j = 0; j < NR; ++j) x[j] = mine && j < rows ? at[j * ld] : 0;
   }
 }
 
-__device__ __forceinline__ void add_c(const uint32_t (&x)[32], float beta, bool f32, bool pairs, float (&v)[32]) {
+template <int NR>
+__device__ __forceinline__ void add_c(const uint32_t (&x)[NR], float beta, bool f32, bool pairs, float (&v)[NR]) {
   const int odd = threadIdx.x & 1;
   if (f32) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = fmaf(beta, __uint_as_float(x[j]), v[j]);
+    for (int j = 0; j < NR; ++j) v[j] = fmaf(beta, __uint_as_float(x[j]), v[j]);
   } else if (pairs) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
+    for (int j = 0; j < NR / 2; ++j) {
       const uint32_t o = __shfl_xor_sync(0xffffffffu, x[j], 1);
       const float a = __uint_as_float(odd ? o & 0xFFFF0000u : x[j] << 16);      // row 2j, this lane's column
       const float b = __uint_as_float(odd ? x[j] & 0xFFFF0000u : o << 16);      // row 2j + 1
@@ -350,7 +382,7 @@ __device__ __forceinline__ void add_c(const uint32_t (&x)[32], float beta, bool 
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = fmaf(beta, __uint_as_float(x[j] << 16), v[j]);
+    for (int j = 0; j < NR; ++j) v[j] = fmaf(beta, __uint_as_float(x[j] << 16), v[j]);
   }
 }
 
@@ -358,6 +390,7 @@ template <int CG, int OP>
 __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     gemm_experts_kernel(const __grid_constant__ ExpertsMaps maps, const __grid_constant__ ExpertsParams p) {
   using S_ = Shape<OP>;
+  constexpr int kEpiWarps = S_::kEpiWarps, kRowsAtOnce = S_::kRowsAtOnce;
   constexpr bool kPair = CG == 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -403,7 +436,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
       tma_prefetch_desc(&maps.cols);
       tma_prefetch_desc(&maps.rows);
       if (S_::kWeights) tma_prefetch_desc(&maps.cols_part);
-      tma_prefetch_desc(&maps.rows_part);
+      for (int i = 0; i < (S_::kWeights ? 1 : p.row_box < 64 ? 0 : 3); ++i) tma_prefetch_desc(&maps.rows_part[i]);
     }
   }
   if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), 2 * p.acc_cols);
@@ -432,13 +465,15 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
       uint32_t phase = 0;
       for (int t = first_tile; t < num_tiles && ok; t += step) {
         const Tile r = tile_of<CG, OP>(t, p, tb);
-        const int c_at = r.col0 + (int)rank * 128;
+        const int c_at = r.col0 + (int)rank * p.col_tile;
         const int share = r.n / CG;            // this CTA's share of the tile's rows
         const int r_at = r.row0 + (int)rank * share;
-        const bool half = !S_::kWeights && share <= p.row_box / 2;
+        // the smallest box that holds the share: whole, 3/4, 1/2 or 1/4 (of at least 64 rows, else whole)
+        const int box = S_::kWeights || p.row_box < 64 ? 3 : (4 * share - 1) / p.row_box;
         const int chunks = p.wide_rows ? p.row_bytes / kChunkBytes : (share + 63) / 64;    // weights
         const uint32_t tx =
-            (uint32_t)(kColBytes + (S_::kWeights ? chunks * kChunkBytes : half ? p.row_box / 2 * 128 : p.row_box * 128));
+            (uint32_t)(p.col_tile * 128 + (S_::kWeights ? chunks * kChunkBytes : (box + 1) * (p.row_box / 4) * 128));
+        const CUtensorMap* row_map = box == 3 ? &maps.rows : &maps.rows_part[box];
         for (int kb = 0; kb < r.num_kb; ++kb) {
           if (!wait_bar<kPair>(empty_bar(stage), phase ^ 1, ab)) {
             ok = false;
@@ -465,16 +500,16 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
               const uint32_t ci = c + i * (kColBytes / 4), bi = b + i * (p.row_bytes / 4);
               if (own) {
                 load_cols<OP, false>(ci, &maps.cols_part, p.wide_cols, c_at, k + 16 * i, r.e, kPartBytes, tail);
-                load_rows<OP, false>(bi, &maps.rows_part, p.wide_rows, r_at, k + 16 * i, kPartBytes, chunks, tail);
+                load_rows<OP, false>(bi, &maps.rows_part[0], p.wide_rows, r_at, k + 16 * i, kPartBytes, chunks, tail);
               } else {
                 load_cols<OP, kPair>(ci, &maps.cols_part, p.wide_cols, c_at, k + 16 * i, r.e, kPartBytes, to);
-                load_rows<OP, kPair>(bi, &maps.rows_part, p.wide_rows, r_at, k + 16 * i, kPartBytes, chunks, to);
+                load_rows<OP, kPair>(bi, &maps.rows_part[0], p.wide_rows, r_at, k + 16 * i, kPartBytes, chunks, to);
               }
             }
           } else {
             if (leader) mbar_arrive_expect_tx(fb, tx * CG);
             load_cols<OP, kPair>(c, &maps.cols, p.wide_cols, c_at, k, r.e, kChunkBytes, to);
-            load_rows<OP, kPair>(b, half ? &maps.rows_part : &maps.rows, p.wide_rows, r_at, k, kChunkBytes, chunks, to);
+            load_rows<OP, kPair>(b, row_map, p.wide_rows, r_at, k, kChunkBytes, chunks, to);
           }
           if (++stage == p.stages) {
             stage = 0;
@@ -557,9 +592,10 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
   } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
-    // Four warps take the tiles of one accumulator, four those of the other:
+    // Half of the warps take the tiles of one accumulator, half those of the other:
     // while some store, the others wait for sums, read and convert.
-    const int acc = (warp - 2) / 4;
+    const int acc = (warp - 2) / (kEpiWarps / 2), c_first = (warp - 2) / 4 % (kEpiWarps / 8) * kRowsAtOnce;
+    constexpr int kRowStep = kEpiWarps / 8 * kRowsAtOnce;
     Abort ab{abort_flag, p.timeout_ns, p.status, kRoleEpilogue};
     const bool f32 = p.out_f32, pairs = p.pairs;
     const int esize = f32 ? 4 : 2;
@@ -567,38 +603,40 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     const uint32_t acce_target = kPair ? mapa_shared(acce_bar(acc), 0) : acce_bar(acc);
     for (int t = first_tile + acc * step; t < num_tiles; t += 2 * step) {
       const Tile r = tile_of<CG, OP>(t, p, tb);
-      const int col = r.col0 + (int)rank * 128 + q * 32 + lane;
-      const bool mine = col < p.cols_out;
+      const int col = r.col0 + (int)rank * p.col_tile + q * 32 + lane;
+      const bool mine = q * 32 + lane < p.col_tile && col < p.cols_out;
       auto element = [&](const void* base, long long ld, long long stride, int row) {
         return const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) +
                ((OP == kExpertsWeights ? (long long)r.e * stride : 0) + (long long)row * ld + col) * esize;
       };
-      [[maybe_unused]] uint32_t xc[32];
+      [[maybe_unused]] uint32_t xc[kRowsAtOnce];
       if constexpr (OP == kExpertsWeights)
         if (p.has_c)
-          load_c(element(p.C, p.ldc, p.stride_c, r.row0), p.ldc, r.rows, mine, f32, pairs, xc);
+          load_c(element(p.C, p.ldc, p.stride_c, r.row0 + c_first), p.ldc, r.rows - c_first, mine, f32, pairs, xc);
       // (the whole warp leaves, or none of it: what follows is warp-wide)
       if (!__all_sync(0xffffffffu, wait_bar<kPair>(accf_bar(acc), acc_phase, ab))) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int c = 0; c < r.rows; c += 32) {
-        float v[32];
+      for (int c = c_first; c < r.rows; c += kRowStep) {
+        float v[kRowsAtOnce];
         if (r.num_kb > 0) {
-          uint32_t x[32];
-          tmem_ld_32x32b_x32(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * p.acc_cols + c), x);
+          uint32_t x[kRowsAtOnce];
+          tmem_ld_rows(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * p.acc_cols + c), x);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = p.alpha * __uint_as_float(x[j]);
+          for (int j = 0; j < kRowsAtOnce; ++j) v[j] = p.alpha * __uint_as_float(x[j]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+          for (int j = 0; j < kRowsAtOnce; ++j) v[j] = 0.0f;
         }
-        if constexpr (OP == kExpertsForward) activate_chunk(v, p.act);
+        if constexpr (OP == kExpertsForward) activate_rows(v, p.act, f32);
         if constexpr (OP == kExpertsWeights) {
           if (p.has_c) {
             add_c(xc, p.beta, f32, pairs, v);
-            if (c + 32 < r.rows)      // the next rows of C are on their way while these are stored
-              load_c(element(p.C, p.ldc, p.stride_c, r.row0 + c + 32), p.ldc, r.rows - c - 32, mine, f32, pairs, xc);
+            // the next rows of C are on their way while these are stored
+            const int next = c + kRowStep;
+            if (next < r.rows)
+              load_c(element(p.C, p.ldc, p.stride_c, r.row0 + next), p.ldc, r.rows - next, mine, f32, pairs, xc);
           }
         }
         uint8_t* to = element(p.D, p.ldd, p.stride_d, r.row0 + c);
@@ -679,7 +717,11 @@ void experts_geometry(ExpertsParams* p, int sms) {
   const bool weights = p->op == kExpertsWeights;
   const int active = p->E < p->R ? p->E : p->R;       // experts that can have rows
   const int average = active > 0 ? p->R / active : 0;
-  p->cg = weights || average >= 48 ? 2 : 1;
+  // Pairs halve what a CTA loads of the other operand.  Where the output's
+  // memory decides, single CTAs, which need not wait for each other, are faster
+  // (weights, 61 matrices of 1000 x 2000 bf16 for 3 rows each: 65 us, pairs 72; 64
+  // of 2048 x 2048 fp32 with C for 256: 404, 421; without C 235, 226).
+  p->cg = average >= (weights ? (p->has_c ? 512 : 128) : 48) ? 2 : 1;
   const int step = 16 * p->cg;
   const int most = 2 * average < 32 ? 32 : 2 * average;
   p->tile_rows = weights || most > 256 ? 256 : (most + 31) / 32 * 32;
@@ -687,6 +729,21 @@ void experts_geometry(ExpertsParams* p, int sms) {
   const int share = p->tile_rows / p->cg;
   p->row_box = share;
   p->row_bytes = weights ? share / 64 * kChunkBytes : (share * 128 + 1023) / 1024 * 1024;
+  // Few rows: W's bytes decide, and each CTA takes the same number of them when
+  // the tiles' columns are chosen so that the rounds of tiles are full (16
+  // tokens through 2 of 8 matrices of 4096 x 4096: 256 tiles of 128 columns on 152
+  // SMs take two rounds; 296 tiles of 112 columns too).
+  p->col_tile = 128;
+  if (p->op == kExpertsForward && p->cg == 1) {
+    long long best = 0;
+    for (int c = 128; c >= 64; c -= 16) {
+      const long long tiles = (long long)active * ((p->cols_out + c - 1) / c), time = (tiles + sms - 1) / sms * c;
+      if (!best || time < best) {
+        best = time;
+        p->col_tile = c;
+      }
+    }
+  }
   p->acc_cols = 32;
   while (p->acc_cols < p->tile_rows) p->acc_cols *= 2;
   p->stages = 0;

@@ -224,7 +224,8 @@ struct ExpertsParams {
   int has_c, out_f32, act;
   int pairs;           // bf16 D and C: even pitches and row lengths on 4 bytes, moved two columns at a time
   float alpha, beta;
-  int cg, tile_rows;   // CTAs per tile (of 128 columns each), most rows per tile
+  int cg, tile_rows;   // CTAs per tile, most rows per tile
+  int col_tile;        // columns per CTA of a tile, at most 128 (forward: any multiple of 16; else 128)
   int row_box;         // forward, rows: rows of their operand per TMA box (a CTA's share of a tile)
   int wide_cols, wide_rows;                // MN-major operands: one box for all of a CTA's columns (or rows) of a stage
   int row_bytes;       // rows' operand in a ring stage of a CTA
@@ -240,13 +241,13 @@ struct ExpertsParams {
 void experts_geometry(ExpertsParams* p, int sms);
 // The operands' tensor maps (128-byte swizzle):
 // cols  the operand of the output's columns: forward, W in boxes of 64 x 128;
-//       rows, W, and weights, A, in boxes of 64 columns x 64 rows, with
+//       (of 64 x col_tile); rows, W, and weights, A, in boxes of 64 columns x 64 rows, with
 //       wide_cols as {64, row, chunk of 64 columns (, expert)} and two chunks
 // rows  that of its rows: 64 x row_box; weights, dD as `cols`, with wide_rows
 //       tile_rows / cg / 64 chunks
-// part  weights: the same with 16 rows; else rows in boxes half as high
+// part  weights: the same with 16 rows; else rows in boxes of 1/4, 1/2 and 3/4 of the height (row_box of 64 and more)
 struct ExpertsMaps {
-  CUtensorMap cols, rows, cols_part, rows_part;
+  CUtensorMap cols, rows, cols_part, rows_part[3];
 };
 cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cudaStream_t stream, LaunchInfo* info);
 
