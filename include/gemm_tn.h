@@ -648,6 +648,41 @@ int gemm_bf16_tn_experts_backward_w(const gemm_expert_plan *plan, int64_t N, int
                                     void *dW, int64_t lddw, int64_t stride_dw, float alpha, float beta,
                                     int out_dtype, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The norm of many gradient tensors, and clipping by it.
+ *
+ *     norm = sqrt(sum of x^2 over all values of all tensors)
+ *     gemm_clip_grad_norm:  y = x * (max_norm / norm) where norm > max_norm,
+ *                           y = x otherwise
+ *
+ * Squares are summed so that no finite value overflows or is lost whatever its
+ * size (fp32 sums of 32 squares, added in fp64), in an order that does not
+ * change from run to run; the norm is stored as fp32 (infinity where it is
+ * larger).  A norm that is not finite, because a value is not, leaves the
+ * values as they are.  In place, values that need not be scaled are not
+ * written.
+ *
+ * The lists are host arrays, read during the call only; the tensors are dense
+ * (count consecutive values) device memory aligned to their element size, of
+ * any types mixed.  out: NULL for in place, else one tensor for each input with
+ * its count, of either type; an output is its input's own memory or overlaps
+ * no tensor.  norm: one fp32 in device memory.  workspace: device memory of
+ * gemm_grad_workspace(num) bytes, 8-byte aligned, whose contents do not matter;
+ * calls that may run at the same time need one each.  No other memory is used,
+ * so the calls may be captured and replayed on any stream. */
+typedef struct gemm_tensor {
+  void *data;
+  int64_t count;
+  int dtype;           /* GEMM_OUT_BF16 or GEMM_OUT_F32 */
+} gemm_tensor;
+
+int64_t gemm_grad_workspace(int num);
+
+int gemm_grad_norm(int num, const gemm_tensor *tensors, float *norm, void *workspace, void *stream);
+
+int gemm_clip_grad_norm(int num, const gemm_tensor *tensors, float max_norm, const gemm_tensor *out, float *norm,
+                        void *workspace, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -41,7 +42,8 @@ EXPORTED = ["gemm_bf16_tn", "gemm_bf16_tn_ex", "gemm_get_status", "gemm_get_stat
             "gemm_bf16_tn_grouped", "gemm_bf16_tn_batched", "gemm_plan", "gemm_stream_read",
             "gemm_mma_rate", "gemm_fp8_tn_bias_act", "gemm_expert_dispatch", "gemm_expert_dispatch_backward",
             "gemm_expert_combine", "gemm_expert_combine_backward", "gemm_w4_tn", "gemm_w4_tn_experts",
-            "gemm_bf16_tn_experts", "gemm_bf16_tn_experts_backward_a", "gemm_bf16_tn_experts_backward_w"]
+            "gemm_bf16_tn_experts", "gemm_bf16_tn_experts_backward_a", "gemm_bf16_tn_experts_backward_w",
+            "gemm_grad_workspace", "gemm_grad_norm", "gemm_clip_grad_norm"]
 
 FP8_E4M3, FP8_E5M2 = 0, 1
 SCHED_DEFAULT, SCHED_STATIC, SCHED_CLC = 0, 1, 2
@@ -108,6 +110,11 @@ class W4MatrixInfo(ctypes.Structure):
                 ("zeros", ctypes.c_void_p), ("ldz", ctypes.c_int64), ("stride_zeros", ctypes.c_int64)]
 
 
+class TensorInfo(ctypes.Structure):
+    """gemm_tensor: a dense tensor of gemm_grad_norm and gemm_clip_grad_norm."""
+    _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -170,6 +177,12 @@ def load(path: str = LIB_PATH):
         lib.gemm_bf16_tn_experts_backward_w.argtypes = [plan, i64, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64,
                                                         f32, f32, i32, vp]
         lib.gemm_bf16_tn_experts_backward_w.restype = i32
+        lib.gemm_grad_workspace.argtypes = [i32]
+        lib.gemm_grad_workspace.restype = i64
+        lib.gemm_grad_norm.argtypes = [i32, vp, vp, vp, vp]
+        lib.gemm_grad_norm.restype = i32
+        lib.gemm_clip_grad_norm.argtypes = [i32, vp, f32, vp, vp, vp, vp]
+        lib.gemm_clip_grad_norm.restype = i32
         lib.gemm_get_status.argtypes = [vp]
         lib.gemm_get_status.restype = i32
         lib.gemm_get_status_detail.restype = i32
@@ -391,6 +404,21 @@ def gemm_bf16_tn_experts_backward_w(plan, N, K, dD, lddd, A, lda, C, ldc, stride
     """Raw C-ABI call: dW_e = alpha * dD_e^T * A_e + beta * C_e."""
     return load().gemm_bf16_tn_experts_backward_w(plan, N, K, dD or None, lddd, A or None, lda, C or None, ldc, stride_c,
                                                   dW or None, lddw, stride_dw, alpha, beta, out_dtype, stream or None)
+
+
+def gemm_grad_workspace(num) -> int:
+    """Bytes of workspace for gemm_grad_norm and gemm_clip_grad_norm of `num` tensors."""
+    return load().gemm_grad_workspace(num)
+
+
+def gemm_grad_norm(num, tensors, norm, workspace, stream) -> int:
+    """Raw C-ABI call (tensors: an array of TensorInfo)."""
+    return load().gemm_grad_norm(num, tensors, norm or None, workspace or None, stream or None)
+
+
+def gemm_clip_grad_norm(num, tensors, max_norm, out, norm, workspace, stream) -> int:
+    """Raw C-ABI call (tensors, out: arrays of TensorInfo; out None: in place)."""
+    return load().gemm_clip_grad_norm(num, tensors, max_norm, out, norm or None, workspace or None, stream or None)
 
 
 _torch = None
@@ -760,3 +788,100 @@ def gemm_experts_backward_w(dD, A, plan: ExpertPlan, alpha: float = 1.0, beta: f
     if rc:
         _check(rc)
     return out
+
+
+def _dense(t):
+    """Whether t's values fill their memory without gaps and none is there twice, in whatever order of dimensions."""
+    step = 1
+    for stride, size in sorted(zip(t.stride(), t.shape)):
+        if size != 1:
+            if stride != step:
+                return False
+            step *= size
+    return True
+
+
+def _tensor_list(tensors, what):
+    """gemm_tensor array (three 64-bit words each) of dense bf16 and fp32 tensors, as bytes, their counts, their GPU, and
+    whether all are contiguous.  One comprehension per property and struct.pack: for a list of small gradients this is
+    most of a call (a ctypes array filled from the words takes six times as long as the bytes)."""
+    gpus = {t.get_device() for t in tensors}
+    if len(gpus) > 1:
+        raise ValueError(f"all {what} must be on one GPU")
+    gpu = gpus.pop() if gpus else _torch.cuda.current_device()
+    if gpu or _several_gpus:
+        _gpu_of(gpu, f"{what}: a tensor")
+    words = [0] * (3 * len(tensors))
+    words[0::3] = [t.data_ptr() for t in tensors]
+    words[1::3] = counts = [t.numel() for t in tensors]
+    words[2::3] = codes = [_CODES.get(t.dtype) for t in tensors]
+    if None in codes:
+        raise ValueError(f"{what} must be bf16 or fp32, not {tensors[codes.index(None)].dtype}")
+    flat = all([t.is_contiguous() for t in tensors])
+    if not flat:
+        for i, t in enumerate(tensors):
+            if t.numel() and not t.is_contiguous() and not _dense(t):
+                raise ValueError(f"{what}: tensor {i} must be dense, not {tuple(t.shape)} with strides {t.stride()}")
+    return struct.pack(f"={len(words)}q", *words), counts, gpu, flat
+
+
+def _norm_buffers(num, gpu, norm, stream):
+    """The norm's place and the workspace.  A fresh norm is the first value of the workspace's tensor, so that both
+    live as long; beside a caller's, the workspace is kept for the stream that uses it."""
+    torch = _torch
+    nbytes = (_lib or load()).gemm_grad_workspace(num)
+    buf = torch.empty(nbytes // 4 + 4, dtype=torch.float32, device=torch.device("cuda", gpu))
+    work = buf.data_ptr() + 16
+    if norm is None:
+        return buf[0], buf.data_ptr(), work
+    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != gpu:
+        raise ValueError(f"norm must be one fp32 on GPU {gpu}")
+    if stream:
+        buf.record_stream(torch.cuda.ExternalStream(stream, device=gpu))
+    return norm, norm.data_ptr(), work
+
+
+def grad_norm(tensors, norm=None, stream=None):
+    """sqrt of the sum of the squares of all values of `tensors` (dense bf16 and fp32 CUDA tensors, mixed), as an fp32
+    tensor without dimensions, or in `norm`.  Nothing waits for the GPU."""
+    _torch or _t()
+    tensors = list(tensors)
+    words, _, gpu, _ = _tensor_list(tensors, "tensors")
+    norm, at, work = _norm_buffers(len(tensors), gpu, norm, stream)
+    s = _torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream
+    rc = (_lib or load()).gemm_grad_norm(len(tensors), words, at, work, s or None)
+    if rc:
+        _check(rc)
+    return norm
+
+
+def clip_grad_norm(tensors, max_norm: float, out=None, norm=None, stream=None):
+    """Multiplies all values by max_norm / norm where their norm (grad_norm()) is above max_norm, in place, or into the
+    tensors `out` (bf16 or fp32, contiguous for contiguous tensors, else of their strides; also where nothing is
+    scaled).  Returns the norm from
+    before.  A norm that is not finite changes nothing.  In place, values within max_norm are not written; the
+    tensors' versions count as changed all the same."""
+    torch = _torch or _t()
+    tensors = list(tensors)
+    words, counts, gpu, flat = _tensor_list(tensors, "tensors")
+    to = None
+    if out is not None:
+        out = list(out)
+        to, counts_out, gpu_out, flat_out = _tensor_list(out, "out")
+        if counts_out != counts:
+            raise ValueError("out must have a tensor of the same size for each tensor")
+        if gpu_out != gpu:
+            raise ValueError("tensors and out must be on one GPU")
+        if not (flat and flat_out):
+            for i, (o, t) in enumerate(zip(out, tensors)):
+                if t.numel() and not (o.is_contiguous() and t.is_contiguous()) and \
+                        (o.shape != t.shape or o.stride() != t.stride()):
+                    raise ValueError(f"out: tensor {i} must have its tensor's shape and order of dimensions")
+    norm, at, work = _norm_buffers(len(tensors), gpu, norm, stream)
+    s = torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream
+    rc = (_lib or load()).gemm_clip_grad_norm(len(tensors), words, max_norm, to, at, work, s or None)
+    if rc:
+        _check(rc)
+    if out is None:
+        torch._C._increment_version(tuple([t for t in tensors if not t.is_inference()]))
+    return norm

@@ -1170,6 +1170,54 @@ int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, cons
   return finish_launch(launch_experts(maps, p, st->sms, static_cast<cudaStream_t>(stream_v), &li), li);
 }
 
+// ---------------------------------------------------------------- gradient norm
+// out: nullptr = in place.  Without `clip` only the norm.
+int run_grad_norm(int num, const gemm_tensor* tensors, bool clip, float max_norm, const gemm_tensor* out, float* norm,
+                  void* workspace, void* stream_v) {
+  t_error.clear();
+  if (num < 0) return fail(GEMM_ERR_INVALID_VALUE, "negative number of tensors %d", num);
+  if (num > 0 && !tensors) return fail(GEMM_ERR_INVALID_VALUE, "tensors is NULL");
+  if (!norm || !aligned_to(norm, 4)) return fail(norm ? GEMM_ERR_MISALIGNED : GEMM_ERR_INVALID_VALUE, "norm must be an fp32 in GPU memory");
+  if (clip && !(max_norm >= 0.0f)) return fail(GEMM_ERR_INVALID_VALUE, "max_norm must not be negative or NaN");
+  if (!workspace) return fail(GEMM_ERR_INVALID_VALUE, "workspace is NULL");
+  if (!aligned_to(workspace, 8)) return fail(GEMM_ERR_MISALIGNED, "workspace must be 8-byte aligned");
+  static thread_local std::vector<GradTensor> list;
+  list.clear();
+  list.reserve(num);
+  for (int i = 0; i < num; ++i) {
+    const gemm_tensor& t = tensors[i];
+    const gemm_tensor& o = out ? out[i] : t;
+    if (t.count < 0 || t.count >= (int64_t)1 << 44 || (t.dtype != GEMM_OUT_BF16 && t.dtype != GEMM_OUT_F32))
+      return fail(GEMM_ERR_INVALID_VALUE, "tensor %d: a count in [0, 2^44) and a dtype of 0 (bf16) or 1 (fp32) are needed, got %lld, %d",
+                  i, (long long)t.count, t.dtype);
+    if (o.count != t.count || (o.dtype != GEMM_OUT_BF16 && o.dtype != GEMM_OUT_F32))
+      return fail(GEMM_ERR_INVALID_VALUE, "output %d must have its tensor's count and be bf16 or fp32", i);
+    if (t.count == 0) continue;
+    const int is = dtype_bytes(t.dtype), os = dtype_bytes(o.dtype);
+    if (!t.data || !o.data) return fail(GEMM_ERR_INVALID_VALUE, "tensor %d is NULL", i);
+    if (!aligned_to(t.data, is) || !aligned_to(o.data, os))
+      return fail(GEMM_ERR_MISALIGNED, "tensor %d must be aligned to its element size", i);
+    GradTensor g = {};
+    g.in = t.data;
+    g.out = o.data;
+    g.count = t.count;
+    g.in_f32 = t.dtype == GEMM_OUT_F32;
+    g.out_f32 = o.dtype == GEMM_OUT_F32;
+    const int64_t head = (int64_t)((16 - reinterpret_cast<uintptr_t>(t.data) % 16) % 16) / is;
+    g.head = (uint8_t)(head < t.count ? head : t.count);
+    g.vector = aligned16(static_cast<const char*>(o.data) + (int64_t)g.head * os);
+    list.push_back(g);
+  }
+  int dev = 0;
+  DeviceState* st = nullptr;
+  int rc = init_device(&dev, &st);
+  if (rc) return rc;
+  LaunchInfo li = {};
+  return finish_launch(launch_grad_norm(list.data(), (int)list.size(), clip, out == nullptr, max_norm, norm,
+                                        static_cast<double*>(workspace), st->sms, static_cast<cudaStream_t>(stream_v), &li),
+                       li);
+}
+
 }  // namespace
 
 // Sets the text gemm_last_error_string returns on this thread, for entry
@@ -1326,6 +1374,17 @@ int gemm_bf16_tn_experts_backward_w(const gemm_expert_plan* plan, int64_t N, int
                                     void* stream) {
   return gtn::run_experts(gtn::kExpertsWeights, plan, N, K, dD, lddd, A, lda, 0, C, ldc, stride_c, dW, lddw, stride_dw,
                           alpha, beta, out_dtype, GEMM_ACT_NONE, stream);
+}
+
+int64_t gemm_grad_workspace(int num) { return num < 0 ? 0 : 8 * gtn::grad_partials(num > 0 ? num : 1); }
+
+int gemm_grad_norm(int num, const gemm_tensor* tensors, float* norm, void* workspace, void* stream) {
+  return gtn::run_grad_norm(num, tensors, false, 0.0f, nullptr, norm, workspace, stream);
+}
+
+int gemm_clip_grad_norm(int num, const gemm_tensor* tensors, float max_norm, const gemm_tensor* out, float* norm,
+                        void* workspace, void* stream) {
+  return gtn::run_grad_norm(num, tensors, true, max_norm, out, norm, workspace, stream);
 }
 
 int gemm_plan(int64_t M, int64_t N, int64_t K, int fp8_inputs, int num_sms, const gemm_tn_config* cfg,

@@ -1,0 +1,395 @@
+// The norm of many gradient tensors, and clipping by it (sm_103a).
+//
+//   norm = sqrt(sum over all tensors and values of x^2)
+//   clip: y = x * c,  c = max_norm / norm where norm > max_norm, else 1
+//
+// Memory bounds both: the norm reads every value once, a clip that has to
+// scale reads it again and writes it once (between the two lies the sum of all
+// of them).  So:
+// - The tensors' addresses travel in the kernel's parameters (a list of 64, or
+//   of 960 for longer ones), no table is copied to the GPU, and one launch
+//   takes all of them: work is cut into chunks of 32 KB, and a block takes every
+//   G-th chunk of the whole list, with the next one's loads in flight.
+// - The clip's second pass runs through the chunks backwards: what the first
+//   pass read last is still in L2 (about 100 MB of it).  Its stores are
+//   streaming, so that they do not push it out.
+// - Sums.  A thread adds 32 squares (16 of fp32 values) in fp32, in four chains
+//   (an error of at most 11 steps of 2^-24), and these sums in fp64: one fp64 addition per 32
+//   values is within what the SMs can do at the memory's rate, one per value
+//   is not.  Where the fp32 sum overflowed, or is so small that squares may
+//   have been lost, the values are squared again in fp64.  So the norm is
+//   right over the whole range of values, and infinite or NaN only if a value is.
+// - No atomics: a block's sum goes to its place in the workspace, and each
+//   block that needs the total adds all places in the same order.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kernels.h"
+#include "ptx.cuh"
+
+namespace gtn {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kBlocksPerSm = 2;
+constexpr int kVectors = 4;              // 16-byte vectors per thread and chunk
+constexpr int kChunkVectors = kThreads * kVectors;
+constexpr int kSmallList = 64;
+
+template <int CAP>
+struct List {
+  GradTensor t[CAP];
+  int count;           // tensors in this launch
+  int chunks;          // of all of them
+};
+
+struct Task {
+  double* partial;     // sums of the blocks of this launch (squares), or of all launches (finish, clip)
+  int partials;
+  float max_norm;
+  float* norm;         // finish, and the first block of a clip
+};
+
+// The values of a vector, 4 fp32 or 8 bf16.
+template <bool F32>
+__device__ __forceinline__ void unpack(uint4 a, float (&v)[F32 ? 4 : 8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (F32) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  }
+}
+
+__device__ __forceinline__ float load1(const void* base, bool f32, long long i) {
+  return f32 ? static_cast<const float*>(base)[i]
+             : __uint_as_float((uint32_t) static_cast<const uint16_t*>(base)[i] << 16);
+}
+
+__device__ __forceinline__ void store1(void* base, bool f32, long long i, float v) {
+  if (f32) static_cast<float*>(base)[i] = v;
+  else static_cast<uint16_t*>(base)[i] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+}
+
+// The tensor of a chunk: the last whose first chunk is not past it, in [lo, hi].
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const List<CAP>& l, int chunk, int lo, int hi) {
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (l.t[mid].first <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A chunk's place: its tensor, this thread's first vector and their number.
+struct Place {
+  const uint4* in;
+  long long at, vectors;
+  int tensor;
+};
+
+template <int CAP>
+__device__ __forceinline__ Place place_of(const List<CAP>& l, int chunk, int lo, int hi) {
+  Place r;
+  r.tensor = tensor_of(l, chunk, lo, hi);
+  const GradTensor& t = l.t[r.tensor];
+  const int size = t.in_f32 ? 4 : 2;
+  r.in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(t.in) + t.head * size);
+  r.vectors = (t.count - t.head) * size / 16;
+  r.at = (long long)(chunk - t.first) * kChunkVectors + threadIdx.x;
+  return r;
+}
+
+__device__ __forceinline__ void load_vectors(const Place& r, uint4 (&x)[kVectors]) {
+#pragma unroll
+  for (int u = 0; u < kVectors; ++u)
+    x[u] = r.at + u * kThreads < r.vectors ? r.in[r.at + u * kThreads] : make_uint4(0, 0, 0, 0);
+}
+
+// The values of a tensor before its first vector and behind its last, one per
+// thread of the first 16: calls f(index).
+template <typename F>
+__device__ __forceinline__ void for_ends(const GradTensor& t, long long vectors, F f) {
+  if (threadIdx.x < 16) {
+    const long long i = threadIdx.x < 8 ? threadIdx.x : t.head + vectors * (t.in_f32 ? 4 : 8) + (threadIdx.x - 8);
+    if (threadIdx.x < 8 ? i < t.head : i < t.count) f(i);
+  }
+}
+
+// The sum over the block, in every thread; the order is fixed.
+__device__ __forceinline__ double block_sum(double v, double* shared) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) s += shared[i];
+  return s;
+}
+
+// The squares of vectors in fp64, for fp32 sums that hold too little or too
+// much; vectors of zeros add nothing without fp64 work.
+template <bool F32>
+__device__ __noinline__ double squares64(uint4 a, uint4 b, uint4 c, uint4 d) {
+  double s = 0.0;
+#pragma unroll 1
+  for (int u = 0; u < kVectors; ++u) {
+    const uint4 x = u == 0 ? a : u == 1 ? b : u == 2 ? c : d;
+    if (((x.x | x.y | x.z | x.w) & (F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) continue;
+    float v[F32 ? 4 : 8];
+    unpack<F32>(x, v);
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 8); ++i) s += (double)v[i] * (double)v[i];
+  }
+  return s;
+}
+
+template <bool F32>
+__device__ __forceinline__ double squares(const uint4 (&x)[kVectors]) {
+  float s[kVectors] = {};
+#pragma unroll
+  for (int u = 0; u < kVectors; ++u) {
+    float v[F32 ? 4 : 8];
+    unpack<F32>(x[u], v);
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 8); ++i) s[u] = fmaf(v[i], v[i], s[u]);
+  }
+  const float all = (s[0] + s[1]) + (s[2] + s[3]);
+  // Squares below 2^-126 lose bits, or all: with a sum above 2^-80 what is
+  // lost is below 2^-41 of it.
+  if (all >= 0x1p-80f && all <= 0x1p127f) return (double)all;
+  return squares64<F32>(x[0], x[1], x[2], x[3]);
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    grad_squares_kernel(const __grid_constant__ List<CAP> l, const Task k) {
+  __shared__ double shared[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  double sum = 0.0;
+  int chunk = blockIdx.x;
+  Place r = place_of(l, chunk, 0, l.count - 1);
+  uint4 x[kVectors];
+  load_vectors(r, x);
+  while (true) {
+    // the next chunk's vectors are on their way while these are summed
+    const int next = chunk + gridDim.x;
+    const bool more = next < l.chunks;
+    Place rn = r;
+    uint4 y[kVectors];
+    if (more) {
+      const bool same = r.tensor + 1 == l.count || l.t[r.tensor + 1].first > next;
+      if (same) rn.at += (long long)gridDim.x * kChunkVectors;
+      else rn = place_of(l, next, r.tensor + 1, l.count - 1);
+      load_vectors(rn, y);
+    }
+    const GradTensor& t = l.t[r.tensor];
+    sum += t.in_f32 ? squares<true>(x) : squares<false>(x);
+    if (chunk == t.first)
+      for_ends(t, r.vectors, [&](long long i) {
+        const double v = load1(t.in, t.in_f32, i);
+        sum += v * v;
+      });
+    if (!more) break;
+    chunk = next;
+    r = rn;
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) x[u] = y[u];
+  }
+  sum = block_sum(sum, shared);
+  if (threadIdx.x == 0) k.partial[blockIdx.x] = sum;
+}
+
+__device__ __forceinline__ double total(const Task& k, double* shared) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < k.partials; i += kThreads) s += k.partial[i];
+  return sqrt(block_sum(s, shared));
+}
+
+// A vector's values times both factors, to their place in `out`.
+template <bool F32>
+__device__ __forceinline__ void store_scaled(uint8_t* out, long long at, uint4 x, float first, float c, bool out_f32) {
+  constexpr int kPer = F32 ? 4 : 8;
+  float v[kPer];
+  unpack<F32>(x, v);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) v[i] = v[i] * first * c;
+  if (out_f32) {
+    float4* to = reinterpret_cast<float4*>(out) + at * (kPer / 4);
+#pragma unroll
+    for (int i = 0; i < kPer / 4; ++i) __stcs(to + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+  } else {
+    uint2* to = reinterpret_cast<uint2*>(out) + at * (kPer / 4);
+    if constexpr (F32)
+      __stcs(to, make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
+    else
+      __stcs(reinterpret_cast<uint4*>(to), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) grad_finish_kernel(const Task k) {
+  __shared__ double shared[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const double norm = total(k, shared);
+  if (threadIdx.x == 0) *k.norm = (float)norm;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+    grad_clip_kernel(const __grid_constant__ List<CAP> l, const Task k, bool in_place) {
+  __shared__ double shared[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const double norm = total(k, shared);
+  if (k.norm && blockIdx.x == 0 && threadIdx.x == 0) *k.norm = (float)norm;
+  // (false for a norm of NaN; an infinite one leaves the values alone too)
+  const bool scale = norm > (double)k.max_norm && norm <= 1.7976931348623157e308;
+  if (!scale && in_place) return;
+  // Two factors, the first a power of two: a single one below 2^-126 (a norm
+  // beyond fp32) would lose bits.
+  const double exact = scale ? (double)k.max_norm / norm : 1.0;
+  const float first = exact < 0x1p-100 ? 0x1p-64f : 1.0f;
+  const float c = (float)(exact < 0x1p-100 ? exact * 0x1p64 : exact);
+  // backwards through the chunks, the next one's vectors on their way while these are scaled
+  int chunk = l.chunks - 1 - (int)blockIdx.x;
+  Place r = place_of(l, chunk, 0, l.count - 1);
+  uint4 x[kVectors];
+  if (l.t[r.tensor].vector) load_vectors(r, x);
+  while (true) {
+    const int next = chunk - (int)gridDim.x;
+    Place rn = r;
+    uint4 y[kVectors];
+    if (next >= 0) {
+      if (l.t[r.tensor].first <= next) rn.at -= (long long)gridDim.x * kChunkVectors;
+      else rn = place_of(l, next, 0, r.tensor - 1);
+      if (l.t[rn.tensor].vector) load_vectors(rn, y);
+    }
+    const GradTensor& t = l.t[r.tensor];
+    const bool in_f32 = t.in_f32, out_f32 = t.out_f32;
+    if (t.vector) {
+      uint8_t* out = static_cast<uint8_t*>(t.out) + t.head * (out_f32 ? 4 : 2);
+#pragma unroll
+      for (int u = 0; u < kVectors; ++u)
+        if (r.at + u * kThreads < r.vectors) {
+          if (in_f32) store_scaled<true>(out, r.at + u * kThreads, x[u], first, c, out_f32);
+          else store_scaled<false>(out, r.at + u * kThreads, x[u], first, c, out_f32);
+        }
+    } else {
+      // out does not lie as in does: value by value, neighbours by neighbouring threads
+      const int per = in_f32 ? 4 : 8;
+      const long long begin = t.head + (r.at - threadIdx.x) * per;
+      const long long end = min(begin + (long long)kChunkVectors * per, t.head + r.vectors * per);
+      for (long long j = begin + threadIdx.x; j < end; j += kThreads)
+        store1(t.out, out_f32, j, load1(t.in, in_f32, j) * first * c);
+    }
+    if (chunk == t.first)
+      for_ends(t, r.vectors, [&](long long j) { store1(t.out, out_f32, j, load1(t.in, in_f32, j) * first * c); });
+    if (next < 0) break;
+    chunk = next;
+    r = rn;
+#pragma unroll
+    for (int u = 0; u < kVectors; ++u) x[u] = y[u];
+  }
+}
+
+int blocks_for(int chunks, int sms) {
+  const int most = kBlocksPerSm * sms < kGradMaxBlocks ? kBlocksPerSm * sms : kGradMaxBlocks;
+  return chunks < most ? chunks : most;
+}
+
+template <typename... Args>
+cudaError_t launch(const void* kernel, int grid, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  void* pointers[] = {const_cast<void*>(static_cast<const void*>(args))...};
+  return cudaLaunchKernelExC(&cfg, kernel, pointers);
+}
+
+// One pass of a kernel over `count` tensors, kGradMaxTensors per launch.
+// `first_partial` gets each launch's place in the workspace.
+template <typename Fill>
+cudaError_t passes(const GradTensor* tensors, int count, bool clip, bool in_place, int sms, cudaStream_t stream, Fill fill,
+                   LaunchInfo* info) {
+  static thread_local List<kGradMaxTensors> list;
+  for (int at = 0; at < count; at += kGradMaxTensors) {
+    const int n = count - at < kGradMaxTensors ? count - at : kGradMaxTensors;
+    long long chunks = 0;
+    for (int i = 0; i < n; ++i) {
+      GradTensor& t = list.t[i];
+      t = tensors[at + i];
+      t.first = (int)chunks;
+      const long long vectors = (t.count - t.head) * (t.in_f32 ? 4 : 2) / 16;
+      chunks += vectors > 0 ? (vectors + kChunkVectors - 1) / kChunkVectors : 1;
+      if (chunks >= (1ll << 31) - 4096) return cudaErrorInvalidValue;
+    }
+    list.count = n;
+    list.chunks = (int)chunks;
+    const int grid = blocks_for((int)chunks, sms);
+    Task task = fill(at / kGradMaxTensors, grid);
+    cudaError_t e;
+    if (n <= kSmallList) {
+      static thread_local List<kSmallList> small;
+      for (int i = 0; i < n; ++i) small.t[i] = list.t[i];
+      small.count = n;
+      small.chunks = list.chunks;
+      e = clip ? launch((const void*)grad_clip_kernel<kSmallList>, grid, stream, &small, &task, &in_place)
+               : launch((const void*)grad_squares_kernel<kSmallList>, grid, stream, &small, &task);
+    } else {
+      e = clip ? launch((const void*)grad_clip_kernel<kGradMaxTensors>, grid, stream, &list, &task, &in_place)
+               : launch((const void*)grad_squares_kernel<kGradMaxTensors>, grid, stream, &list, &task);
+    }
+    if (e != cudaSuccess) return e;
+    info->grid = grid;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+long long grad_partials(int count) {
+  return (long long)kGradMaxBlocks * ((count + kGradMaxTensors - 1) / kGradMaxTensors);
+}
+
+cudaError_t launch_grad_norm(const GradTensor* tensors, int count, bool clip, bool in_place, float max_norm, float* norm,
+                             double* workspace, int sms, cudaStream_t stream, LaunchInfo* info) {
+  *info = LaunchInfo{};
+  info->cluster = 1;
+  info->block = kThreads;
+  info->kernel = clip ? "grad_clip_kernel" : "grad_squares_kernel";
+  // the launches' sums, one behind the other without gaps
+  int used = 0;
+  cudaError_t e = passes(tensors, count, false, false, sms, stream, [&](int, int grid) {
+    Task t = {workspace + used, 0, 0.0f, nullptr};
+    used += grid;
+    return t;
+  }, info);
+  if (e != cudaSuccess) return e;
+  if (!clip || count == 0) {
+    Task t = {workspace, used, 0.0f, norm};
+    return launch((const void*)grad_finish_kernel, 1, stream, &t);
+  }
+  return passes(tensors, count, true, in_place, sms, stream, [&](int launch_index, int) {
+    return Task{workspace, used, max_norm, launch_index == 0 ? norm : nullptr};
+  }, info);
+}
+
+}  // namespace gtn

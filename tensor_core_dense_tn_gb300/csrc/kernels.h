@@ -251,6 +251,24 @@ struct ExpertsMaps {
 };
 cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cudaStream_t stream, LaunchInfo* info);
 
+// The norm of gradient tensors and clipping by it (grad_norm.cu).
+constexpr int kGradMaxTensors = 960;      // per launch: 30 KB of the 32 KB of kernel parameters
+constexpr int kGradMaxBlocks = 512;       // per launch: its places in the workspace
+
+struct GradTensor {
+  const void* in;
+  void* out;           // clip; `in` itself in place
+  int64_t count;       // values, at least one
+  int first;           // launch: its first chunk
+  uint8_t in_f32, out_f32;
+  uint8_t head;        // values before the first 16-byte boundary of `in`
+  uint8_t vector;      // clip: `out` lies on 16 bytes behind as many
+};
+
+long long grad_partials(int count);       // doubles of workspace for `count` tensors
+cudaError_t launch_grad_norm(const GradTensor* tensors, int count, bool clip, bool in_place, float max_norm, float* norm,
+                             double* workspace, int sms, cudaStream_t stream, LaunchInfo* info);
+
 struct LaunchInfo {
   int path;            // 1 = 1-SM tiled, 2 = 2-SM tiled, 3 = skinny
   int grid, cluster, block;
