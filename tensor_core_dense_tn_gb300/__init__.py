@@ -803,7 +803,7 @@ def _dense(t):
 
 def _tensor_list(tensors, what):
     """gemm_tensor array (three 64-bit words each) of dense bf16 and fp32 tensors, as bytes, their counts, their GPU, and
-    whether all are contiguous.  One comprehension per property and struct.pack: for a list of small gradients this is
+    whether all are contiguous.  One pass per property and struct.pack: for a list of small gradients this is
     most of a call (a ctypes array filled from the words takes six times as long as the bytes)."""
     gpus = {t.get_device() for t in tensors}
     if len(gpus) > 1:
@@ -812,12 +812,13 @@ def _tensor_list(tensors, what):
     if gpu or _several_gpus:
         _gpu_of(gpu, f"{what}: a tensor")
     words = [0] * (3 * len(tensors))
-    words[0::3] = [t.data_ptr() for t in tensors]
-    words[1::3] = counts = [t.numel() for t in tensors]
+    Tensor = _torch.Tensor
+    words[0::3] = [*map(Tensor.data_ptr, tensors)]
+    words[1::3] = counts = [*map(Tensor.numel, tensors)]
     words[2::3] = codes = [_CODES.get(t.dtype) for t in tensors]
     if None in codes:
         raise ValueError(f"{what} must be bf16 or fp32, not {tensors[codes.index(None)].dtype}")
-    flat = all([t.is_contiguous() for t in tensors])
+    flat = all(map(Tensor.is_contiguous, tensors))
     if not flat:
         for i, t in enumerate(tensors):
             if t.numel() and not t.is_contiguous() and not _dense(t):
@@ -825,20 +826,21 @@ def _tensor_list(tensors, what):
     return struct.pack(f"={len(words)}q", *words), counts, gpu, flat
 
 
+_GRAD_WORKSPACE = {}        # number of tensors -> bytes
+
+
 def _norm_buffers(num, gpu, norm, stream):
-    """The norm's place and the workspace.  A fresh norm is the first value of the workspace's tensor, so that both
-    live as long; beside a caller's, the workspace is kept for the stream that uses it."""
+    """The norm's tensor and the workspace, which is kept for the stream that uses it."""
     torch = _torch
-    nbytes = (_lib or load()).gemm_grad_workspace(num)
-    buf = torch.empty(nbytes // 4 + 4, dtype=torch.float32, device=torch.device("cuda", gpu))
-    work = buf.data_ptr() + 16
+    nbytes = _GRAD_WORKSPACE.get(num) or _GRAD_WORKSPACE.setdefault(num, (_lib or load()).gemm_grad_workspace(num))
+    work = torch.empty(nbytes, dtype=torch.uint8, device=gpu)
     if norm is None:
-        return buf[0], buf.data_ptr(), work
-    if norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != gpu:
+        norm = torch.empty((), dtype=torch.float32, device=gpu)
+    elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != gpu:
         raise ValueError(f"norm must be one fp32 on GPU {gpu}")
     if stream:
-        buf.record_stream(torch.cuda.ExternalStream(stream, device=gpu))
-    return norm, norm.data_ptr(), work
+        work.record_stream(torch.cuda.ExternalStream(stream, device=gpu))
+    return norm, work
 
 
 def grad_norm(tensors, norm=None, stream=None):
@@ -847,9 +849,9 @@ def grad_norm(tensors, norm=None, stream=None):
     _torch or _t()
     tensors = list(tensors)
     words, _, gpu, _ = _tensor_list(tensors, "tensors")
-    norm, at, work = _norm_buffers(len(tensors), gpu, norm, stream)
+    norm, work = _norm_buffers(len(tensors), gpu, norm, stream)
     s = _torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream
-    rc = (_lib or load()).gemm_grad_norm(len(tensors), words, at, work, s or None)
+    rc = (_lib or load()).gemm_grad_norm(len(tensors), words, norm.data_ptr(), work.data_ptr(), s or None)
     if rc:
         _check(rc)
     return norm
@@ -877,9 +879,10 @@ def clip_grad_norm(tensors, max_norm: float, out=None, norm=None, stream=None):
                 if t.numel() and not (o.is_contiguous() and t.is_contiguous()) and \
                         (o.shape != t.shape or o.stride() != t.stride()):
                     raise ValueError(f"out: tensor {i} must have its tensor's shape and order of dimensions")
-    norm, at, work = _norm_buffers(len(tensors), gpu, norm, stream)
+    norm, work = _norm_buffers(len(tensors), gpu, norm, stream)
     s = torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream
-    rc = (_lib or load()).gemm_clip_grad_norm(len(tensors), words, max_norm, to, at, work, s or None)
+    rc = (_lib or load()).gemm_clip_grad_norm(len(tensors), words, max_norm, to, norm.data_ptr(), work.data_ptr(),
+                                               s or None)
     if rc:
         _check(rc)
     if out is None:

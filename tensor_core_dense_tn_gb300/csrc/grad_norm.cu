@@ -77,12 +77,19 @@ __device__ __forceinline__ void store1(void* base, bool f32, long long i, float 
   else static_cast<uint16_t*>(base)[i] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
 }
 
-// The tensor of a chunk: the last whose first chunk is not past it, in [lo, hi].
+// The tensors' first chunks in shared memory, where a search does not wait for
+// the parameters at every step.
 template <int CAP>
-__device__ __forceinline__ int tensor_of(const List<CAP>& l, int chunk, int lo, int hi) {
+__device__ __forceinline__ void copy_firsts(const List<CAP>& l, int* firsts) {
+  for (int i = threadIdx.x; i < l.count; i += kThreads) firsts[i] = l.t[i].first;
+  __syncthreads();
+}
+
+// The tensor of a chunk: the last whose first chunk is not past it, in [lo, hi].
+__device__ __forceinline__ int tensor_of(const int* firsts, int chunk, int lo, int hi) {
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (l.t[mid].first <= chunk) lo = mid;
+    if (firsts[mid] <= chunk) lo = mid;
     else hi = mid - 1;
   }
   return lo;
@@ -96,9 +103,9 @@ struct Place {
 };
 
 template <int CAP>
-__device__ __forceinline__ Place place_of(const List<CAP>& l, int chunk, int lo, int hi) {
+__device__ __forceinline__ Place place_of(const List<CAP>& l, const int* firsts, int chunk, int lo, int hi) {
   Place r;
-  r.tensor = tensor_of(l, chunk, lo, hi);
+  r.tensor = tensor_of(firsts, chunk, lo, hi);
   const GradTensor& t = l.t[r.tensor];
   const int size = t.in_f32 ? 4 : 2;
   r.in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(t.in) + t.head * size);
@@ -123,17 +130,29 @@ __device__ __forceinline__ void for_ends(const GradTensor& t, long long vectors,
   }
 }
 
-// The sum over the block, in every thread; the order is fixed.
-__device__ __forceinline__ double block_sum(double v, double* shared) {
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+// The sum over the block, in every thread; the order is fixed.  One warp adds
+// what all threads put down: an SM does two fp64 additions a cycle, and a tree
+// over all threads with a last step in each of them took 5000 cycles.
+struct Sums {
+  double of_thread[kThreads];
+  double all;
+};
+
+__device__ __forceinline__ double block_sum(double v, Sums& shared) {
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = v;
+  shared.of_thread[threadIdx.x] = v;
   __syncthreads();
-  double s = 0.0;
+  if (threadIdx.x < 32) {
+    double a[4] = {};
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) s += shared[i];
-  return s;
+    for (int i = 0; i < kThreads / 32; ++i) a[i & 3] += shared.of_thread[i * 32 + threadIdx.x];
+    double s = (a[0] + a[1]) + (a[2] + a[3]);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+    if (threadIdx.x == 0) shared.all = s;
+  }
+  __syncthreads();
+  return shared.all;
 }
 
 // The squares of vectors in fp64, for fp32 sums that hold too little or too
@@ -173,12 +192,14 @@ __device__ __forceinline__ double squares(const uint4 (&x)[kVectors]) {
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_squares_kernel(const __grid_constant__ List<CAP> l, const Task k) {
-  __shared__ double shared[kThreads / 32];
+  __shared__ Sums shared;
+  __shared__ int firsts[CAP];
+  copy_firsts(l, firsts);
   griddep_wait();
   griddep_launch_dependents();
   double sum = 0.0;
   int chunk = blockIdx.x;
-  Place r = place_of(l, chunk, 0, l.count - 1);
+  Place r = place_of(l, firsts, chunk, 0, l.count - 1);
   uint4 x[kVectors];
   load_vectors(r, x);
   while (true) {
@@ -188,9 +209,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     Place rn = r;
     uint4 y[kVectors];
     if (more) {
-      const bool same = r.tensor + 1 == l.count || l.t[r.tensor + 1].first > next;
+      const bool same = r.tensor + 1 == l.count || firsts[r.tensor + 1] > next;
       if (same) rn.at += (long long)gridDim.x * kChunkVectors;
-      else rn = place_of(l, next, r.tensor + 1, l.count - 1);
+      else rn = place_of(l, firsts, next, r.tensor + 1, l.count - 1);
       load_vectors(rn, y);
     }
     const GradTensor& t = l.t[r.tensor];
@@ -210,10 +231,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   if (threadIdx.x == 0) k.partial[blockIdx.x] = sum;
 }
 
-__device__ __forceinline__ double total(const Task& k, double* shared) {
+// The sum of all squares, in every thread.
+__device__ __forceinline__ double total(const Task& k, Sums& shared) {
   double s = 0.0;
   for (int i = threadIdx.x; i < k.partials; i += kThreads) s += k.partial[i];
-  return sqrt(block_sum(s, shared));
+  return block_sum(s, shared);
 }
 
 // A vector's values times both factors, to their place in `out`.
@@ -239,32 +261,43 @@ __device__ __forceinline__ void store_scaled(uint8_t* out, long long at, uint4 x
 }
 
 __global__ void __launch_bounds__(kThreads) grad_finish_kernel(const Task k) {
-  __shared__ double shared[kThreads / 32];
+  __shared__ Sums shared;
   griddep_wait();
   griddep_launch_dependents();
-  const double norm = total(k, shared);
-  if (threadIdx.x == 0) *k.norm = (float)norm;
+  const double sum = total(k, shared);
+  if (threadIdx.x == 0) *k.norm = (float)sqrt(sum);
 }
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     grad_clip_kernel(const __grid_constant__ List<CAP> l, const Task k, bool in_place) {
-  __shared__ double shared[kThreads / 32];
+  __shared__ Sums shared;
+  __shared__ int firsts[CAP];
+  copy_firsts(l, firsts);
   griddep_wait();
   griddep_launch_dependents();
-  const double norm = total(k, shared);
-  if (k.norm && blockIdx.x == 0 && threadIdx.x == 0) *k.norm = (float)norm;
-  // (false for a norm of NaN; an infinite one leaves the values alone too)
-  const bool scale = norm > (double)k.max_norm && norm <= 1.7976931348623157e308;
-  if (!scale && in_place) return;
-  // Two factors, the first a power of two: a single one below 2^-126 (a norm
-  // beyond fp32) would lose bits.
-  const double exact = scale ? (double)k.max_norm / norm : 1.0;
-  const float first = exact < 0x1p-100 ? 0x1p-64f : 1.0f;
-  const float c = (float)(exact < 0x1p-100 ? exact * 0x1p64 : exact);
+  const double sum = total(k, shared);
+  // One thread takes the root and the quotient: in fp64, all threads' would
+  // take 4 us.  Two factors, the first a power of two: a single one below 2^-126
+  // (a norm beyond fp32) would lose bits.  A norm that is not finite leaves the
+  // values alone.
+  __shared__ float factors[2];
+  __shared__ int scaled;
+  if (threadIdx.x == 0) {
+    const double norm = sqrt(sum);
+    if (k.norm && blockIdx.x == 0) *k.norm = (float)norm;
+    scaled = norm > (double)k.max_norm && norm <= 1.7976931348623157e308;
+    const double exact = scaled ? (double)k.max_norm / norm : 1.0;
+    const bool tiny = exact < 0x1p-100;
+    factors[0] = tiny ? 0x1p-64f : 1.0f;
+    factors[1] = (float)(tiny ? exact * 0x1p64 : exact);
+  }
+  __syncthreads();
+  if (!scaled && in_place) return;
+  const float first = factors[0], c = factors[1];
   // backwards through the chunks, the next one's vectors on their way while these are scaled
   int chunk = l.chunks - 1 - (int)blockIdx.x;
-  Place r = place_of(l, chunk, 0, l.count - 1);
+  Place r = place_of(l, firsts, chunk, 0, l.count - 1);
   uint4 x[kVectors];
   if (l.t[r.tensor].vector) load_vectors(r, x);
   while (true) {
@@ -272,8 +305,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     Place rn = r;
     uint4 y[kVectors];
     if (next >= 0) {
-      if (l.t[r.tensor].first <= next) rn.at -= (long long)gridDim.x * kChunkVectors;
-      else rn = place_of(l, next, 0, r.tensor - 1);
+      if (firsts[r.tensor] <= next) rn.at -= (long long)gridDim.x * kChunkVectors;
+      else rn = place_of(l, firsts, next, 0, r.tensor - 1);
       if (l.t[rn.tensor].vector) load_vectors(rn, y);
     }
     const GradTensor& t = l.t[r.tensor];

@@ -74,6 +74,7 @@ def lib(monkeypatch):
     g._t()
     monkeypatch.setattr(g, "_several_gpus", True)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(g, "_GRAD_WORKSPACE", {})
     empty = torch.empty
     monkeypatch.setattr(torch, "empty", lambda *a, **k: gpu(empty(*a, **{n: v for n, v in k.items() if n != "device"})))
     return recorder
