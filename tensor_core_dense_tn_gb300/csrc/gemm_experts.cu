@@ -133,6 +133,18 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, int chunk) {
          ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// What the multiplying warp has to know of a tile, in the leader's shared
+// memory beside the ring stage of the tile's first block: the loading thread
+// puts it there before it arrives on that stage's barrier.  Tiles without a sum
+// take no stage.  (One for their note would be handed back to the peer CTA
+// without its having loaded anything, and so perhaps a second time before it
+// has seen the first.)
+struct Note {
+  int n;        // the MMA's N; 0 behind the last tile
+  int sum;      // summation indices
+  int empty;    // tiles without a sum before this one
+};
+
 // The experts' first rows (E + 1) and first row blocks (E + 2: behind the
 // experts the rows of nobody) of one launch, in shared memory.
 struct Table {
@@ -407,8 +419,9 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
   const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + 4);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile uint32_t* abort_flag = tmem_slot + 1;
+  Note* notes = reinterpret_cast<Note*>(tmem_slot + 2);     // one per stage
   Table tb;
-  tb.row = reinterpret_cast<int*>(tmem_slot + 2);
+  tb.row = reinterpret_cast<int*>(notes + kMaxStages);
   tb.tile = tb.row + p.E + 1;
 
   const int warp = threadIdx.x >> 5;
@@ -463,8 +476,13 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
       bool ok = true;
       int stage = 0;
       uint32_t phase = 0;
+      int empty = 0;          // tiles without a sum since the last note
       for (int t = first_tile; t < num_tiles && ok; t += step) {
         const Tile r = tile_of<CG, OP>(t, p, tb);
+        if (r.num_kb == 0) {
+          ++empty;
+          continue;
+        }
         const int c_at = r.col0 + (int)rank * p.col_tile;
         const int share = r.n / CG;            // this CTA's share of the tile's rows
         const int r_at = r.row0 + (int)rank * share;
@@ -478,6 +496,10 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
           if (!wait_bar<kPair>(empty_bar(stage), phase ^ 1, ab)) {
             ok = false;
             break;
+          }
+          if (kb == 0) {
+            notes[stage] = Note{r.n, r.k_end - r.k0, empty};
+            empty = 0;
           }
           const int k = r.k0 + kb * kBlockK;
           const uint32_t c = sC + stage * kColBytes, b = sR + stage * p.row_bytes;
@@ -517,38 +539,62 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
           }
         }
       }
+      if (ok && leader && wait_bar<kPair>(empty_bar(stage), phase ^ 1, ab)) {
+        notes[stage] = Note{0, 0, empty};
+        mbar_arrive(full_bar(stage));
+      }
       if (!ok) settle(2000000);   // copies already issued land before teardown
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
-    if (lane == 0 && leader) {
+    // The whole warp runs this, and one elected lane issues: with one lane in
+    // here alone each MMA took 69 cycles to issue and each block 590, whatever its N.
+    if (leader) {
       Abort ab{abort_flag, p.timeout_ns, p.status, kRoleMma};
-      bool ok = true;
+      // (the whole warp leaves, or none of it)
+      auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_bar<kPair>(bar, parity, ab)) != 0;
+      };
       int stage = 0;
       uint32_t phase = 0, ready_phase = 0;      // ready: one bit per stage
       int acc = 0;
       uint32_t acc_phase = 0;
-      for (int t = first_tile; t < num_tiles && ok; t += step) {
-        const Tile r = tile_of<CG, OP>(t, p, tb);
+      auto commit = [&](uint32_t bar) {
+        if constexpr (kPair) mma_commit_pair(bar, 0x3);
+        else mma_commit(bar);
+      };
+      auto advance = [&] {
+        if (++stage == p.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      };
+      // the accumulator goes to the warps that store it, the other is next
+      auto hand_over = [&] {
+        if (elect_one()) commit(accf_bar(acc));
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1;
+      };
+      while (true) {
+        if (!wait_all(full_bar(stage), phase)) break;
+        const int n = __shfl_sync(0xffffffffu, notes[stage].n, 0), sum = __shfl_sync(0xffffffffu, notes[stage].sum, 0);
+        const int empty = __shfl_sync(0xffffffffu, notes[stage].empty, 0);
+        bool ok = true;
+        for (int i = 0; i < empty && ok; ++i) {       // their zeros are stored without a look at the accumulator
+          ok = wait_all(acce_bar(acc), acc_phase ^ 1);
+          if (ok) hand_over();
+        }
+        if (!ok || n == 0) break;
         const uint32_t idesc =
-            instr_desc_bf16_f32(128 * CG, r.n) | (S_::kMnCols ? 1u << 15 : 0u) | (S_::kMnRows ? 1u << 16 : 0u);
-        if (!wait_bar<kPair>(acce_bar(acc), acc_phase ^ 1, ab)) break;
-        tc_fence_after();
+            instr_desc_bf16_f32(128 * CG, n) | (S_::kMnCols ? 1u << 15 : 0u) | (S_::kMnRows ? 1u << 16 : 0u);
+        if (!wait_all(acce_bar(acc), acc_phase ^ 1)) break;
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * p.acc_cols);
-        auto hand_back = [&] {
-          if constexpr (kPair) mma_commit_pair(empty_bar(stage), 0x3);
-          else mma_commit(empty_bar(stage));
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        };
         // Whole blocks; the last, shorter one apart: with the two in one loop,
         // and so its steps and strides in registers, the MMAs came with pauses
         // (2048 rows for each of 8 matrices of 8192 x 4096: 747 us, apart 625).
-        const int whole = S_::kWeights ? (r.k_end - r.k0) / kBlockK : r.num_kb;
+        const int blocks = (sum + kBlockK - 1) / kBlockK, whole = S_::kWeights ? sum / kBlockK : blocks;
         for (int kb = 0; kb < whole; ++kb) {
-          ok = wait_bar<kPair>(full_bar(stage), phase, ab);
+          if (kb > 0) ok = wait_all(full_bar(stage), phase);
           if (!ok) break;
           tc_fence_after();
           const uint32_t c = sC + stage * kColBytes, b = sR + stage * p.row_bytes;
@@ -556,39 +602,43 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
           const uint64_t b0 = S_::kMnRows ? desc_mn(b, kChunkBytes) : smem_desc_sw128(b);
           // 16 summation indices are 32 bytes of a K-major operand's rows, 16 rows of each chunk of an MN-major one
           constexpr uint64_t kStepC = S_::kMnCols ? kPartBytes / 16 : 2, kStepR = S_::kMnRows ? kPartBytes / 16 : 2;
+          if (elect_one()) {
 #pragma unroll
-          for (int i = 0; i < kBlockK / 16; ++i)
-            mma_issue<CG, kKindF16>(d_tmem, c0 + kStepC * i, b0 + kStepR * i, idesc, (kb != 0 || i != 0) ? 1u : 0u);
-          hand_back();
+            for (int i = 0; i < kBlockK / 16; ++i)
+              mma_issue<CG, kKindF16>(d_tmem, c0 + kStepC * i, b0 + kStepR * i, idesc, (kb != 0 || i != 0) ? 1u : 0u);
+            commit(empty_bar(stage));
+          }
+          advance();
         }
-        if (S_::kWeights && ok && whole < r.num_kb) {
-          ok = wait_bar<kPair>(full_bar(stage), phase, ab);
-          if (ok && ragged(r)) {
-            ok = wait_bar<kPair>(ready_bar(stage), (ready_phase >> stage) & 1u, ab);
+        if (S_::kWeights && ok && whole < blocks) {
+          if (whole > 0) ok = wait_all(full_bar(stage), phase);
+          if (ok && (sum & 15) != 0) {
+            ok = wait_all(ready_bar(stage), (ready_phase >> stage) & 1u);
             ready_phase ^= 1u << stage;
           }
           if (!ok) break;
           tc_fence_after();
           // parts of 16 rows, each with its chunks together
-          const int parts = (r.k_end - r.k0 - whole * kBlockK + 15) / 16;
-          for (int i = 0; i < parts; ++i)
-            mma_issue<CG, kKindF16>(d_tmem, desc_mn(sC + stage * kColBytes + i * (kColBytes / 4), kPartBytes),
-                                    desc_mn(sR + stage * p.row_bytes + i * (p.row_bytes / 4), kPartBytes), idesc,
-                                    (whole != 0 || i != 0) ? 1u : 0u);
-          hand_back();
+          const int parts = (sum - whole * kBlockK + 15) / 16;
+          if (elect_one()) {
+            for (int i = 0; i < parts; ++i)
+              mma_issue<CG, kKindF16>(d_tmem, desc_mn(sC + stage * kColBytes + i * (kColBytes / 4), kPartBytes),
+                                      desc_mn(sR + stage * p.row_bytes + i * (p.row_bytes / 4), kPartBytes), idesc,
+                                      (whole != 0 || i != 0) ? 1u : 0u);
+            commit(empty_bar(stage));
+          }
+          advance();
         }
         if (!ok) break;
-        if constexpr (kPair) mma_commit_pair(accf_bar(acc), 0x3);
-        else mma_commit(accf_bar(acc));
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1;
+        hand_over();
       }
-      // All MMAs issued by this thread complete before TMEM is released.
-      if constexpr (kPair) mma_commit_pair(drain_bar, 0x1);
-      else mma_commit(drain_bar);
-      Abort ab_drain{nullptr, p.timeout_ns, p.status, kRoleMma};
-      wait_bar<kPair>(drain_bar, 0, ab_drain);
+      // All MMAs that were issued complete before TMEM is released.
+      if (elect_one()) commit(drain_bar);
     }
+    // Both CTAs of a pair wait: the commits before this one arrive on both, and
+    // none may come after a CTA has left its shared memory to the next.
+    Abort ab_drain{nullptr, p.timeout_ns, p.status, kRoleMma};
+    wait_bar<kPair>(drain_bar, 0, ab_drain);
   } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
@@ -661,7 +711,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     const int chunks = p.row_bytes / kChunkBytes;
     for (int t = first_tile; t < num_tiles; t += step) {
       const Tile r = tile_of<CG, OP>(t, p, tb);
-      const int last = (stage + r.num_kb - 1) % p.stages;      // (num_kb = 0 is not ragged)
+      const int last = (stage + r.num_kb - 1) % p.stages;      // (a tile without a sum is not ragged)
       stage = (stage + r.num_kb) % p.stages;
       if (!ragged(r)) continue;
       if (!__all_sync(0xffffffffu, wait_bar<false>(tail_bar(last), (tail_phase >> last) & 1u, ab))) break;
@@ -708,7 +758,7 @@ int threads_of(int op) {
 constexpr int kSmemMax = 232448;
 
 int smem_bytes(const ExpertsParams& p) {
-  return 1024 + p.stages * (kColBytes + p.row_bytes) + kBars * 8 + 8 + table_bytes(p.E);
+  return 1024 + p.stages * (kColBytes + p.row_bytes) + kBars * 8 + 8 + kMaxStages * (int)sizeof(Note) + table_bytes(p.E);
 }
 
 }  // namespace

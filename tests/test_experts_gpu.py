@@ -271,3 +271,21 @@ def test_empty_calls():
     assert torch.all(g.gemm_experts_backward_a(none, torch.empty(2, 0, 32, device="cuda", dtype=BF16), plan) == 0)
     assert g.gemm_experts_backward_w(none, none, plan).shape == (2, 0, 0)
     status()
+
+
+def test_tiles_without_a_sum_between_others_many_times():
+    """CTA pairs that store zeros for rows of nobody, or for experts without rows, before, between and after tiles with
+    long sums, one launch close behind another: the two CTAs of a pair must stay in step whichever is ahead."""
+    plan = plan_of([900, 0, 0, 1800, 0, 333, 0], 700)
+    A, dD, W = values((plan.rows, 1024), 1, True), values((plan.rows, 2048), 2, True), values((7, 2048, 1024), 3, True)
+    first = None
+    for _ in range(60):
+        got = [(g.gemm_experts(A, W, plan), g.gemm_experts_backward_a(dD, W, plan),
+                g.gemm_experts_backward_w(dD, A, plan)) for _ in range(3)]
+        status()
+        first = first or got[0]
+        for three in got:
+            assert all(torch.equal(a, b) for a, b in zip(three, first))
+    check(first[0], *forward64(A, W, plan), 1024, True)
+    check(first[1], *forward64(dD, W.transpose(1, 2), plan), 2048, True)
+    check(first[2], *weights64(dD, A, plan), 1800, True)
