@@ -471,80 +471,93 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------------------ loads
-    if (lane == 0) {
-      Abort ab{abort_flag, p.timeout_ns, p.status, kRoleProducer};
-      bool ok = true;
-      int stage = 0;
-      uint32_t phase = 0;
-      int empty = 0;          // tiles without a sum since the last note
-      for (int t = first_tile; t < num_tiles && ok; t += step) {
-        const Tile r = tile_of<CG, OP>(t, p, tb);
-        if (r.num_kb == 0) {
-          ++empty;
-          continue;
-        }
-        const int c_at = r.col0 + (int)rank * p.col_tile;
-        const int share = r.n / CG;            // this CTA's share of the tile's rows
-        const int r_at = r.row0 + (int)rank * share;
-        // the smallest box that holds the share: whole, 3/4, 1/2 or 1/4 (of at least 64 rows, else whole)
-        const int box = S_::kWeights || p.row_box < 64 ? 3 : (4 * share - 1) / p.row_box;
-        const int chunks = p.wide_rows ? p.row_bytes / kChunkBytes : (share + 63) / 64;    // weights
-        const uint32_t tx =
-            (uint32_t)(p.col_tile * 128 + (S_::kWeights ? chunks * kChunkBytes : (box + 1) * (p.row_box / 4) * 128));
-        const CUtensorMap* row_map = box == 3 ? &maps.rows : &maps.rows_part[box];
-        for (int kb = 0; kb < r.num_kb; ++kb) {
-          if (!wait_bar<kPair>(empty_bar(stage), phase ^ 1, ab)) {
-            ok = false;
-            break;
-          }
-          if (kb == 0) {
-            notes[stage] = Note{r.n, r.k_end - r.k0, empty};
-            empty = 0;
-          }
-          const int k = r.k0 + kb * kBlockK;
-          const uint32_t c = sC + stage * kColBytes, b = sR + stage * p.row_bytes;
-          const uint32_t fb = full_bar(stage);
-          const uint32_t to = kPair ? mapa_shared(fb, 0) : fb;    // a pair's bytes all count on its leader's barrier
-          if (S_::kWeights && r.k_end - k < kBlockK) {
-            // the rest of the expert's rows, 16 at a time.  Where the last are
-            // not all its own, the bytes count on each CTA's own barrier, for the
-            // warp that zeroes
-            const int parts = (r.k_end - k + 15) / 16;
-            const uint32_t part_tx = (uint32_t)(parts * (2 + chunks) * kPartBytes);
-            const bool own = ragged(r);
-            const uint32_t tail = tail_bar(stage);
-            if (leader) {
-              if (own) mbar_arrive(fb);
-              else mbar_arrive_expect_tx(fb, part_tx * CG);
-            }
-            if (own) mbar_arrive_expect_tx(tail, part_tx);
-            for (int i = 0; i < parts; ++i) {
-              const uint32_t ci = c + i * (kColBytes / 4), bi = b + i * (p.row_bytes / 4);
-              if (own) {
-                load_cols<OP, false>(ci, &maps.cols_part, p.wide_cols, c_at, k + 16 * i, r.e, kPartBytes, tail);
-                load_rows<OP, false>(bi, &maps.rows_part[0], p.wide_rows, r_at, k + 16 * i, kPartBytes, chunks, tail);
-              } else {
-                load_cols<OP, kPair>(ci, &maps.cols_part, p.wide_cols, c_at, k + 16 * i, r.e, kPartBytes, to);
-                load_rows<OP, kPair>(bi, &maps.rows_part[0], p.wide_rows, r_at, k + 16 * i, kPartBytes, chunks, to);
-              }
-            }
-          } else {
-            if (leader) mbar_arrive_expect_tx(fb, tx * CG);
-            load_cols<OP, kPair>(c, &maps.cols, p.wide_cols, c_at, k, r.e, kChunkBytes, to);
-            load_rows<OP, kPair>(b, row_map, p.wide_rows, r_at, k, kChunkBytes, chunks, to);
-          }
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1;
-          }
-        }
+    // (the whole warp, one elected lane of which issues, as below)
+    Abort ab{abort_flag, p.timeout_ns, p.status, kRoleProducer};
+    auto wait_empty = [&](int s, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_bar<kPair>(empty_bar(s), parity, ab)) != 0;
+    };
+    bool ok = true;
+    int stage = 0;
+    uint32_t phase = 0;
+    auto advance = [&] {
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1;
       }
-      if (ok && leader && wait_bar<kPair>(empty_bar(stage), phase ^ 1, ab)) {
-        notes[stage] = Note{0, 0, empty};
-        mbar_arrive(full_bar(stage));
+    };
+    int empty = 0;          // tiles without a sum since the last note
+    for (int t = first_tile; t < num_tiles && ok; t += step) {
+      Tile r = tile_of<CG, OP>(t, p, tb);
+      if (r.num_kb == 0) {
+        ++empty;
+        continue;
       }
-      if (!ok) settle(2000000);   // copies already issued land before teardown
+      const int e = __shfl_sync(0xffffffffu, r.e, 0), n = __shfl_sync(0xffffffffu, r.n, 0);
+      const int k0 = __shfl_sync(0xffffffffu, r.k0, 0), sum = __shfl_sync(0xffffffffu, r.k_end, 0) - k0;
+      const int share = n / CG;              // this CTA's share of the tile's rows
+      const int c_at = __shfl_sync(0xffffffffu, r.col0, 0) + (int)rank * p.col_tile;
+      const int r_at = __shfl_sync(0xffffffffu, r.row0, 0) + (int)rank * share;
+      // the smallest box that holds the share: whole, 3/4, 1/2 or 1/4 (of at least 64 rows, else whole)
+      const int box = S_::kWeights || p.row_box < 64 ? 3 : (4 * share - 1) / p.row_box;
+      const int chunks = p.wide_rows ? p.row_bytes / kChunkBytes : (share + 63) / 64;    // weights
+      const uint32_t tx =
+          (uint32_t)(p.col_tile * 128 + (S_::kWeights ? chunks * kChunkBytes : (box + 1) * (p.row_box / 4) * 128));
+      const CUtensorMap* row_map = box == 3 ? &maps.rows : &maps.rows_part[box];
+      const int blocks = (sum + kBlockK - 1) / kBlockK, whole = S_::kWeights ? sum / kBlockK : blocks;
+      for (int kb = 0; kb < whole; ++kb) {
+        ok = wait_empty(stage, phase ^ 1);
+        if (!ok) break;
+        const int k = k0 + kb * kBlockK;
+        const uint32_t c = sC + stage * kColBytes, b = sR + stage * p.row_bytes;
+        const uint32_t fb = full_bar(stage);
+        const uint32_t to = kPair ? mapa_shared(fb, 0) : fb;    // a pair's bytes all count on its leader's barrier
+        if (elect_one()) {
+          if (kb == 0) notes[stage] = Note{n, sum, empty};
+          if (leader) mbar_arrive_expect_tx(fb, tx * CG);
+          load_cols<OP, kPair>(c, &maps.cols, p.wide_cols, c_at, k, e, kChunkBytes, to);
+          load_rows<OP, kPair>(b, row_map, p.wide_rows, r_at, k, kChunkBytes, chunks, to);
+        }
+        advance();
+      }
+      if (S_::kWeights && ok && whole < blocks) {
+        // the rest of the expert's rows, 16 at a time.  Where the last are not
+        // all its own, the bytes count on each CTA's own barrier, for the warp
+        // that zeroes
+        ok = wait_empty(stage, phase ^ 1);
+        if (!ok) break;
+        const int parts = (sum - whole * kBlockK + 15) / 16;
+        const uint32_t part_tx = (uint32_t)(parts * (2 + chunks) * kPartBytes);
+        const bool own = (sum & 15) != 0;
+        const uint32_t fb = full_bar(stage), tail = tail_bar(stage);
+        const uint32_t to = kPair ? mapa_shared(fb, 0) : fb;
+        if (elect_one()) {
+          if (whole == 0) notes[stage] = Note{n, sum, empty};
+          if (leader) {
+            if (own) mbar_arrive(fb);
+            else mbar_arrive_expect_tx(fb, part_tx * CG);
+          }
+          if (own) mbar_arrive_expect_tx(tail, part_tx);
+          for (int i = 0; i < parts; ++i) {
+            const uint32_t ci = sC + stage * kColBytes + i * (kColBytes / 4), bi = sR + stage * p.row_bytes + i * (p.row_bytes / 4);
+            const int k = k0 + whole * kBlockK + 16 * i;
+            if (own) {
+              load_cols<OP, false>(ci, &maps.cols_part, p.wide_cols, c_at, k, e, kPartBytes, tail);
+              load_rows<OP, false>(bi, &maps.rows_part[0], p.wide_rows, r_at, k, kPartBytes, chunks, tail);
+            } else {
+              load_cols<OP, kPair>(ci, &maps.cols_part, p.wide_cols, c_at, k, e, kPartBytes, to);
+              load_rows<OP, kPair>(bi, &maps.rows_part[0], p.wide_rows, r_at, k, kPartBytes, chunks, to);
+            }
+          }
+        }
+        advance();
+      }
+      empty = 0;
     }
+    if (ok && leader && wait_empty(stage, phase ^ 1) && elect_one()) {
+      notes[stage] = Note{0, 0, empty};
+      mbar_arrive(full_bar(stage));
+    }
+    if (!ok) settle(2000000);   // copies already issued land before teardown
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     // The whole warp runs this, and one elected lane issues: with one lane in
