@@ -326,12 +326,22 @@ __device__ __forceinline__ void activate_rows(float (&v)[NR], int act, bool f32)
 // are 128 contiguous bytes of a warp.  bf16: in pairs, where the addresses
 // allow: an even lane moves both columns of its pair in one row, the odd lane
 // in the next, so that a step moves two rows of 64 bytes.
+//
+// For short sums these instructions are the kernel's time (with a select, a
+// shuffle and two more selects a pair and a compare at each store 61 matrices
+// of 1000 x 2000 took 64 us), so all words are made before the stores, and rows
+// that are all there are stored without a look at each.
 template <int NR>
 __device__ __forceinline__ void store_rows_f32(float* at, long long ld, int rows, bool mine, const float (&v)[NR]) {
   if (!mine) return;
+  if (rows >= NR) {
 #pragma unroll
-  for (int j = 0; j < NR; ++j)
-    if (j < rows) at[j * ld] = v[j];
+    for (int j = 0; j < NR; ++j, at += ld) *at = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < NR; ++j, at += ld)
+      if (j < rows) *at = v[j];
+  }
 }
 
 template <int NR>
@@ -339,18 +349,28 @@ __device__ __forceinline__ void store_rows_bf16(uint16_t* at, long long ld, int 
                                                 const float (&v)[NR]) {
   const int odd = threadIdx.x & 1;
   if (pairs) {
-    uint32_t* to = reinterpret_cast<uint32_t*>(at - odd + odd * ld);
+    uint32_t w[NR / 2];
 #pragma unroll
     for (int j = 0; j < NR; j += 2) {
-      const float give = odd ? v[j] : v[j + 1];
-      const float got = __shfl_xor_sync(0xffffffffu, give, 1);
-      const uint32_t w = odd ? pack_bf16x2(got, v[j + 1]) : pack_bf16x2(v[j], got);
-      if (mine && j + odd < rows) to[j / 2 * ld] = w;
+      const uint32_t own = pack_bf16x2(v[j], v[j + 1]);      // rows j and j + 1 of this column
+      const uint32_t other = __shfl_xor_sync(0xffffffffu, own, 1);
+      // even: both low halves (row j), odd: both high halves (row j + 1)
+      w[j / 2] = __byte_perm(own, other, odd ? 0x3276 : 0x5410);
+    }
+    if (!mine) return;
+    uint32_t* to = reinterpret_cast<uint32_t*>(at - odd + odd * ld);
+    if (rows >= NR) {
+#pragma unroll
+      for (int j = 0; j < NR / 2; ++j, to += ld) *to = w[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < NR / 2; ++j, to += ld)
+        if (2 * j + odd < rows) *to = w[j];
     }
   } else if (mine) {
 #pragma unroll
-    for (int j = 0; j < NR; ++j)
-      if (j < rows) at[j * ld] = (uint16_t)(pack_bf16x2(v[j], 0.0f) & 0xFFFFu);
+    for (int j = 0; j < NR; ++j, at += ld)
+      if (j < rows) *at = (uint16_t)(pack_bf16x2(v[j], 0.0f) & 0xFFFFu);
   }
 }
 
@@ -687,7 +707,11 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
           tmem_ld_rows(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * p.acc_cols + c), x);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < kRowsAtOnce; ++j) v[j] = p.alpha * __uint_as_float(x[j]);
+          for (int j = 0; j < kRowsAtOnce; ++j) v[j] = __uint_as_float(x[j]);
+          if (p.alpha != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < kRowsAtOnce; ++j) v[j] *= p.alpha;
+          }
         } else {
 #pragma unroll
           for (int j = 0; j < kRowsAtOnce; ++j) v[j] = 0.0f;
