@@ -377,24 +377,26 @@ __device__ __forceinline__ void store_rows_bf16(uint16_t* at, long long ld, int 
 __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&x)[32]) { tmem_ld_32x32b_x32(taddr, x); }
 __device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&x)[16]) { tmem_ld_32x32b_x16(taddr, x); }
 
-// C's raw words as store_rows_* would write them; unpack_c turns them into values.
+// C's raw words, of the rows and columns that store_rows_* writes; add_c makes values of them.
+template <int N, typename T>
+__device__ __forceinline__ void load_words(const T* at, long long step, int count, bool mine, uint32_t* x) {
+  if (mine && count >= N) {
+#pragma unroll
+    for (int j = 0; j < N; ++j, at += step) x[j] = *at;
+  } else {
+#pragma unroll
+    for (int j = 0; j < N; ++j, at += step) x[j] = mine && j < count ? *at : 0;
+  }
+}
+
 template <int NR>
 __device__ __forceinline__ void load_c(const void* base, long long ld, int rows, bool mine, bool f32, bool pairs,
                                        uint32_t (&x)[NR]) {
   const int odd = threadIdx.x & 1;
-  if (f32) {
-    const uint32_t* at = static_cast<const uint32_t*>(base);
-#pragma unroll
-    for (int j = 0; j < NR; ++j) x[j] = mine && j < rows ? at[j * ld] : 0;
-  } else if (pairs) {
-    const uint32_t* at = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(base) - odd + odd * ld);
-#pragma unroll
-    for (int j = 0; j < NR / 2; ++j) x[j] = mine && 2 * j + odd < rows ? at[j * ld] : 0;
-  } else {
-    const uint16_t* at = static_cast<const uint16_t*>(base);
-#pragma unroll
-    for (int j = 0; j < NR; ++j) x[j] = mine && j < rows ? at[j * ld] : 0;
-  }
+  const uint16_t* half = static_cast<const uint16_t*>(base);
+  if (f32) load_words<NR>(static_cast<const uint32_t*>(base), ld, rows, mine, x);
+  else if (pairs) load_words<NR / 2>(reinterpret_cast<const uint32_t*>(half - odd + odd * ld), ld, (rows + 1 - odd) / 2, mine, x);
+  else load_words<NR>(half, ld, rows, mine, x);
 }
 
 template <int NR>
@@ -804,11 +806,11 @@ void experts_geometry(ExpertsParams* p, int sms) {
   const bool weights = p->op == kExpertsWeights;
   const int active = p->E < p->R ? p->E : p->R;       // experts that can have rows
   const int average = active > 0 ? p->R / active : 0;
-  // Pairs halve what a CTA loads of the other operand.  Where the output's
-  // memory decides, single CTAs, which need not wait for each other, are faster
-  // (weights, 61 matrices of 1000 x 2000 bf16 for 3 rows each: 65 us, pairs 72; 64
-  // of 2048 x 2048 fp32 with C for 256: 404, 421; without C 235, 226).
-  p->cg = average >= (weights ? (p->has_c ? 512 : 128) : 48) ? 2 : 1;
+  // Pairs halve what a CTA loads of the other operand.  Weights of few rows,
+  // where the output's memory decides: single CTAs, which need not wait for each
+  // other (64 matrices of 2048 x 2048, single / pairs: 128 rows each, bf16, 130 /
+  // 142 us; 256 rows 174 / 171; fp32 with C, 512 rows 444 / 454, 1024 rows 582 / 555).
+  p->cg = weights && average < (p->has_c ? 768 : 192) ? 1 : 2;
   const int step = 16 * p->cg;
   const int most = 2 * average < 32 ? 32 : 2 * average;
   p->tile_rows = weights || most > 256 ? 256 : (most + 31) / 32 * 32;
@@ -818,13 +820,13 @@ void experts_geometry(ExpertsParams* p, int sms) {
   p->row_bytes = weights ? share / 64 * kChunkBytes : (share * 128 + 1023) / 1024 * 1024;
   // Few rows: W's bytes decide, and each CTA takes the same number of them when
   // the tiles' columns are chosen so that the rounds of tiles are full (16
-  // tokens through 2 of 8 matrices of 4096 x 4096: 256 tiles of 128 columns on 152
-  // SMs take two rounds; 296 tiles of 112 columns too).
+  // tokens through 2 of 8 matrices of 4096 x 4096: 128 tiles of 256 columns on 76
+  // pairs take two rounds; 152 tiles of 224 columns too).
   p->col_tile = 128;
-  if (p->op == kExpertsForward && p->cg == 1) {
+  if (p->op == kExpertsForward && average < 64) {
     long long best = 0;
-    for (int c = 128; c >= 64; c -= 16) {
-      const long long tiles = (long long)active * ((p->cols_out + c - 1) / c), time = (tiles + sms - 1) / sms * c;
+    for (int c = 128; c >= 96; c -= 16) {
+      const long long tiles = (long long)active * ((p->cols_out + 2 * c - 1) / (2 * c)), time = (tiles + sms / 2 - 1) / (sms / 2) * c;
       if (!best || time < best) {
         best = time;
         p->col_tile = c;
