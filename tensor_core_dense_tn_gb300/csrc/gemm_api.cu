@@ -1068,6 +1068,20 @@ int encode_chunks(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, 
   return GEMM_OK;
 }
 
+// Map of a K-major operand whose boxes hold `group` k-blocks: {64, row, k-block
+// (, matrix)}; K is whole k-blocks.
+int encode_kblocks(CUtensorMap* m, const void* base, int64_t K, int64_t rows, int64_t count, int64_t ld, int64_t stride,
+                   int box_rows, int group, const char* what) {
+  cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)(K / 64), (cuuint64_t)count};
+  cuuint64_t strides[3] = {(cuuint64_t)ld * 2, 128, (cuuint64_t)stride * 2};
+  cuuint32_t box[4] = {64, (cuuint32_t)box_rows, (cuuint32_t)group, 1}, estr[4] = {1, 1, 1, 1};
+  const CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, stride ? 4 : 3, const_cast<void*>(base), dims, strides,
+                              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(GEMM_ERR_LAUNCH, "cuTensorMapEncodeTiled(%s) failed with %d", what, (int)r);
+  return GEMM_OK;
+}
+
 // op: kExpertsForward (X = A), kExpertsRows (X = dD) with out = R rows, or
 // kExpertsWeights (X = dD, Y = A) with out = E matrices of N x K.
 int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, const void* X, int64_t ldx, const void* Y,
@@ -1158,12 +1172,18 @@ int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, cons
         return rc;
     } else {
       const int64_t S = p.S;
-      p.wide_cols = op == kExpertsRows && K % 64 == 0;
-      if (op == kExpertsForward) rc = encode_3d(&maps.cols, bf16, 2, Y, K, N, E, ldy, stride_y, 64, p.col_tile, sw, "W");
+      if (op == kExpertsRows) p.wide_cols = K % 64 == 0;
+      if (p.group > 1) rc = encode_kblocks(&maps.cols, Y, K, N, E, ldy, stride_y, p.col_tile, p.group, "W");
+      else if (op == kExpertsForward) rc = encode_3d(&maps.cols, bf16, 2, Y, K, N, E, ldy, stride_y, 64, p.col_tile, sw, "W");
       else rc = encode_chunks(&maps.cols, Y, K, N, E, ldy, stride_y, 64, p.wide_cols ? 2 : 0, "W");
-      if (rc || (rc = encode_2d(&maps.rows, bf16, 2, X, S, R, ldx, 64, p.row_box, sw, "rows"))) return rc;
-      for (int i = 0; i < 3 && p.row_box >= 64; ++i)
-        if ((rc = encode_2d(&maps.rows_part[i], bf16, 2, X, S, R, ldx, 64, (i + 1) * (p.row_box / 4), sw, "rows"))) return rc;
+      for (int i = 0; i < 4 && !rc; ++i) {      // boxes of a quarter, a half, three quarters and all of the rows
+        if (i < 3 && p.row_box < 64) continue;
+        CUtensorMap* m = i < 3 ? &maps.rows_part[i] : &maps.rows;
+        const int rows = i < 3 ? (i + 1) * (p.row_box / 4) : p.row_box;
+        rc = p.group > 1 ? encode_kblocks(m, X, S, R, 1, ldx, 0, rows, p.group, "rows")
+                         : encode_2d(m, bf16, 2, X, S, R, ldx, 64, rows, sw, "rows");
+      }
+      if (rc) return rc;
     }
   }
   LaunchInfo li = {};

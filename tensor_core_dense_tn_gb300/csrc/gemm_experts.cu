@@ -143,6 +143,7 @@ struct Note {
   int n;        // the MMA's N; 0 behind the last tile
   int sum;      // summation indices
   int empty;    // tiles without a sum before this one
+  int box;      // groups of k-blocks: rows that lie between one of a stage and the next
 };
 
 // The experts' first rows (E + 1) and first row blocks (E + 2: behind the
@@ -197,7 +198,7 @@ struct Tile {
   int k0, k_end, num_kb;      // weights: the expert's rows; else 0 and the sum's length
 };
 
-template <int CG, int OP>
+template <int CG, int OP, bool GROUPS>
 __device__ __forceinline__ Tile tile_of(int t, const ExpertsParams& p, const Table& tb) {
   constexpr int kStep = 16 * CG;
   Tile r;
@@ -232,7 +233,7 @@ __device__ __forceinline__ Tile tile_of(int t, const ExpertsParams& p, const Tab
     each = blocks == 1 ? high : ((high + blocks - 1) / blocks + kStep - 1) / kStep * kStep;
     r.k0 = 0;
     r.k_end = p.S;
-    r.num_kb = lo < p.E ? (p.S + kBlockK - 1) / kBlockK : 0;
+    r.num_kb = lo < p.E ? (p.S + kBlockK * (GROUPS ? p.group : 1) - 1) / (kBlockK * (GROUPS ? p.group : 1)) : 0;
   }
   // strips of p.strip row blocks, row blocks fastest within a strip
   int rb, cb;
@@ -255,10 +256,13 @@ __device__ __forceinline__ Tile tile_of(int t, const ExpertsParams& p, const Tab
 // ---------------------------------------------------------------- loads
 // A stage's columns from `col`, summation indices from k, to dst.  PAIR: on
 // the leader's barrier.  chunk: bytes from one chunk of 64 columns to the next.
-template <int OP, bool PAIR>
+template <int OP, bool PAIR, bool GROUPS>
 __device__ __forceinline__ void load_cols(uint32_t dst, const CUtensorMap* m, bool wide, int col, int k, int e, int chunk,
                                           uint32_t bar) {
-  if constexpr (OP == kExpertsForward) {
+  if constexpr (OP == kExpertsForward && GROUPS) {
+    if constexpr (PAIR) tma_load_4d_pair(dst, m, 0, col, k / 64, e, bar);
+    else tma_load_4d(dst, m, 0, col, k / 64, e, bar);
+  } else if constexpr (OP == kExpertsForward) {
     if constexpr (PAIR) tma_load_3d_pair(dst, m, k, col, e, bar);
     else tma_load_3d(dst, m, k, col, e, bar);
   } else if (wide) {
@@ -283,10 +287,13 @@ __device__ __forceinline__ void load_cols(uint32_t dst, const CUtensorMap* m, bo
 }
 
 // The same for the rows from `row`; chunks: of 64 rows (weights).
-template <int OP, bool PAIR>
+template <int OP, bool PAIR, bool GROUPS>
 __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* m, bool wide, int row, int k, int chunk,
                                           int chunks, uint32_t bar) {
-  if constexpr (OP != kExpertsWeights) {
+  if constexpr (GROUPS) {
+    if constexpr (PAIR) tma_load_3d_pair(dst, m, 0, row, k / 64, bar);
+    else tma_load_3d(dst, m, 0, row, k / 64, bar);
+  } else if constexpr (OP != kExpertsWeights) {
     if constexpr (PAIR) tma_load_2d_pair(dst, m, k, row, bar);
     else tma_load_2d(dst, m, k, row, bar);
   } else if (wide) {
@@ -420,7 +427,7 @@ __device__ __forceinline__ void add_c(const uint32_t (&x)[NR], float beta, bool 
   }
 }
 
-template <int CG, int OP>
+template <int CG, int OP, bool GROUPS>
 __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     gemm_experts_kernel(const __grid_constant__ ExpertsMaps maps, const __grid_constant__ ExpertsParams p) {
   using S_ = Shape<OP>;
@@ -429,8 +436,8 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sC = smem_u32(smem);                       // the columns' operand
-  const uint32_t sR = sC + p.stages * kColBytes;            // the rows' operand
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.stages * (kColBytes + p.row_bytes));
+  const uint32_t sR = sC + p.stages * p.group * kColBytes;            // the rows' operand
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + p.stages * p.group * (kColBytes + p.row_bytes));
   const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
@@ -451,6 +458,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
   const uint32_t rank = kPair ? cluster_ctarank() : 0;
   const bool leader = rank == 0;
   const int first_tile = blockIdx.x / CG, step = gridDim.x / CG;
+  const int group = GROUPS ? p.group : 1;      // k-blocks per stage
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -509,7 +517,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     };
     int empty = 0;          // tiles without a sum since the last note
     for (int t = first_tile; t < num_tiles && ok; t += step) {
-      Tile r = tile_of<CG, OP>(t, p, tb);
+      Tile r = tile_of<CG, OP, GROUPS>(t, p, tb);
       if (r.num_kb == 0) {
         ++empty;
         continue;
@@ -522,22 +530,23 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
       // the smallest box that holds the share: whole, 3/4, 1/2 or 1/4 (of at least 64 rows, else whole)
       const int box = S_::kWeights || p.row_box < 64 ? 3 : (4 * share - 1) / p.row_box;
       const int chunks = p.wide_rows ? p.row_bytes / kChunkBytes : (share + 63) / 64;    // weights
+      const int box_rows = box == 3 ? p.row_box : (box + 1) * (p.row_box / 4);
       const uint32_t tx =
-          (uint32_t)(p.col_tile * 128 + (S_::kWeights ? chunks * kChunkBytes : (box + 1) * (p.row_box / 4) * 128));
+          (uint32_t)(group * (p.col_tile * 128 + (S_::kWeights ? chunks * kChunkBytes : box_rows * 128)));
       const CUtensorMap* row_map = box == 3 ? &maps.rows : &maps.rows_part[box];
-      const int blocks = (sum + kBlockK - 1) / kBlockK, whole = S_::kWeights ? sum / kBlockK : blocks;
+      const int blocks = (sum + kBlockK * group - 1) / (kBlockK * group), whole = S_::kWeights ? sum / kBlockK : blocks;
       for (int kb = 0; kb < whole; ++kb) {
         ok = wait_empty(stage, phase ^ 1);
         if (!ok) break;
-        const int k = k0 + kb * kBlockK;
-        const uint32_t c = sC + stage * kColBytes, b = sR + stage * p.row_bytes;
+        const int k = k0 + kb * kBlockK * group;
+        const uint32_t c = sC + stage * group * kColBytes, b = sR + stage * group * p.row_bytes;
         const uint32_t fb = full_bar(stage);
         const uint32_t to = kPair ? mapa_shared(fb, 0) : fb;    // a pair's bytes all count on its leader's barrier
         if (elect_one()) {
-          if (kb == 0) notes[stage] = Note{n, sum, empty};
+          if (kb == 0) notes[stage] = Note{n, sum, empty, box_rows};
           if (leader) mbar_arrive_expect_tx(fb, tx * CG);
-          load_cols<OP, kPair>(c, &maps.cols, p.wide_cols, c_at, k, e, kChunkBytes, to);
-          load_rows<OP, kPair>(b, row_map, p.wide_rows, r_at, k, kChunkBytes, chunks, to);
+          load_cols<OP, kPair, GROUPS>(c, &maps.cols, p.wide_cols, c_at, k, e, kChunkBytes, to);
+          load_rows<OP, kPair, GROUPS>(b, row_map, p.wide_rows, r_at, k, kChunkBytes, chunks, to);
         }
         advance();
       }
@@ -553,7 +562,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
         const uint32_t fb = full_bar(stage), tail = tail_bar(stage);
         const uint32_t to = kPair ? mapa_shared(fb, 0) : fb;
         if (elect_one()) {
-          if (whole == 0) notes[stage] = Note{n, sum, empty};
+          if (whole == 0) notes[stage] = Note{n, sum, empty, 0};
           if (leader) {
             if (own) mbar_arrive(fb);
             else mbar_arrive_expect_tx(fb, part_tx * CG);
@@ -563,11 +572,11 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
             const uint32_t ci = sC + stage * kColBytes + i * (kColBytes / 4), bi = sR + stage * p.row_bytes + i * (p.row_bytes / 4);
             const int k = k0 + whole * kBlockK + 16 * i;
             if (own) {
-              load_cols<OP, false>(ci, &maps.cols_part, p.wide_cols, c_at, k, e, kPartBytes, tail);
-              load_rows<OP, false>(bi, &maps.rows_part[0], p.wide_rows, r_at, k, kPartBytes, chunks, tail);
+              load_cols<OP, false, false>(ci, &maps.cols_part, p.wide_cols, c_at, k, e, kPartBytes, tail);
+              load_rows<OP, false, false>(bi, &maps.rows_part[0], p.wide_rows, r_at, k, kPartBytes, chunks, tail);
             } else {
-              load_cols<OP, kPair>(ci, &maps.cols_part, p.wide_cols, c_at, k, e, kPartBytes, to);
-              load_rows<OP, kPair>(bi, &maps.rows_part[0], p.wide_rows, r_at, k, kPartBytes, chunks, to);
+              load_cols<OP, kPair, GROUPS>(ci, &maps.cols_part, p.wide_cols, c_at, k, e, kPartBytes, to);
+              load_rows<OP, kPair, GROUPS>(bi, &maps.rows_part[0], p.wide_rows, r_at, k, kPartBytes, chunks, to);
             }
           }
         }
@@ -576,7 +585,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
       empty = 0;
     }
     if (ok && leader && wait_empty(stage, phase ^ 1) && elect_one()) {
-      notes[stage] = Note{0, 0, empty};
+      notes[stage] = Note{0, 0, empty, 0};
       mbar_arrive(full_bar(stage));
     }
     if (!ok) settle(2000000);   // copies already issued land before teardown
@@ -613,7 +622,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
       while (true) {
         if (!wait_all(full_bar(stage), phase)) break;
         const int n = __shfl_sync(0xffffffffu, notes[stage].n, 0), sum = __shfl_sync(0xffffffffu, notes[stage].sum, 0);
-        const int empty = __shfl_sync(0xffffffffu, notes[stage].empty, 0);
+        const int empty = __shfl_sync(0xffffffffu, notes[stage].empty, 0), box = __shfl_sync(0xffffffffu, notes[stage].box, 0);
         bool ok = true;
         for (int i = 0; i < empty && ok; ++i) {       // their zeros are stored without a look at the accumulator
           ok = wait_all(acce_bar(acc), acc_phase ^ 1);
@@ -627,20 +636,28 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
         // Whole blocks; the last, shorter one apart: with the two in one loop,
         // and so its steps and strides in registers, the MMAs came with pauses
         // (2048 rows for each of 8 matrices of 8192 x 4096: 747 us, apart 625).
-        const int blocks = (sum + kBlockK - 1) / kBlockK, whole = S_::kWeights ? sum / kBlockK : blocks;
+        const int blocks = (sum + kBlockK * group - 1) / (kBlockK * group), whole = S_::kWeights ? sum / kBlockK : blocks;
         for (int kb = 0; kb < whole; ++kb) {
           if (kb > 0) ok = wait_all(full_bar(stage), phase);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t c = sC + stage * kColBytes, b = sR + stage * p.row_bytes;
+          const uint32_t c = sC + stage * group * kColBytes, b = sR + stage * group * p.row_bytes;
           const uint64_t c0 = S_::kMnCols ? desc_mn(c, kChunkBytes) : smem_desc_sw128(c);
           const uint64_t b0 = S_::kMnRows ? desc_mn(b, kChunkBytes) : smem_desc_sw128(b);
           // 16 summation indices are 32 bytes of a K-major operand's rows, 16 rows of each chunk of an MN-major one
           constexpr uint64_t kStepC = S_::kMnCols ? kPartBytes / 16 : 2, kStepR = S_::kMnRows ? kPartBytes / 16 : 2;
           if (elect_one()) {
+            if constexpr (GROUPS) {
+              for (int j = 0; j < group; ++j)
 #pragma unroll
-            for (int i = 0; i < kBlockK / 16; ++i)
-              mma_issue<CG, kKindF16>(d_tmem, c0 + kStepC * i, b0 + kStepR * i, idesc, (kb != 0 || i != 0) ? 1u : 0u);
+                for (int i = 0; i < kBlockK / 16; ++i)
+                  mma_issue<CG, kKindF16>(d_tmem, c0 + (uint64_t)(j * p.col_tile * 8 + 2 * i), b0 + (uint64_t)(j * box * 8 + 2 * i),
+                                          idesc, (kb != 0 || j != 0 || i != 0) ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int i = 0; i < kBlockK / 16; ++i)
+                mma_issue<CG, kKindF16>(d_tmem, c0 + kStepC * i, b0 + kStepR * i, idesc, (kb != 0 || i != 0) ? 1u : 0u);
+            }
             commit(empty_bar(stage));
           }
           advance();
@@ -687,7 +704,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     uint32_t acc_phase = 0;
     const uint32_t acce_target = kPair ? mapa_shared(acce_bar(acc), 0) : acce_bar(acc);
     for (int t = first_tile + acc * step; t < num_tiles; t += 2 * step) {
-      const Tile r = tile_of<CG, OP>(t, p, tb);
+      const Tile r = tile_of<CG, OP, GROUPS>(t, p, tb);
       const int col = r.col0 + (int)rank * p.col_tile + q * 32 + lane;
       const bool mine = q * 32 + lane < p.col_tile && col < p.cols_out;
       auto element = [&](const void* base, long long ld, long long stride, int row) {
@@ -749,7 +766,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     uint32_t tail_phase = 0;            // one bit per stage
     const int chunks = p.row_bytes / kChunkBytes;
     for (int t = first_tile; t < num_tiles; t += step) {
-      const Tile r = tile_of<CG, OP>(t, p, tb);
+      const Tile r = tile_of<CG, OP, GROUPS>(t, p, tb);
       const int last = (stage + r.num_kb - 1) % p.stages;      // (a tile without a sum is not ragged)
       stage = (stage + r.num_kb) % p.stages;
       if (!ragged(r)) continue;
@@ -781,23 +798,29 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
   }
 }
 
-const void* kernel_for(int cg, int op) {
-  static const void* const table[2][3] = {
-      {(const void*)gemm_experts_kernel<1, kExpertsForward>, (const void*)gemm_experts_kernel<1, kExpertsRows>,
-       (const void*)gemm_experts_kernel<1, kExpertsWeights>},
-      {(const void*)gemm_experts_kernel<2, kExpertsForward>, (const void*)gemm_experts_kernel<2, kExpertsRows>,
-       (const void*)gemm_experts_kernel<2, kExpertsWeights>}};
-  return table[cg - 1][op];
+// 0: products on single k-blocks, 1: on groups, 2: rows, 3: weights on single CTAs, 4: on pairs
+constexpr int kKernels = 5;
+
+int kernel_index(const ExpertsParams& p) {
+  return p.op == kExpertsForward ? (p.group > 1 ? 1 : 0) : p.op == kExpertsRows ? 2 : p.cg + 2;
 }
 
-int threads_of(int op) {
-  return op == kExpertsWeights ? Shape<kExpertsWeights>::kThreads : Shape<kExpertsForward>::kThreads;
+const void* kernel_of(int index) {
+  static const void* const table[kKernels] = {
+      (const void*)gemm_experts_kernel<2, kExpertsForward, false>, (const void*)gemm_experts_kernel<2, kExpertsForward, true>,
+      (const void*)gemm_experts_kernel<2, kExpertsRows, false>, (const void*)gemm_experts_kernel<1, kExpertsWeights, false>,
+      (const void*)gemm_experts_kernel<2, kExpertsWeights, false>};
+  return table[index];
+}
+
+int threads_of(int index) {
+  return index >= 3 ? Shape<kExpertsWeights>::kThreads : Shape<kExpertsForward>::kThreads;
 }
 
 constexpr int kSmemMax = 232448;
 
 int smem_bytes(const ExpertsParams& p) {
-  return 1024 + p.stages * (kColBytes + p.row_bytes) + kBars * 8 + 8 + kMaxStages * (int)sizeof(Note) + table_bytes(p.E);
+  return 1024 + p.stages * p.group * (kColBytes + p.row_bytes) + kBars * 8 + 8 + kMaxStages * (int)sizeof(Note) + table_bytes(p.E);
 }
 
 }  // namespace
@@ -835,8 +858,18 @@ void experts_geometry(ExpertsParams* p, int sms) {
   }
   p->acc_cols = 32;
   while (p->acc_cols < p->tile_rows) p->acc_cols *= 2;
+  // Boxes of four or two k-blocks, where three stages of them fit: an SM asks
+  // for the bytes of few rows sooner (one token through 2 of 8 matrices of 4096 x
+  // 4096: 17.4, with two 16.1, with four 13.3 us; 16 rows each for 64 of 4096 x
+  // 2048: 171, 163, 160; 32 rows each 172, 163, with four and two stages 173).
+  // With long tiles the code for it costs (a prompt 696, 725).
   p->stages = 0;
-  p->stages = (kSmemMax - smem_bytes(*p)) / (kColBytes + p->row_bytes);
+  p->group = 1;
+  const int room = kSmemMax - smem_bytes(*p);
+  if (p->op == kExpertsForward && average < 64 && p->S % kBlockK == 0)
+    for (int g = 4; g > 1 && p->group == 1; g /= 2)
+      if (p->S >= g * kBlockK && room >= 3 * g * (kColBytes + p->row_bytes)) p->group = g;
+  p->stages = room / (p->group * (kColBytes + p->row_bytes));
   if (p->stages > kMaxStages) p->stages = kMaxStages;
 }
 
@@ -852,7 +885,7 @@ FastDiv fast_div(uint32_t d) {
 
 cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cudaStream_t stream, LaunchInfo* info) {
   static bool configured[64] = {};
-  static int pairs[64][3] = {};
+  static int pairs[64][kKernels] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -867,19 +900,18 @@ cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cu
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   if (!configured[dev]) {
-    for (int op = 0; op < 3; ++op) {
-      for (int cg = 1; cg <= 2; ++cg)
-        if ((e = cudaFuncSetAttribute(kernel_for(cg, op), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax)))
-          return e;
+    for (int i = 0; i < kKernels; ++i) {
+      if ((e = cudaFuncSetAttribute(kernel_of(i), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax))) return e;
       cfg.gridDim = dim3(2);
-      cfg.blockDim = dim3(threads_of(op));
+      cfg.blockDim = dim3(threads_of(i));
       cfg.dynamicSmemBytes = kSmemMax;
       cfg.numAttrs = 1;
-      if ((e = cudaOccupancyMaxActiveClusters(&pairs[dev][op], kernel_for(2, op), &cfg))) return e;
+      if (i != 3 && (e = cudaOccupancyMaxActiveClusters(&pairs[dev][i], kernel_of(i), &cfg))) return e;
     }
     configured[dev] = true;
   }
-  const int most = p.cg == 2 ? pairs[dev][p.op] : sms;
+  const int index = kernel_index(p);
+  const int most = p.cg == 2 ? pairs[dev][index] : sms;
   if (most < 1) return cudaErrorInvalidConfiguration;
   // Tiles: known for the weights' gradient; else the most that the rows can
   // make, each expert and the rows of nobody ending with one part tile.
@@ -888,7 +920,7 @@ cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cu
   const int units = (int)(blocks * p.col_blocks < most ? blocks * p.col_blocks : most);
   attr[0].val.clusterDim.x = p.cg;
   cfg.gridDim = dim3(units * p.cg);
-  cfg.blockDim = dim3(threads_of(p.op));
+  cfg.blockDim = dim3(threads_of(index));
   cfg.dynamicSmemBytes = smem_bytes(p);
   cfg.stream = stream;
   cfg.numAttrs = 2;
@@ -902,15 +934,16 @@ cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cu
   info->smem_bytes = cfg.dynamicSmemBytes;
   info->k_parts = 1;
   info->scheduler = 1;
-  static const char* const names[3] = {"gemm_experts_kernel<forward>", "gemm_experts_kernel<rows>",
-                                       "gemm_experts_kernel<weights>"};
-  info->kernel = names[p.op];
+  static const char* const names[kKernels] = {"gemm_experts_kernel<forward>", "gemm_experts_kernel<forward, groups>",
+                                              "gemm_experts_kernel<rows>", "gemm_experts_kernel<weights, 1>",
+                                              "gemm_experts_kernel<weights, 2>"};
+  info->kernel = names[index];
   p.by_cols = fast_div(p.col_blocks);
   p.by_tiles = fast_div(p.row_blocks * p.col_blocks);
   p.by_strip = fast_div(p.strip);
   p.by_strip_tiles = fast_div(p.strip * p.col_blocks);
   void* args[2] = {const_cast<ExpertsMaps*>(&maps), &p};
-  return cudaLaunchKernelExC(&cfg, kernel_for(p.cg, p.op), args);
+  return cudaLaunchKernelExC(&cfg, kernel_of(index), args);
 }
 
 }  // namespace gtn

@@ -228,7 +228,8 @@ struct ExpertsParams {
   int col_tile;        // columns per CTA of a tile, at most 128 (forward: any multiple of 16; else 128)
   int row_box;         // forward, rows: rows of their operand per TMA box (a CTA's share of a tile)
   int wide_cols, wide_rows;                // MN-major operands: one box for all of a CTA's columns (or rows) of a stage
-  int row_bytes;       // rows' operand in a ring stage of a CTA
+  int group;           // forward: k-blocks per ring stage
+  int row_bytes;       // rows' operand in a k-block of a CTA
   int stages, acc_cols;                    // ring stages, columns of one accumulator
   int row_blocks, col_blocks;              // weights: tiles of a matrix; else col_blocks alone
   int strip;           // row blocks per strip of the tile order
