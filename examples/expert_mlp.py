@@ -2,8 +2,9 @@
 
     y[t] = sum_j w[t, j] * down_e( silu( up_e( x[t] ) ) ),   e = the token's j-th expert
 
-Training: dispatch, two grouped bf16 products, combine, and the gradients of
-all of them.  Decoding: the experts' matrices held in 4 bits, the plan of a
+Training: dispatch, two bf16 products by expert, combine, and the gradients of
+all of them, clipped by their norm; nothing waits for the experts' row counts.
+Decoding: the experts' matrices held in 4 bits, the plan of a
 step and its products on few tokens, captured in a CUDA graph.
 
     python examples/expert_mlp.py
@@ -22,23 +23,6 @@ def route(x, gate, k):
     logits = x.float() @ gate.float().T
     top, ids = torch.topk(logits, k, dim=1)
     return ids, torch.softmax(top, dim=1)
-
-
-def _stream():
-    return torch.cuda.current_stream().cuda_stream
-
-
-def grouped(A, bounds, B):
-    """Rows bounds[e] .. bounds[e + 1] of A times B[e].T, one launch for all experts."""
-    D = torch.zeros(A.shape[0], B.shape[1], dtype=A.dtype, device=A.device)
-    problems = [dict(M=hi - lo, N=B.shape[1], K=B.shape[2], A=A[lo:].data_ptr(), lda=A.stride(0), B=B[e].data_ptr(),
-                     ldb=B.stride(1), C=None, ldc=0, D=D[lo:].data_ptr(), ldd=D.stride(0))
-                for e, (lo, hi) in enumerate(zip(bounds, bounds[1:])) if hi > lo]
-    if problems:
-        rc = g.gemm_bf16_tn_grouped(problems, 1.0, 0.0, g.OUT_BF16, _stream())
-        if rc:
-            raise RuntimeError(f"grouped GEMM failed: {rc}")
-    return D
 
 
 class Dispatch(torch.autograd.Function):
@@ -75,18 +59,15 @@ class ExpertLinear(torch.autograd.Function):
     """Each expert's rows times its matrix."""
 
     @staticmethod
-    def forward(ctx, A, W, bounds):
-        ctx.bounds = bounds
-        ctx.save_for_backward(A, W)
-        return grouped(A, bounds, W)
+    def forward(ctx, A, W, plan):
+        ctx.save_for_backward(A, W, plan.offsets, plan.slot_row, plan.row_token)
+        return g.gemm_experts(A, W, plan)
 
     @staticmethod
     def backward(ctx, dD):
-        A, W = ctx.saved_tensors
-        dD = dD.contiguous()
-        dA = grouped(dD, ctx.bounds, W.transpose(1, 2).contiguous())
-        dW = torch.stack([dD[lo:hi].T @ A[lo:hi] for lo, hi in zip(ctx.bounds, ctx.bounds[1:])])
-        return dA, dW, None
+        A, W, *arrays = ctx.saved_tensors
+        plan, dD = g.ExpertPlan.of(*arrays), dD.contiguous()
+        return g.gemm_experts_backward_a(dD, W, plan), g.gemm_experts_backward_w(dD, A, plan), None
 
 
 def train_forward(x, gate, up, down, k):
@@ -94,9 +75,8 @@ def train_forward(x, gate, up, down, k):
     ids, weights = route(x, gate, k)
     plan = g.ExpertPlan(x.shape[0], k, gate.shape[0], x.device)
     rows = Dispatch.apply(x, ids, plan)
-    bounds = plan.offsets.tolist()          # the grouped call's row counts live on the host
-    hidden = torch.nn.functional.silu(ExpertLinear.apply(rows, up, bounds))
-    return Combine.apply(ExpertLinear.apply(hidden, down, bounds), weights, plan)
+    hidden = torch.nn.functional.silu(ExpertLinear.apply(rows, up, plan))
+    return Combine.apply(ExpertLinear.apply(hidden, down, plan), weights, plan)
 
 
 def to_4_bits(W, group):
@@ -151,7 +131,9 @@ def main():
     y = train_forward(x, gate, up, down, k)
     loss = y.float().square().mean()
     loss.backward()
-    print(f"training: {T} tokens through {k} of {E} experts, loss {loss.item():.5f}, |dx| {x.grad.float().norm():.3f}")
+    norm = g.clip_grad_norm([up.grad, down.grad], 1e-3)
+    print(f"training: {T} tokens through {k} of {E} experts, loss {loss.item():.5f}, |dx| {x.grad.float().norm():.3f}, "
+          f"gradients of the experts {norm.item():.5f}, clipped to {g.grad_norm([up.grad, down.grad]).item():.5f}")
     with torch.no_grad():
         decoder = Decoder(8, k, gate, up, down)
         full = train_forward(x[:8], gate, up, down, k)

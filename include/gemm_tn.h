@@ -665,8 +665,9 @@ int gemm_bf16_tn_experts_backward_w(const gemm_expert_plan *plan, int64_t N, int
  * The lists are host arrays, read during the call only; the tensors are dense
  * (count consecutive values) device memory aligned to their element size, of
  * any types mixed.  out: NULL for in place, else one tensor for each input with
- * its count, of either type; an output is its input's own memory or overlaps
- * no tensor.  norm: one fp32 in device memory.  workspace: device memory of
+ * its count, of either type; an output is its input's own memory, in its type,
+ * or overlaps no tensor (GEMM_ERR_INVALID_VALUE otherwise; so a clip takes no
+ * tensor twice).  norm: one fp32 in device memory.  workspace: device memory of
  * gemm_grad_workspace(num) bytes, 8-byte aligned, whose contents do not matter;
  * calls that may run at the same time need one each.  No other memory is used,
  * so the calls may be captured and replayed on any stream. */

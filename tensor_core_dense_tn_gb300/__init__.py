@@ -830,17 +830,18 @@ _GRAD_WORKSPACE = {}        # number of tensors -> bytes
 
 
 def _norm_buffers(num, gpu, norm, stream):
-    """The norm's tensor and the workspace, which is kept for the stream that uses it."""
+    """The norm's tensor and the workspace.  With a stream of the caller's they come from that stream's memory: the
+    workspace is given back when the call returns, and must neither be in use on the current stream still nor be used
+    there while the kernels run on the other."""
     torch = _torch
-    nbytes = _GRAD_WORKSPACE.get(num) or _GRAD_WORKSPACE.setdefault(num, (_lib or load()).gemm_grad_workspace(num))
-    work = torch.empty(nbytes, dtype=torch.uint8, device=gpu)
-    if norm is None:
-        norm = torch.empty((), dtype=torch.float32, device=gpu)
-    elif norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != gpu:
+    if norm is not None and (norm.dtype != torch.float32 or norm.numel() != 1 or norm.get_device() != gpu):
         raise ValueError(f"norm must be one fp32 on GPU {gpu}")
-    if stream:
-        work.record_stream(torch.cuda.ExternalStream(stream, device=gpu))
-    return norm, work
+    nbytes = _GRAD_WORKSPACE.get(num) or _GRAD_WORKSPACE.setdefault(num, (_lib or load()).gemm_grad_workspace(num))
+    if stream is not None:
+        with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=gpu) if stream else torch.cuda.default_stream(gpu)):
+            return _norm_buffers(num, gpu, norm, None)
+    work = torch.empty(nbytes, dtype=torch.uint8, device=gpu)
+    return torch.empty((), dtype=torch.float32, device=gpu) if norm is None else norm, work
 
 
 def grad_norm(tensors, norm=None, stream=None):
@@ -860,7 +861,7 @@ def grad_norm(tensors, norm=None, stream=None):
 def clip_grad_norm(tensors, max_norm: float, out=None, norm=None, stream=None):
     """Multiplies all values by max_norm / norm where their norm (grad_norm()) is above max_norm, in place, or into the
     tensors `out` (bf16 or fp32, contiguous for contiguous tensors, else of their strides; also where nothing is
-    scaled).  Returns the norm from
+    scaled).  No tensor may be there twice or overlap another.  Returns the norm from
     before.  A norm that is not finite changes nothing.  In place, values within max_norm are not written; the
     tensors' versions count as changed all the same."""
     torch = _torch or _t()

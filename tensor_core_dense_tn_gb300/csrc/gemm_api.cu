@@ -11,6 +11,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -1191,6 +1192,34 @@ int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, cons
 }
 
 // ---------------------------------------------------------------- gradient norm
+// Whether some output overlaps another, or the input of another, or its own
+// without being it: those would be scaled twice, or before they are read.
+bool clip_overlaps(const std::vector<GradTensor>& list) {
+  struct Span {
+    uintptr_t begin, end;
+    size_t index;
+  };
+  static thread_local std::vector<Span> outs;
+  outs.clear();
+  for (size_t i = 0; i < list.size(); ++i) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(list[i].out);
+    outs.push_back({at, at + (uintptr_t)list[i].count * (list[i].out_f32 ? 4 : 2), i});
+  }
+  std::sort(outs.begin(), outs.end(), [](const Span& a, const Span& b) { return a.begin < b.begin; });
+  for (size_t i = 1; i < outs.size(); ++i)
+    if (outs[i].begin < outs[i - 1].end) return true;
+  for (size_t i = 0; i < list.size(); ++i) {
+    const GradTensor& t = list[i];
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(t.in), end = begin + (uintptr_t)t.count * (t.in_f32 ? 4 : 2);
+    // (the outputs are apart: only those from the last that begins at or before `begin` on can touch)
+    auto at = std::upper_bound(outs.begin(), outs.end(), begin, [](uintptr_t v, const Span& s) { return v < s.begin; });
+    if (at != outs.begin()) --at;
+    for (; at != outs.end() && at->begin < end; ++at)
+      if (at->end > begin && !(at->index == i && t.in == t.out && t.in_f32 == t.out_f32)) return true;
+  }
+  return false;
+}
+
 // out: nullptr = in place.  Without `clip` only the norm.
 int run_grad_norm(int num, const gemm_tensor* tensors, bool clip, float max_norm, const gemm_tensor* out, float* norm,
                   void* workspace, void* stream_v) {
@@ -1228,6 +1257,7 @@ int run_grad_norm(int num, const gemm_tensor* tensors, bool clip, float max_norm
     g.vector = aligned16(static_cast<const char*>(o.data) + (int64_t)g.head * os);
     list.push_back(g);
   }
+  if (clip && clip_overlaps(list)) return fail(GEMM_ERR_INVALID_VALUE, "an output overlaps another tensor");
   int dev = 0;
   DeviceState* st = nullptr;
   int rc = init_device(&dev, &st);

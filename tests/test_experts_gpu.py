@@ -289,3 +289,95 @@ def test_tiles_without_a_sum_between_others_many_times():
     check(first[0], *forward64(A, W, plan), 1024, True)
     check(first[1], *forward64(dD, W.transpose(1, 2), plan), 2048, True)
     check(first[2], *weights64(dD, A, plan), 1800, True)
+
+
+def test_a_training_step_without_the_host():
+    """Dispatch, two products, combine, the gradients of all, added up over two micro-batches, and the clip, captured in
+    one graph and replayed on other tokens and routes, against the formulas in 64 bits.  Every stage rounds to bf16
+    once (2^-9 of a value); norms of errors are compared with 2^-6 of the norms, eight times that."""
+    T, k, E, H, F = 96, 2, 5, 64, 136
+    x, dout = values((T, H), 1, False), values((T, H), 2, False)
+    ids = torch.zeros(T, k, dtype=torch.int64, device="cuda")
+    w = torch.rand(T, k, generator=gen(3), device="cuda")
+    up, down = values((E, F, H), 4, False) * H ** -0.5, values((E, H, F), 5, False) * F ** -0.5
+    plan = g.ExpertPlan(T, k, E, "cuda")
+    sums = [torch.zeros(E, F, H, device="cuda"), torch.zeros(E, H, F, device="cuda")]
+    clipped = [torch.empty_like(t, dtype=BF16) for t in sums]
+    limit = 5.0
+
+    def step():
+        for i in range(2):
+            rows = g.expert_dispatch(ids, plan, x)
+            hidden = g.gemm_experts(rows, up, plan, activation=g.ACT_RELU)
+            Y = g.gemm_experts(hidden, down, plan)
+            out = g.expert_combine(plan, Y, w)
+            dY, dw = g.expert_combine_backward(plan, Y, w, dout)
+            dhidden = g.gemm_experts_backward_a(dY, down, plan) * (hidden > 0)
+            for total, a, b in ((sums[1], dY, hidden), (sums[0], dhidden, rows)):
+                g.gemm_experts_backward_w(a, b, plan, beta=float(i), C=total, out=total)
+            dx = g.expert_dispatch_backward(plan, g.gemm_experts_backward_a(dhidden, up, plan))
+        return out, dx, dw, g.clip_grad_norm(sums, limit, out=clipped)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            held = step()
+    torch.cuda.current_stream().wait_stream(side)
+    near = lambda a, b: ((a.double() - b).norm() <= 2.0 ** -6 * b.norm()).item()  # noqa: E731
+    for seed in range(3):
+        ids.copy_(torch.randint(-1, E, (T, k), generator=gen(70 + seed), device="cuda"))
+        x.copy_(values((T, H), 80 + seed, False))
+        graph.replay()
+        status()
+        wide = [t.double().requires_grad_() for t in (x, w, up, down)]
+        y = torch.zeros(T, H, dtype=torch.float64, device="cuda")
+        for j in range(k):
+            e = ids[:, j].clamp(min=0)
+            h = torch.relu(torch.einsum("th,tfh->tf", wide[0], wide[2][e]))
+            y = y + ((ids[:, j] >= 0) * wide[1][:, j])[:, None] * torch.einsum("tf,thf->th", h, wide[3][e])
+        y.backward(dout.double())
+        out, dx, dw, norm = held
+        gx, gw, gup, gdown = [t.grad for t in wide]
+        assert near(out, y.detach()) and near(dx, gx) and near(dw, gw * (ids >= 0))
+        assert near(sums[0], 2 * gup) and near(sums[1], 2 * gdown)
+        want = 2 * torch.sqrt(gup.square().sum() + gdown.square().sum())
+        assert abs(norm.item() - want.item()) <= 2.0 ** -6 * want.item()
+        for c, t in zip(clipped, sums):
+            assert torch.all((c.double() - t.double() * min(1.0, limit / norm.item())).abs() <= 2.0 ** -8 * 1.01 * t.double().abs())
+
+
+@pytest.mark.parametrize("what", ["rows", "columns"])
+def test_places_beyond_2_31(what):
+    """Outputs and operands of more than 2^31 elements, a few of whose values are looked at."""
+    if torch.cuda.get_device_properties(0).total_memory < 60 << 30:
+        pytest.skip("needs 60 GB")
+    R, N, K, E = (70000, 40000, 64, 3) if what == "rows" else (64, 1 << 15, 1 << 15, 3)
+    counts = [R - 30, 0, 29]
+    plan = plan_of(counts, 1)
+    A, W = values((R, K), 1, True), values((E, N, K), 2, True)
+    D = g.gemm_experts(A, W, plan)
+    status()
+    rows = torch.tensor([0, R // 2, R - 31, R - 30, R - 2, R - 1], device="cuda")
+    cols = torch.tensor([0, 1, N // 2, N - 1], device="cuda")
+    for r in rows.tolist():
+        e = 0 if r < counts[0] else 2 if r < R - 1 else None
+        want = torch.zeros(len(cols), dtype=torch.float64, device="cuda") if e is None else W[e][cols].double() @ A[r].double()
+        assert torch.equal(D[r, cols], want.to(F32).to(BF16))
+    dD = D.clamp_(-3, 3)
+    dD[R - 1] = 1.0
+    dA = g.gemm_experts_backward_a(dD, W, plan, out_dtype=F32)
+    for r in (0, R - 30, R - 2):
+        e = 0 if r < counts[0] else 2
+        assert torch.equal(dA[r].double(), dD[r].double() @ W[e].double())
+    assert torch.all(dA[R - 1] == 0)
+    del D, dA
+    dW = g.gemm_experts_backward_w(dD, A, plan)
+    status()
+    for e, lo, hi in ((0, 0, counts[0]), (2, counts[0], R - 1)):
+        want = dD[lo:hi, cols].double().T @ A[lo:hi].double()
+        assert torch.equal(dW[e, cols], want.to(F32).to(BF16))
+    assert torch.all(dW[1] == 0)

@@ -219,6 +219,30 @@ def test_two_calls_at_once():
         assert abs(n.item() - norm64(ts)) <= NORM_EPS * norm64(ts)
 
 
+def test_a_workspace_from_another_streams_memory():
+    """The workspace of a call on another stream is not memory that the current stream has given back but still uses."""
+    ts = tensors_of([200000, 31], 41)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(10):
+        a = torch.full((2560 // 4,), 3.0, device="cuda")        # of a workspace's size
+        for _ in range(50):
+            a = a * 1.0
+        g.grad_norm(ts, stream=side.cuda_stream)
+        assert torch.all(a == 3.0)
+    g.grad_norm(ts, stream=0)
+    torch.cuda.synchronize()
+
+
+def test_the_same_tensor_twice():
+    t = torch.randn(1000, device="cuda")
+    b = t.clone()
+    assert abs(g.grad_norm([t, t]).item() - norm64([t, t])) <= NORM_EPS * norm64([t, t])
+    with pytest.raises(g.GemmError):
+        g.clip_grad_norm([t, t], 1.0)
+    assert torch.equal(t, b)
+
+
 def test_versions():
     """In place counts as a change of the tensors; into others does not."""
     t, o = torch.randn(100, device="cuda"), torch.empty(100, device="cuda")

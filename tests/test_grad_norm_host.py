@@ -1,4 +1,5 @@
 """Refusals of the gradient norm's calls, and what the wrappers hand to the C ABI, without a GPU."""
+import contextlib
 import ctypes
 
 import pytest
@@ -55,6 +56,28 @@ def test_bad_clips(built, max_norm, out, code):
     refused(g.gemm_clip_grad_norm(1, array(GOOD), max_norm, None if out is None else array(*out), 0x1000, 0x2000, 0), code)
 
 
+@pytest.mark.parametrize("rows,out", [
+    ([(0x10000, 100, 1), (0x10000, 100, 1)], None), ([(0x10000, 100, 1), (0x10000 + 396, 100, 1)], None),
+    ([(0x10000, 100, 0), (0x10000 - 198, 100, 0)], None), ([(0x10000, 9, 1)], [(0x10000, 9, 0)]),
+    ([(0x10000, 100, 1)], [(0x10004, 100, 1)]), ([(0x10000, 8, 1), (0x20000, 8, 1)], [(0x20000, 8, 1), (0x10000, 8, 1)]),
+    ([(0x10000, 8, 1), (0x20000, 8, 1)], [(0x30000, 8, 1), (0x3001C, 8, 1)]),
+    ([(0x10000, 1000, 1), (0x40000, 8, 1)], [(0x50000, 1000, 1), (0x10100, 8, 1)]),
+])
+def test_outputs_that_overlap_are_refused(built, rows, out):
+    """They would be scaled twice, or before they are read."""
+    refused(g.gemm_clip_grad_norm(len(rows), array(*rows), 1.0, None if out is None else array(*out), 0x1000, 0x2000, 0), INV)
+    assert "overlap" in g.last_error()
+
+
+def test_neighbours_do_not_overlap(built):
+    """Without a GPU the call gets as far as asking for the device."""
+    rows = [(0x10000, 100, 1), (0x10000 + 400, 100, 0), (0x10000 + 600, 3, 0)]
+    for out in (None, rows, [(r[0] + 0x100000, *r[1:]) for r in rows]):
+        g.gemm_clip_grad_norm(3, array(*rows), 1.0, None if out is None else array(*out), 0x1000, 0x2000, 0) \
+            if not torch.cuda.is_available() else None
+        assert "overlap" not in g.last_error()
+
+
 def test_workspace(built):
     assert g.gemm_grad_workspace(-1) == 0
     sizes = [g.gemm_grad_workspace(n) for n in (0, 1, 960, 961, 5000)]
@@ -75,6 +98,8 @@ def lib(monkeypatch):
     monkeypatch.setattr(g, "_several_gpus", True)
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(g, "_GRAD_WORKSPACE", {})
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda gpu: None)
     empty = torch.empty
     monkeypatch.setattr(torch, "empty", lambda *a, **k: gpu(empty(*a, **{n: v for n, v in k.items() if n != "device"})))
     return recorder
