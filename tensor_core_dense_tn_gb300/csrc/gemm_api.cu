@@ -1156,6 +1156,13 @@ int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, cons
   if (col_blocks * most >= kMaxDim - 4096) return fail(GEMM_ERR_INVALID_VALUE, "too many tiles");
   p.col_blocks = (int)col_blocks;
   p.row_blocks = weights ? (int)row_blocks : 0;
+  if (weights) {
+    // equal blocks (with 256, 256, 256 and 11 rows for 779, every fourth CTA
+    // would get nothing but elevens), of whole boxes where one holds them all
+    p.wide_rows = N % (64 * p.cg) == 0;
+    const int64_t step = (p.wide_rows ? 64 : 16) * p.cg;
+    p.row_block = (int)(((N + row_blocks - 1) / row_blocks + step - 1) / step * step);
+  }
   p.strip = weights ? 8 : raster_group_for(p.tile_rows, sum, 2, 16);
   ExpertsMaps maps;
   memset(&maps, 0, sizeof maps);
@@ -1164,7 +1171,6 @@ int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, cons
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     if (weights) {
       p.wide_cols = K % 64 == 0;
-      p.wide_rows = N % (64 * p.cg) == 0;
       const int chunks = p.tile_rows / p.cg / 64;
       if ((rc = encode_chunks(&maps.cols, Y, K, R, 1, ldy, 0, 64, p.wide_cols ? 2 : 0, "A")) ||
           (rc = encode_chunks(&maps.cols_part, Y, K, R, 1, ldy, 0, 16, p.wide_cols ? 2 : 0, "A")) ||

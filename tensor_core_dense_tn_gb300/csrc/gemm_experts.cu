@@ -209,7 +209,7 @@ __device__ __forceinline__ Tile tile_of(int t, const ExpertsParams& p, const Tab
     blocks = p.row_blocks;
     first = 0;
     high = p.rows_out;
-    each = p.tile_rows;
+    each = p.row_block;
     r.k0 = tb.row[r.e];
     r.k_end = tb.row[r.e + 1];
     r.num_kb = (r.k_end - r.k0 + kBlockK - 1) / kBlockK;

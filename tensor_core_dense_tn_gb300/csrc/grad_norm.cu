@@ -95,37 +95,40 @@ __device__ __forceinline__ int tensor_of(const int* firsts, int chunk, int lo, i
   return lo;
 }
 
-// A chunk's place: its tensor, this thread's first vector and their number.
+// A chunk's place: its tensor, this thread's first vector and how many there are from it on.
 struct Place {
-  const uint4* in;
-  long long at, vectors;
-  int tensor;
+  long long at;
+  int left, tensor;
 };
 
+__device__ __forceinline__ long long vectors_of(const GradTensor& t) { return (t.count - t.head) * (t.in_f32 ? 4 : 2) / 16; }
+
 template <int CAP>
-__device__ __forceinline__ Place place_of(const List<CAP>& l, const int* firsts, int chunk, int lo, int hi) {
+__device__ __forceinline__ Place place_in(const List<CAP>& l, int chunk, int tensor) {
   Place r;
-  r.tensor = tensor_of(firsts, chunk, lo, hi);
-  const GradTensor& t = l.t[r.tensor];
-  const int size = t.in_f32 ? 4 : 2;
-  r.in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(t.in) + t.head * size);
-  r.vectors = (t.count - t.head) * size / 16;
+  const GradTensor& t = l.t[tensor];
+  r.tensor = tensor;
   r.at = (long long)(chunk - t.first) * kChunkVectors + threadIdx.x;
+  const long long left = vectors_of(t) - r.at;
+  r.left = left < kChunkVectors ? (int)left : kChunkVectors;
   return r;
 }
 
-__device__ __forceinline__ void load_vectors(const Place& r, uint4 (&x)[kVectors]) {
+template <int CAP>
+__device__ __forceinline__ void load_vectors(const List<CAP>& l, const Place& r, uint4 (&x)[kVectors]) {
+  const GradTensor& t = l.t[r.tensor];
+  const uint4* in = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(t.in) + t.head * (t.in_f32 ? 4 : 2)) + r.at;
 #pragma unroll
-  for (int u = 0; u < kVectors; ++u)
-    x[u] = r.at + u * kThreads < r.vectors ? r.in[r.at + u * kThreads] : make_uint4(0, 0, 0, 0);
+  for (int u = 0; u < kVectors; ++u) x[u] = u * kThreads < r.left ? in[u * kThreads] : make_uint4(0, 0, 0, 0);
 }
 
 // The values of a tensor before its first vector and behind its last, one per
 // thread of the first 16: calls f(index).
 template <typename F>
-__device__ __forceinline__ void for_ends(const GradTensor& t, long long vectors, F f) {
+__device__ __forceinline__ void for_ends(const GradTensor& t, F f) {
   if (threadIdx.x < 16) {
-    const long long i = threadIdx.x < 8 ? threadIdx.x : t.head + vectors * (t.in_f32 ? 4 : 8) + (threadIdx.x - 8);
+    const long long i =
+        threadIdx.x < 8 ? threadIdx.x : t.head + vectors_of(t) * (t.in_f32 ? 4 : 8) + (threadIdx.x - 8);
     if (threadIdx.x < 8 ? i < t.head : i < t.count) f(i);
   }
 }
@@ -155,15 +158,13 @@ __device__ __forceinline__ double block_sum(double v, Sums& shared) {
   return shared.all;
 }
 
-// The squares of vectors in fp64, for fp32 sums that hold too little or too
-// much; vectors of zeros add nothing without fp64 work.
+// The squares of vectors in fp64, for fp32 sums that hold too little or too much.
 template <bool F32>
 __device__ __noinline__ double squares64(uint4 a, uint4 b, uint4 c, uint4 d) {
   double s = 0.0;
 #pragma unroll 1
   for (int u = 0; u < kVectors; ++u) {
     const uint4 x = u == 0 ? a : u == 1 ? b : u == 2 ? c : d;
-    if (((x.x | x.y | x.z | x.w) & (F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) continue;
     float v[F32 ? 4 : 8];
     unpack<F32>(x, v);
 #pragma unroll
@@ -186,6 +187,10 @@ __device__ __forceinline__ double squares(const uint4 (&x)[kVectors]) {
   // Squares below 2^-126 lose bits, or all: with a sum above 2^-80 what is
   // lost is below 2^-41 of it.
   if (all >= 0x1p-80f && all <= 0x1p127f) return (double)all;
+  uint32_t any = 0;      // zeros (also those behind a tensor's end) take no fp64 work
+#pragma unroll
+  for (int u = 0; u < kVectors; ++u) any |= x[u].x | x[u].y | x[u].z | x[u].w;
+  if ((any & (F32 ? 0x7FFFFFFFu : 0x7FFF7FFFu)) == 0) return 0.0;
   return squares64<F32>(x[0], x[1], x[2], x[3]);
 }
 
@@ -199,9 +204,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   griddep_launch_dependents();
   double sum = 0.0;
   int chunk = blockIdx.x;
-  Place r = place_of(l, firsts, chunk, 0, l.count - 1);
+  Place r = place_in(l, chunk, tensor_of(firsts, chunk, 0, l.count - 1));
   uint4 x[kVectors];
-  load_vectors(r, x);
+  load_vectors(l, r, x);
   while (true) {
     // the next chunk's vectors are on their way while these are summed
     const int next = chunk + gridDim.x;
@@ -210,14 +215,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     uint4 y[kVectors];
     if (more) {
       const bool same = r.tensor + 1 == l.count || firsts[r.tensor + 1] > next;
-      if (same) rn.at += (long long)gridDim.x * kChunkVectors;
-      else rn = place_of(l, firsts, next, r.tensor + 1, l.count - 1);
-      load_vectors(rn, y);
+      rn = place_in(l, next, same ? r.tensor : tensor_of(firsts, next, r.tensor + 1, l.count - 1));
+      load_vectors(l, rn, y);
     }
     const GradTensor& t = l.t[r.tensor];
     sum += t.in_f32 ? squares<true>(x) : squares<false>(x);
     if (chunk == t.first)
-      for_ends(t, r.vectors, [&](long long i) {
+      for_ends(t, [&](long long i) {
         const double v = load1(t.in, t.in_f32, i);
         sum += v * v;
       });
@@ -238,25 +242,39 @@ __device__ __forceinline__ double total(const Task& k, Sums& shared) {
   return block_sum(s, shared);
 }
 
-// A vector's values times both factors, to their place in `out`.
+// A vector's values times both factors, `at` vectors behind `out`; `valid`: the
+// vector is there.  All lanes of a warp call it: bf16 to fp32, a vector becomes
+// 32 bytes, which one lane would store in halves of sectors (210 million values
+// clipped: 1017 us), so a pair of lanes stores first the even lane's, then the
+// odd lane's (273 us).
 template <bool F32>
-__device__ __forceinline__ void store_scaled(uint8_t* out, long long at, uint4 x, float first, float c, bool out_f32) {
+__device__ __forceinline__ void store_scaled(uint8_t* out, int at, bool valid, uint4 x, float first, float c, bool out_f32) {
   constexpr int kPer = F32 ? 4 : 8;
   float v[kPer];
   unpack<F32>(x, v);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) v[i] = v[i] * first * c;
-  if (out_f32) {
-    float4* to = reinterpret_cast<float4*>(out) + at * (kPer / 4);
-#pragma unroll
-    for (int i = 0; i < kPer / 4; ++i) __stcs(to + i, make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]));
+  if constexpr (F32) {
+    if (!valid) return;
+    if (out_f32) __stcs(reinterpret_cast<float4*>(out) + at, make_float4(v[0], v[1], v[2], v[3]));
+    else __stcs(reinterpret_cast<uint2*>(out) + at, make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
+  } else if (!out_f32) {
+    if (valid)
+      __stcs(reinterpret_cast<uint4*>(out) + at, make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                            pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
   } else {
-    uint2* to = reinterpret_cast<uint2*>(out) + at * (kPer / 4);
-    if constexpr (F32)
-      __stcs(to, make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])));
-    else
-      __stcs(reinterpret_cast<uint4*>(to), make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                      pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])));
+    const int odd = threadIdx.x & 1;
+    // the other lane's half of its own vector that this lane stores, into the half it does not need
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float got = __shfl_xor_sync(0xffffffffu, odd ? v[i] : v[4 + i], 1);
+      if (odd) v[i] = got;
+      else v[4 + i] = got;
+    }
+    const bool other = __shfl_xor_sync(0xffffffffu, (int)valid, 1);
+    float4* to = reinterpret_cast<float4*>(out) + at * 2 - odd;
+    if (odd ? other : valid) __stcs(to, make_float4(v[0], v[1], v[2], v[3]));              // the even lane's vector
+    if (odd ? valid : other) __stcs(to + 2, make_float4(v[4], v[5], v[6], v[7]));          // the odd lane's
   }
 }
 
@@ -297,38 +315,37 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   const float first = factors[0], c = factors[1];
   // backwards through the chunks, the next one's vectors on their way while these are scaled
   int chunk = l.chunks - 1 - (int)blockIdx.x;
-  Place r = place_of(l, firsts, chunk, 0, l.count - 1);
+  Place r = place_in(l, chunk, tensor_of(firsts, chunk, 0, l.count - 1));
   uint4 x[kVectors];
-  if (l.t[r.tensor].vector) load_vectors(r, x);
+  if (l.t[r.tensor].vector) load_vectors(l, r, x);
   while (true) {
     const int next = chunk - (int)gridDim.x;
     Place rn = r;
     uint4 y[kVectors];
     if (next >= 0) {
-      if (firsts[r.tensor] <= next) rn.at -= (long long)gridDim.x * kChunkVectors;
-      else rn = place_of(l, firsts, next, 0, r.tensor - 1);
-      if (l.t[rn.tensor].vector) load_vectors(rn, y);
+      rn = place_in(l, next, firsts[r.tensor] <= next ? r.tensor : tensor_of(firsts, next, 0, r.tensor - 1));
+      if (l.t[rn.tensor].vector) load_vectors(l, rn, y);
     }
     const GradTensor& t = l.t[r.tensor];
     const bool in_f32 = t.in_f32, out_f32 = t.out_f32;
     if (t.vector) {
-      uint8_t* out = static_cast<uint8_t*>(t.out) + t.head * (out_f32 ? 4 : 2);
+      const int per = in_f32 ? 4 : 8;
+      uint8_t* out = static_cast<uint8_t*>(t.out) + (t.head + r.at * per) * (out_f32 ? 4 : 2);
 #pragma unroll
-      for (int u = 0; u < kVectors; ++u)
-        if (r.at + u * kThreads < r.vectors) {
-          if (in_f32) store_scaled<true>(out, r.at + u * kThreads, x[u], first, c, out_f32);
-          else store_scaled<false>(out, r.at + u * kThreads, x[u], first, c, out_f32);
-        }
+      for (int u = 0; u < kVectors; ++u) {
+        if (in_f32) store_scaled<true>(out, u * kThreads, u * kThreads < r.left, x[u], first, c, out_f32);
+        else store_scaled<false>(out, u * kThreads, u * kThreads < r.left, x[u], first, c, out_f32);
+      }
     } else {
       // out does not lie as in does: value by value, neighbours by neighbouring threads
       const int per = in_f32 ? 4 : 8;
       const long long begin = t.head + (r.at - threadIdx.x) * per;
-      const long long end = min(begin + (long long)kChunkVectors * per, t.head + r.vectors * per);
+      const long long end = min(begin + (long long)kChunkVectors * per, t.head + vectors_of(t) * per);
       for (long long j = begin + threadIdx.x; j < end; j += kThreads)
         store1(t.out, out_f32, j, load1(t.in, in_f32, j) * first * c);
     }
     if (chunk == t.first)
-      for_ends(t, r.vectors, [&](long long j) { store1(t.out, out_f32, j, load1(t.in, in_f32, j) * first * c); });
+      for_ends(t, [&](long long j) { store1(t.out, out_f32, j, load1(t.in, in_f32, j) * first * c); });
     if (next < 0) break;
     chunk = next;
     r = rn;

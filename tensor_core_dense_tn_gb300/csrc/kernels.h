@@ -232,6 +232,7 @@ struct ExpertsParams {
   int row_bytes;       // rows' operand in a k-block of a CTA
   int stages, acc_cols;                    // ring stages, columns of one accumulator
   int row_blocks, col_blocks;              // weights: tiles of a matrix; else col_blocks alone
+  int row_block;       // weights: rows of a tile but the last of a matrix
   int strip;           // row blocks per strip of the tile order
   FastDiv by_cols, by_tiles, by_strip, by_strip_tiles;   // launch: col_blocks, tiles of a matrix, strip, strip * col_blocks
   uint64_t timeout_ns;
