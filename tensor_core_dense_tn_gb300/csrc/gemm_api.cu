@@ -17,6 +17,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <string>
@@ -1238,7 +1239,6 @@ int run_grad_norm(int num, const gemm_tensor* tensors, bool clip, float max_norm
   if (!aligned_to(workspace, 8)) return fail(GEMM_ERR_MISALIGNED, "workspace must be 8-byte aligned");
   static thread_local std::vector<GradTensor> list;
   list.clear();
-  list.reserve(num);
   for (int i = 0; i < num; ++i) {
     const gemm_tensor& t = tensors[i];
     const gemm_tensor& o = out ? out[i] : t;
@@ -1432,15 +1432,25 @@ int gemm_bf16_tn_experts_backward_w(const gemm_expert_plan* plan, int64_t N, int
                           alpha, beta, out_dtype, GEMM_ACT_NONE, stream);
 }
 
+// (The lists grow with num: what the allocator throws ends here.)
+static int grad_norm_call(int num, const gemm_tensor* tensors, bool clip, float max_norm, const gemm_tensor* out,
+                          float* norm, void* workspace, void* stream) {
+  try {
+    return gtn::run_grad_norm(num, tensors, clip, max_norm, out, norm, workspace, stream);
+  } catch (const std::exception&) {
+    return GEMM_ERR_OUT_OF_MEMORY;
+  }
+}
+
 int64_t gemm_grad_workspace(int num) { return num < 0 ? 0 : 8 * gtn::grad_partials(num > 0 ? num : 1); }
 
 int gemm_grad_norm(int num, const gemm_tensor* tensors, float* norm, void* workspace, void* stream) {
-  return gtn::run_grad_norm(num, tensors, false, 0.0f, nullptr, norm, workspace, stream);
+  return grad_norm_call(num, tensors, false, 0.0f, nullptr, norm, workspace, stream);
 }
 
 int gemm_clip_grad_norm(int num, const gemm_tensor* tensors, float max_norm, const gemm_tensor* out, float* norm,
                         void* workspace, void* stream) {
-  return gtn::run_grad_norm(num, tensors, true, max_norm, out, norm, workspace, stream);
+  return grad_norm_call(num, tensors, true, max_norm, out, norm, workspace, stream);
 }
 
 int gemm_plan(int64_t M, int64_t N, int64_t K, int fp8_inputs, int num_sms, const gemm_tn_config* cfg,

@@ -35,11 +35,26 @@
 //   warp of its own.  Only such blocks take that way: when all blocks did, it
 //   doubled the kernel's time.
 //
-// Structure (one CTA per SM): warp 0 loads, warp 1 multiplies, warps 2..9
-// store, warp 10 (weights only) zeroes.  CG = 2 pairs two CTAs on a tile of
-// 256 columns x up to 256 rows, CG = 1 takes 128 columns.  Accumulators are
-// double buffered in Tensor Memory, so that a tile's epilogue runs beside the
-// next one's loop.
+// Structure (one CTA per SM): warp 0 loads, warp 1 multiplies, the next 8 (weights:
+// 16) store, the last (weights only) zeroes.  CG = 2 pairs two CTAs on a tile of
+// 256 columns x up to 256 rows, CG = 1 takes 128 columns.  Accumulators are double
+// buffered in Tensor Memory, so that a tile's epilogue runs beside the next
+// one's loop; half of the storing warps belong to each.  GROUPS: stages of two
+// or four k-blocks in one box, for products of few rows.
+//
+// What bounds it and what it measured (graph-replayed, bf16 results unless said;
+// floor: bytes at 6793 GB/s or operations at 1895 TFLOP/s):
+//   weights' bytes   16 tokens, 2 of 8 experts of 4096 x 4096     43.5 us, floor 39.2
+//                    16 rows for each of 64 of 4096 x 2048       160, floor 160
+//   operations       8192 tokens, 8 of 128 of 4096 x 2048, silu  684-713, floor 580
+//                    rows, 16384 rows, 8 of 8192 x 4096          599-629, floor 569
+//                    weights, the same                           587-608, floor 569
+//   both             9003 rows, 61 of 5000 x 2000, fp32          233, floor 211
+//   output's bytes   weights, 64 of 2048 x 2048 fp32 with C      389, floor 336
+//                    weights, 61 of 1000 x 2000, 3 rows each      52, floor 36
+// (The ranges are of one program at different times: at 1400 W the clock moves.)
+// In the second group the tensor pipe is active 89-91% of the time with about 1000
+// rows an expert, and 72-74% in `weights`, whose tiles are 16 k-blocks then.
 //
 // Every mbarrier wait is bounded by %globaltimer; one that gives up sets a
 // CTA abort flag and the device status word, and all roles leave.

@@ -10,9 +10,10 @@
 //   of 960 for longer ones), no table is copied to the GPU, and one launch
 //   takes all of them: work is cut into chunks of 32 KB, and a block takes every
 //   G-th chunk of the whole list, with the next one's loads in flight.
-// - The clip's second pass runs through the chunks backwards: what the first
-//   pass read last is still in L2 (about 100 MB of it).  Its stores are
-//   streaming, so that they do not push it out.
+// - The clip's second pass runs through the chunks backwards: some 60 MB that
+//   the first pass read last are still in L2 (132 MB of fp32 values into bf16: 48
+//   us, forwards 57; 400 MB 151, 158).  Its stores are streaming, so that they do
+//   not push them out.
 // - Sums.  A thread adds 32 squares (16 of fp32 values) in fp32, in four chains
 //   (an error of at most 11 steps of 2^-24), and these sums in fp64: one fp64 addition per 32
 //   values is within what the SMs can do at the memory's rate, one per value
@@ -21,6 +22,15 @@
 //   right over the whole range of values, and infinite or NaN only if a value is.
 // - No atomics: a block's sum goes to its place in the workspace, and each
 //   block that needs the total adds all places in the same order.
+//
+// Measured (graph-replayed): 1.07 GB of bf16 values 161 us, 0.98 of the copy
+// bandwidth; 1.07 GB of fp32 values clipped into bf16 400 us for 2.68 GB, 0.99 of it;
+// 16 small tensors of 4 MB 5.5 us, 40 of 6 MB clipped 9.2 us, each two launches
+// that wait for one another.  In fp64, of which an SM does two operations a cycle, every
+// step that all threads took together showed: a tree over 512 threads 2.5 us,
+// a root and a quotient in each of them 4.5, squares of the zeros behind a
+// tensor's end 3.6.
+
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -239,15 +239,19 @@ struct ExpertsParams {
   int* status;
 };
 
-// Chooses the tile shape (cg, tile_rows and what follows from them) from op, R and E.
+// Chooses the tile shape (cg, tile_rows, col_tile, group and what follows from
+// them) from op, R, E, S, cols_out and has_c.
 void experts_geometry(ExpertsParams* p, int sms);
-// The operands' tensor maps (128-byte swizzle):
-// cols  the operand of the output's columns: forward, W in boxes of 64 x 128;
-//       (of 64 x col_tile); rows, W, and weights, A, in boxes of 64 columns x 64 rows, with
-//       wide_cols as {64, row, chunk of 64 columns (, expert)} and two chunks
-// rows  that of its rows: 64 x row_box; weights, dD as `cols`, with wide_rows
-//       tile_rows / cg / 64 chunks
-// part  weights: the same with 16 rows; else rows in boxes of 1/4, 1/2 and 3/4 of the height (row_box of 64 and more)
+// The operands' tensor maps (128-byte swizzle), by op:
+//             cols: the output's columns           rows: its rows
+//   forward   W {k, row, expert}, 64 x col_tile    A {k, row}, 64 x row_box
+//   rows      W, MN-major                          dD {k, row}, 64 x row_box
+//   weights   A, MN-major                          dD, MN-major
+// MN-major: {column, row (, expert)} in boxes of 64 x 64; with wide_cols or
+// wide_rows {64, row, chunk of 64 columns (, expert)} in boxes of all of a CTA's
+// chunks.  Forward with groups: {64, row, k-block (, expert)} in boxes of `group`
+// k-blocks.  _part: weights, boxes of 16 rows instead of 64; else rows_part[i],
+// i + 1 quarters of row_box (where that is at least 64).
 struct ExpertsMaps {
   CUtensorMap cols, rows, cols_part, rows_part[3];
 };
