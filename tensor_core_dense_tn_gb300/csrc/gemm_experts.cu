@@ -35,12 +35,13 @@
 //   warp of its own.  Only such blocks take that way: when all blocks did, it
 //   doubled the kernel's time.
 //
-// Structure (one CTA per SM): warp 0 loads, warp 1 multiplies, the next 8 (weights:
-// 16) store, the last (weights only) zeroes.  CG = 2 pairs two CTAs on a tile of
+// Structure (one CTA per SM): warp 0 loads, warp 1 multiplies, the next 8 (weights
+// and LONG: 16) store, the last (weights only) zeroes.  CG = 2 pairs two CTAs on a tile of
 // 256 columns x up to 256 rows, CG = 1 takes 128 columns.  Accumulators are double
 // buffered in Tensor Memory, so that a tile's epilogue runs beside the next
 // one's loop; half of the storing warps belong to each.  GROUPS: stages of two
-// or four k-blocks in one box, for products of few rows.
+// or four k-blocks in one box, for products of few rows.  LONG: fp32 results of
+// long sums, added up in segments.
 //
 // What bounds it and what it measured (graph-replayed, bf16 results unless said;
 // floor: bytes at 6793 GB/s or operations at 1895 TFLOP/s):
@@ -49,7 +50,7 @@
 //   operations       8192 tokens, 8 of 128 of 4096 x 2048, silu  684-713, floor 580
 //                    rows, 16384 rows, 8 of 8192 x 4096          599-629, floor 569
 //                    weights, the same                           587-608, floor 569
-//   both             9003 rows, 61 of 5000 x 2000, fp32          233, floor 211
+//   both             9003 rows, 61 of 5000 x 2000, fp32          258, floor 211
 //   output's bytes   weights, 64 of 2048 x 2048 fp32 with C      389, floor 336
 //                    weights, 61 of 1000 x 2000, 3 rows each      52, floor 36
 // (The ranges are of one program at different times: at 1400 W the clock moves.)
@@ -78,7 +79,19 @@ constexpr int kColBytes = 128 * 128;       // a stage of the columns' operand: 1
 constexpr int kErrTimeout = -5;            // GEMM_ERR_TIMEOUT
 constexpr int kMaxStages = 16;
 
-template <int OP>
+// Terms that the tensor core adds up by itself for an fp32 result of a long sum
+// (LONG).  Its accumulator cuts bits off at every MMA instead of rounding, so
+// the error grows with the number of terms: 1.0e-6 of the result's norm at 1024,
+// 2.1e-6 at 2000, about 8e-6 at 8192.  In LONG the two accumulators take segments
+// in turn and the storing warps add them, rounded, in registers.  Segments of 8,
+// 12 and 16 blocks leave 4.7e-7, 7.2e-7 and 1.0e-6 at every length; 9003 rows of
+// 61 experts of 5000 x 2000 take 270, 258 and 247 us with them, and 233 without any:
+// a segment's end costs the MMAs a wait for the warps that read the one
+// before.  bf16 results (an error of 1e-3) are added up by the tensor core alone.
+constexpr int kSegmentBlocks = 12;         // k-blocks of a segment
+static_assert(kSegmentBlocks % 4 == 0, "a whole number of stages of four k-blocks");
+
+template <int OP, bool LONG>
 struct Shape {
   static constexpr bool kWeights = OP == kExpertsWeights;
   static constexpr bool kMnCols = OP != kExpertsForward, kMnRows = kWeights;   // operands that are MN-major
@@ -86,8 +99,10 @@ struct Shape {
   // takes at a time.  With more of them more of C is on its way (64 matrices of
   // 2048 x 2048 fp32 with C: 16 warps 404 us, 8 424); a product's long sums hide
   // the stores of 8 (one prompt through 128 experts: 818 us, with 16 840).
-  static constexpr int kEpiWarps = kWeights ? 16 : 8;
-  static constexpr int kRowsAtOnce = kWeights ? 16 : 32;
+  // LONG: all of them take every segment, 64 rows each, whose fp32 sums fill
+  // most of a thread's 96 registers (24 to 132 bytes of them spill).
+  static constexpr int kEpiWarps = kWeights || LONG ? 16 : 8;
+  static constexpr int kRowsAtOnce = kWeights || LONG ? 16 : 32;
   static constexpr int kThreads = 32 * (2 + kEpiWarps + (kWeights ? 1 : 0));
 };
 
@@ -442,10 +457,10 @@ __device__ __forceinline__ void add_c(const uint32_t (&x)[NR], float beta, bool 
   }
 }
 
-template <int CG, int OP, bool GROUPS>
-__global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
+template <int CG, int OP, bool GROUPS, bool LONG>
+__global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
     gemm_experts_kernel(const __grid_constant__ ExpertsMaps maps, const __grid_constant__ ExpertsParams p) {
-  using S_ = Shape<OP>;
+  using S_ = Shape<OP, LONG>;
   constexpr int kEpiWarps = S_::kEpiWarps, kRowsAtOnce = S_::kRowsAtOnce;
   constexpr bool kPair = CG == 2;
   extern __shared__ uint8_t smem_raw[];
@@ -484,7 +499,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
-      mbar_init(acce_bar(b), kEpiWarps / 2 * CG);
+      mbar_init(acce_bar(b), (LONG ? kEpiWarps : kEpiWarps / 2) * CG);
     }
     mbar_init(drain_bar, 1);
     *abort_flag = 0;
@@ -647,35 +662,52 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
         const uint32_t idesc =
             instr_desc_bf16_f32(128 * CG, n) | (S_::kMnCols ? 1u << 15 : 0u) | (S_::kMnRows ? 1u << 16 : 0u);
         if (!wait_all(acce_bar(acc), acc_phase ^ 1)) break;
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * p.acc_cols);
+        auto d_tmem = [&] { return tmem_base + (uint32_t)(acc * p.acc_cols); };
         // Whole blocks; the last, shorter one apart: with the two in one loop,
         // and so its steps and strides in registers, the MMAs came with pauses
         // (2048 rows for each of 8 matrices of 8192 x 4096: 747 us, apart 625).
         const int blocks = (sum + kBlockK * group - 1) / (kBlockK * group), whole = S_::kWeights ? sum / kBlockK : blocks;
-        for (int kb = 0; kb < whole; ++kb) {
-          if (kb > 0) ok = wait_all(full_bar(stage), phase);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t c = sC + stage * group * kColBytes, b = sR + stage * group * p.row_bytes;
-          const uint64_t c0 = S_::kMnCols ? desc_mn(c, kChunkBytes) : smem_desc_sw128(c);
-          const uint64_t b0 = S_::kMnRows ? desc_mn(b, kChunkBytes) : smem_desc_sw128(b);
-          // 16 summation indices are 32 bytes of a K-major operand's rows, 16 rows of each chunk of an MN-major one
-          constexpr uint64_t kStepC = S_::kMnCols ? kPartBytes / 16 : 2, kStepR = S_::kMnRows ? kPartBytes / 16 : 2;
-          if (elect_one()) {
-            if constexpr (GROUPS) {
-              for (int j = 0; j < group; ++j)
+        // blocks of one segment into the current accumulator
+        auto multiply = [&](int kb0, int kb1) {
+          const uint32_t d = d_tmem();
+          for (int kb = kb0; kb < kb1; ++kb) {
+            if (kb > 0) ok = wait_all(full_bar(stage), phase);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t c = sC + stage * group * kColBytes, b = sR + stage * group * p.row_bytes;
+            const uint64_t c0 = S_::kMnCols ? desc_mn(c, kChunkBytes) : smem_desc_sw128(c);
+            const uint64_t b0 = S_::kMnRows ? desc_mn(b, kChunkBytes) : smem_desc_sw128(b);
+            // 16 summation indices are 32 bytes of a K-major operand's rows, 16 rows of each chunk of an MN-major one
+            constexpr uint64_t kStepC = S_::kMnCols ? kPartBytes / 16 : 2, kStepR = S_::kMnRows ? kPartBytes / 16 : 2;
+            if (elect_one()) {
+              if constexpr (GROUPS) {
+                for (int j = 0; j < group; ++j)
+#pragma unroll
+                  for (int i = 0; i < kBlockK / 16; ++i)
+                    mma_issue<CG, kKindF16>(d, c0 + (uint64_t)(j * p.col_tile * 8 + 2 * i), b0 + (uint64_t)(j * box * 8 + 2 * i),
+                                            idesc, (kb != kb0 || j != 0 || i != 0) ? 1u : 0u);
+              } else {
 #pragma unroll
                 for (int i = 0; i < kBlockK / 16; ++i)
-                  mma_issue<CG, kKindF16>(d_tmem, c0 + (uint64_t)(j * p.col_tile * 8 + 2 * i), b0 + (uint64_t)(j * box * 8 + 2 * i),
-                                          idesc, (kb != 0 || j != 0 || i != 0) ? 1u : 0u);
-            } else {
-#pragma unroll
-              for (int i = 0; i < kBlockK / 16; ++i)
-                mma_issue<CG, kKindF16>(d_tmem, c0 + kStepC * i, b0 + kStepR * i, idesc, (kb != 0 || i != 0) ? 1u : 0u);
+                  mma_issue<CG, kKindF16>(d, c0 + kStepC * i, b0 + kStepR * i, idesc, (kb != kb0 || i != 0) ? 1u : 0u);
+              }
+              commit(empty_bar(stage));
             }
-            commit(empty_bar(stage));
+            advance();
           }
-          advance();
+        };
+        if constexpr (LONG) {
+          const int segment = kSegmentBlocks / group;
+          for (int kb = 0; kb < whole && ok; kb += segment) {
+            if (kb > 0) {
+              hand_over();
+              ok = wait_all(acce_bar(acc), acc_phase ^ 1);
+              if (!ok) break;
+            }
+            multiply(kb, min(whole, kb + segment));
+          }
+        } else {
+          multiply(0, whole);
         }
         if (S_::kWeights && ok && whole < blocks) {
           if (whole > 0) ok = wait_all(full_bar(stage), phase);
@@ -689,7 +721,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
           const int parts = (sum - whole * kBlockK + 15) / 16;
           if (elect_one()) {
             for (int i = 0; i < parts; ++i)
-              mma_issue<CG, kKindF16>(d_tmem, desc_mn(sC + stage * kColBytes + i * (kColBytes / 4), kPartBytes),
+              mma_issue<CG, kKindF16>(d_tmem(), desc_mn(sC + stage * kColBytes + i * (kColBytes / 4), kPartBytes),
                                       desc_mn(sR + stage * p.row_bytes + i * (p.row_bytes / 4), kPartBytes), idesc,
                                       (whole != 0 || i != 0) ? 1u : 0u);
             commit(empty_bar(stage));
@@ -711,14 +743,24 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
     // Half of the warps take the tiles of one accumulator, half those of the other:
     // while some store, the others wait for sums, read and convert.
-    const int acc = (warp - 2) / (kEpiWarps / 2), c_first = (warp - 2) / 4 % (kEpiWarps / 8) * kRowsAtOnce;
+    [[maybe_unused]] int done = 0;            // LONG: segments taken
+    const int acc = LONG ? 0 : (warp - 2) / (kEpiWarps / 2), c_first = (warp - 2) / 4 % (kEpiWarps / 8) * kRowsAtOnce;
     constexpr int kRowStep = kEpiWarps / 8 * kRowsAtOnce;
     Abort ab{abort_flag, p.timeout_ns, p.status, kRoleEpilogue};
     const bool f32 = p.out_f32, pairs = p.pairs;
     const int esize = f32 ? 4 : 2;
     uint32_t acc_phase = 0;
     const uint32_t acce_target = kPair ? mapa_shared(acce_bar(acc), 0) : acce_bar(acc);
-    for (int t = first_tile + acc * step; t < num_tiles; t += 2 * step) {
+    // accumulator read: it goes back to the MMA warp
+    auto hand_back = [&](int a) {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kPair) mbar_arrive_cluster(acce_target + 8u * (a - acc));
+        else mbar_arrive(acce_bar(a));
+      }
+    };
+    for (int t = first_tile + acc * step; t < num_tiles; t += (LONG ? 1 : 2) * step) {
       const Tile r = tile_of<CG, OP, GROUPS>(t, p, tb);
       const int col = r.col0 + (int)rank * p.col_tile + q * 32 + lane;
       const bool mine = q * 32 + lane < p.col_tile && col < p.cols_out;
@@ -726,6 +768,60 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
         return const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) +
                ((OP == kExpertsWeights ? (long long)r.e * stride : 0) + (long long)row * ld + col) * esize;
       };
+      if constexpr (LONG) {
+        // this warp's 64 rows of every segment, added up in fp32 registers
+        const int part = (warp - 2) / 4 * 64;
+        float sum[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) sum[j] = 0.0f;
+        if (S_::kWeights && p.has_c && r.col0 + (int)rank * p.col_tile + q * 32 < p.cols_out)
+          // C, which no registers are left for, on its way to L2: 128 bytes of rows lane and lane + 32
+          // (32 matrices of 2048 x 2048 with C, 1000 rows each: 342 us without, 298 with)
+#pragma unroll
+          for (int j = 0; j < 64; j += 32)
+            if (part + lane + j < r.rows)
+              prefetch_l2(static_cast<const uint8_t*>(element(p.C, p.ldc, p.stride_c, r.row0 + part + lane + j)) - lane * esize);
+        const int whole = S_::kWeights ? (r.k_end - r.k0) / kBlockK : r.num_kb;
+        const int segments = max(1, (whole * group + kSegmentBlocks - 1) / kSegmentBlocks);
+        bool ok = true;
+        for (int i = 0; i < segments && ok; ++i, ++done) {
+          const int a = done & 1;
+          ok = __all_sync(0xffffffffu, wait_bar<kPair>(accf_bar(a), (uint32_t)(done >> 1) & 1u, ab)) != 0;
+          if (!ok) break;
+          tc_fence_after();
+          if (r.num_kb > 0) {
+#pragma unroll
+            for (int j = 0; j < 64; j += 16)
+              if (part + j < r.rows) {
+                uint32_t x[16];
+                tmem_ld_rows(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * p.acc_cols + part + j), x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) sum[j + k] += __uint_as_float(x[k]);
+              }
+          }
+          hand_back(a);
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 64; j += 8)
+          if (part + j < r.rows) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = p.alpha * sum[j + k];
+            if constexpr (OP == kExpertsForward) activate_rows(v, p.act, true);
+            if constexpr (OP == kExpertsWeights)
+              if (p.has_c) {
+                uint32_t xc[8];
+                load_c(element(p.C, p.ldc, p.stride_c, r.row0 + part + j), p.ldc, r.rows - part - j, mine, true, false, xc);
+                add_c(xc, p.beta, true, false, v);
+              }
+            store_rows_f32(reinterpret_cast<float*>(element(p.D, p.ldd, p.stride_d, r.row0 + part + j)), p.ldd,
+                           r.rows - part - j, mine, v);
+          }
+        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+        continue;
+      }
       [[maybe_unused]] uint32_t xc[kRowsAtOnce];
       if constexpr (OP == kExpertsWeights)
         if (p.has_c)
@@ -764,13 +860,7 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
         if (f32) store_rows_f32(reinterpret_cast<float*>(to), p.ldd, r.rows - c, mine, v);
         else store_rows_bf16(reinterpret_cast<uint16_t*>(to), p.ldd, r.rows - c, mine, pairs, v);
       }
-      // accumulator read: hand it back to the MMA warp
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kPair) mbar_arrive_cluster(acce_target);
-        else mbar_arrive(acce_bar(acc));
-      }
+      hand_back(acc);
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       acc_phase ^= 1;
     }
@@ -813,23 +903,31 @@ __global__ void __launch_bounds__(Shape<OP>::kThreads, 1)
   }
 }
 
-// 0: products on single k-blocks, 1: on groups, 2: rows, 3: weights on single CTAs, 4: on pairs
-constexpr int kKernels = 5;
+// 0: products on single k-blocks, 1: on groups, 2: rows, 3: weights on single
+// CTAs, 4: on pairs; from 5 on the same with long sums in fp32 (none of 3)
+constexpr int kKernels = 10;
 
 int kernel_index(const ExpertsParams& p) {
-  return p.op == kExpertsForward ? (p.group > 1 ? 1 : 0) : p.op == kExpertsRows ? 2 : p.cg + 2;
+  return (p.op == kExpertsForward ? (p.group > 1 ? 1 : 0) : p.op == kExpertsRows ? 2 : p.cg + 2) + (p.long_sum ? 5 : 0);
 }
 
+template <bool LONG>
 const void* kernel_of(int index) {
-  static const void* const table[kKernels] = {
-      (const void*)gemm_experts_kernel<2, kExpertsForward, false>, (const void*)gemm_experts_kernel<2, kExpertsForward, true>,
-      (const void*)gemm_experts_kernel<2, kExpertsRows, false>, (const void*)gemm_experts_kernel<1, kExpertsWeights, false>,
-      (const void*)gemm_experts_kernel<2, kExpertsWeights, false>};
+  static const void* const table[5] = {
+      (const void*)gemm_experts_kernel<2, kExpertsForward, false, LONG>,
+      (const void*)gemm_experts_kernel<2, kExpertsForward, true, LONG>,
+      (const void*)gemm_experts_kernel<2, kExpertsRows, false, LONG>,
+      LONG ? nullptr : (const void*)gemm_experts_kernel<1, kExpertsWeights, false, false>,
+      (const void*)gemm_experts_kernel<2, kExpertsWeights, false, LONG>};
   return table[index];
 }
 
+const void* kernel_at(int index) { return index < 5 ? kernel_of<false>(index) : kernel_of<true>(index - 5); }
+
 int threads_of(int index) {
-  return index >= 3 ? Shape<kExpertsWeights>::kThreads : Shape<kExpertsForward>::kThreads;
+  return index >= 5   ? (index == 9 ? Shape<kExpertsWeights, true>::kThreads : Shape<kExpertsForward, true>::kThreads)
+         : index >= 3 ? Shape<kExpertsWeights, false>::kThreads
+                      : Shape<kExpertsForward, false>::kThreads;
 }
 
 constexpr int kSmemMax = 232448;
@@ -848,7 +946,11 @@ void experts_geometry(ExpertsParams* p, int sms) {
   // where the output's memory decides: single CTAs, which need not wait for each
   // other (64 matrices of 2048 x 2048, single / pairs: 128 rows each, bf16, 130 /
   // 142 us; 256 rows 174 / 171; fp32 with C, 512 rows 444 / 454, 1024 rows 582 / 555).
-  p->cg = weights && average < (p->has_c ? 768 : 192) ? 1 : 2;
+  // (LONG by the average: the sums' lengths are known on the device only, and
+  // with it for every call 256 rows each with C take 539 instead of 392 us, as C
+  // is then read behind the sum.)
+  p->long_sum = p->out_f32 && (weights ? average : p->S) > kSegmentBlocks * kBlockK;
+  p->cg = weights && !p->long_sum && average < (p->has_c ? 768 : 192) ? 1 : 2;
   const int step = 16 * p->cg;
   const int most = 2 * average < 32 ? 32 : 2 * average;
   p->tile_rows = weights || most > 256 ? 256 : (most + 31) / 32 * 32;
@@ -916,12 +1018,13 @@ cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cu
   cfg.attrs = attr;
   if (!configured[dev]) {
     for (int i = 0; i < kKernels; ++i) {
-      if ((e = cudaFuncSetAttribute(kernel_of(i), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax))) return e;
+      if (!kernel_at(i)) continue;
+      if ((e = cudaFuncSetAttribute(kernel_at(i), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax))) return e;
       cfg.gridDim = dim3(2);
       cfg.blockDim = dim3(threads_of(i));
       cfg.dynamicSmemBytes = kSmemMax;
       cfg.numAttrs = 1;
-      if (i != 3 && (e = cudaOccupancyMaxActiveClusters(&pairs[dev][i], kernel_of(i), &cfg))) return e;
+      if (i != 3 && (e = cudaOccupancyMaxActiveClusters(&pairs[dev][i], kernel_at(i), &cfg))) return e;
     }
     configured[dev] = true;
   }
@@ -949,16 +1052,19 @@ cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cu
   info->smem_bytes = cfg.dynamicSmemBytes;
   info->k_parts = 1;
   info->scheduler = 1;
-  static const char* const names[kKernels] = {"gemm_experts_kernel<forward>", "gemm_experts_kernel<forward, groups>",
-                                              "gemm_experts_kernel<rows>", "gemm_experts_kernel<weights, 1>",
-                                              "gemm_experts_kernel<weights, 2>"};
+  static const char* const names[kKernels] = {
+      "gemm_experts_kernel<forward>",         "gemm_experts_kernel<forward, groups>",
+      "gemm_experts_kernel<rows>",            "gemm_experts_kernel<weights, 1>",
+      "gemm_experts_kernel<weights, 2>",      "gemm_experts_kernel<forward, long>",
+      "gemm_experts_kernel<forward, groups, long>", "gemm_experts_kernel<rows, long>",
+      nullptr,                                "gemm_experts_kernel<weights, 2, long>"};
   info->kernel = names[index];
   p.by_cols = fast_div(p.col_blocks);
   p.by_tiles = fast_div(p.row_blocks * p.col_blocks);
   p.by_strip = fast_div(p.strip);
   p.by_strip_tiles = fast_div(p.strip * p.col_blocks);
   void* args[2] = {const_cast<ExpertsMaps*>(&maps), &p};
-  return cudaLaunchKernelExC(&cfg, kernel_of(index), args);
+  return cudaLaunchKernelExC(&cfg, kernel_at(index), args);
 }
 
 }  // namespace gtn

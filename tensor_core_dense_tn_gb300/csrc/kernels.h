@@ -223,6 +223,7 @@ struct ExpertsParams {
   const void* C; long long ldc, stride_c;  // weights: read where has_c
   int has_c, out_f32, act;
   int pairs;           // bf16 D and C: even pitches and row lengths on 4 bytes, moved two columns at a time
+  int long_sum;        // fp32 results of long sums: segments are added outside the tensor core
   float alpha, beta;
   int cg, tile_rows;   // CTAs per tile, most rows per tile
   int col_tile;        // columns per CTA of a tile, at most 128 (forward: any multiple of 16; else 128)
@@ -240,7 +241,7 @@ struct ExpertsParams {
 };
 
 // Chooses the tile shape (cg, tile_rows, col_tile, group and what follows from
-// them) from op, R, E, S, cols_out and has_c.
+// them) from op, R, E, S, cols_out, has_c and out_f32.
 void experts_geometry(ExpertsParams* p, int sms);
 // The operands' tensor maps (128-byte swizzle), by op:
 //             cols: the output's columns           rows: its rows

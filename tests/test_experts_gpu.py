@@ -381,3 +381,60 @@ def test_places_beyond_2_31(what):
         want = dD[lo:hi, cols].double().T @ A[lo:hi].double()
         assert torch.equal(dW[e, cols], want.to(F32).to(BF16))
     assert torch.all(dW[1] == 0)
+
+
+SEGMENT = 768      # terms that an fp32 result's sum takes between two rounded additions
+
+
+@pytest.mark.parametrize("terms", [769, 832, 1536, 1537, 2304, 2305, 4096, 5000])
+@pytest.mark.parametrize("counts", [[5, 0, 40], [300, 1, 128, 0, 257]])
+def test_long_sums_of_products_in_fp32(terms, counts):
+    """Whole numbers come out exactly at lengths around whole segments, few rows and many."""
+    plan, N = plan_of(counts, 3), 200
+    A, W = values((sum(counts) + 3, terms), 41, True), values((len(counts), N, terms), 42, True)
+    buf, D = canvas((A.shape[0], N), F32, 5)
+    g.gemm_experts(A, W, plan, out=D)
+    check(D, forward64(A, W, plan)[0], None, terms, True)
+    assert torch.all(buf[:, N:] == 7)
+    dD, W = values((sum(counts) + 3, terms), 43, True), values((len(counts), terms, N), 44, True)
+    dA = g.gemm_experts_backward_a(dD, W, plan, out_dtype=F32)
+    check(dA, forward64(dD, W.transpose(1, 2), plan)[0], None, terms, True)
+    status()
+
+
+@pytest.mark.parametrize("counts", [[0, 1, 767, 768, 769, 1536, 1537, 2305, 5000], [9000, 0, 16], [3001, 2999]])
+@pytest.mark.parametrize("with_c", [True, False])
+def test_long_sums_of_weights_in_fp32(counts, with_c):
+    """Experts of few rows and of many in one call, in place and with pitches of no alignment."""
+    plan, N, K = plan_of(counts, 2), 300, 270
+    dD, A = values((sum(counts) + 2, N), 45, True), values((sum(counts) + 2, K), 46, True)
+    buf, dW = canvas((len(counts), N, K), F32, 3)
+    C = torch.randint(-99, 100, dW.shape, generator=gen(47), device="cuda").float()
+    dW.copy_(C)
+    g.gemm_experts_backward_w(dD, A, plan, out=dW, beta=1.0 if with_c else 0.0, C=dW if with_c else None)
+    check(dW, weights64(dD, A, plan)[0] + (C.double() if with_c else 0), None, 0, True)
+    assert torch.all(buf[..., K:] == 7)
+    status()
+
+
+def test_fp32_results_keep_their_bits_over_long_sums():
+    """Terms of one sign, where what the tensor core cuts off adds up.  Within a segment of 48 MMAs each one loses
+    less than two units of 2^-23 of the sum (its terms' alignment, its result); the segments are added rounded."""
+    terms, rows, N = 32768, 40, 136
+    bound = (2 * SEGMENT // 16 + -(-terms // SEGMENT) + 2) * 2.0 ** -23
+
+    def positive(shape, seed):
+        return (torch.rand(shape, generator=gen(seed), device="cuda") / 2 + 0.5).to(BF16)
+
+    def near(got, ref):
+        assert torch.all((got.double() - ref).abs() <= bound * ref)
+
+    plan = plan_of([rows], 0)
+    A, W = positive((rows, terms), 51), positive((1, N, terms), 52)
+    near(g.gemm_experts(A, W, plan, out_dtype=F32), forward64(A, W, plan)[0])
+    Wt = W.transpose(1, 2).contiguous()
+    near(g.gemm_experts_backward_a(A, Wt, plan, out_dtype=F32), forward64(A, W, plan)[0])
+    plan = plan_of([terms], 0)
+    dD, A = positive((terms, N), 53), positive((terms, rows), 54)
+    near(g.gemm_experts_backward_w(dD, A, plan, out_dtype=F32), weights64(dD, A, plan)[0])
+    status()
