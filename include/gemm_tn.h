@@ -669,7 +669,8 @@ int gemm_bf16_tn_experts_backward_w(const gemm_expert_plan *plan, int64_t N, int
  * or overlaps no tensor (GEMM_ERR_INVALID_VALUE otherwise; so a clip takes no
  * tensor twice).  norm: one fp32 in device memory.  workspace: device memory of
  * gemm_grad_workspace(num) bytes, 8-byte aligned, whose contents do not matter;
- * calls that may run at the same time need one each.  No other memory is used,
+ * calls that may run at the same time need one each.  Neither may overlap a
+ * tensor (GEMM_ERR_INVALID_VALUE).  No other memory is used,
  * so the calls may be captured and replayed on any stream. */
 typedef struct gemm_tensor {
   void *data;

@@ -717,7 +717,8 @@ def gemm_experts(A, W, plan: ExpertPlan, alpha: float = 1.0, activation: int = A
                  stream=None):
     """D[r] = act(alpha * A[r] @ W[e].T) for the rows r of expert e in `plan`: A (plan.rows, K) bf16 in expert order,
     W (experts, N, K) bf16; zeros in the rows past plan.offsets[experts].  Nothing waits for the row counts.  Without
-    an autograd graph: the gradients of the product without an activation are gemm_experts_backward_a() and _w()."""
+    an autograd graph: the gradients of the product without an activation are gemm_experts_backward_a() and _w().
+    Without `out` the result is the current stream's memory: a `stream` of the caller's waits for that one first."""
     return _experts_rows(False, A, W, plan, alpha, activation, out_dtype, out, stream)
 
 

@@ -1227,6 +1227,19 @@ bool clip_overlaps(const std::vector<GradTensor>& list) {
   return false;
 }
 
+// Whether memory that is written before the values are read for the last time
+// holds any of them, or of their outputs.
+bool holds_values(const void* p, int64_t bytes, const std::vector<GradTensor>& list) {
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+  const auto meets = [&](const void* data, int64_t size) {
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(data);
+    return begin < at + (uintptr_t)bytes && at < begin + (uintptr_t)size;
+  };
+  for (const GradTensor& t : list)
+    if (meets(t.in, t.count * (t.in_f32 ? 4 : 2)) || meets(t.out, t.count * (t.out_f32 ? 4 : 2))) return true;
+  return false;
+}
+
 // out: nullptr = in place.  Without `clip` only the norm.
 int run_grad_norm(int num, const gemm_tensor* tensors, bool clip, float max_norm, const gemm_tensor* out, float* norm,
                   void* workspace, void* stream_v) {
@@ -1264,6 +1277,8 @@ int run_grad_norm(int num, const gemm_tensor* tensors, bool clip, float max_norm
     list.push_back(g);
   }
   if (clip && clip_overlaps(list)) return fail(GEMM_ERR_INVALID_VALUE, "an output overlaps another tensor");
+  if (holds_values(norm, 4, list) || holds_values(workspace, gemm_grad_workspace(num), list))
+    return fail(GEMM_ERR_INVALID_VALUE, "norm or workspace overlaps a tensor");
   int dev = 0;
   DeviceState* st = nullptr;
   int rc = init_device(&dev, &st);

@@ -69,6 +69,22 @@ def test_outputs_that_overlap_are_refused(built, rows, out):
     assert "overlap" in g.last_error()
 
 
+@pytest.mark.parametrize("clip", [True, False])
+@pytest.mark.parametrize("norm,work", [
+    (0x10000, 0x2000), (0x1018C, 0x2000), (0x1000, 0x10000), (0x1000, 0x10188), (0x1000, 0x10000 - 8),
+])
+def test_a_norm_or_workspace_in_a_tensor_is_refused(built, clip, norm, work):
+    """It would be written before the values there are read, or are scaled."""
+    a = array((0x40000, 8, 0), (0x10000, 100, 1))
+    refused(g.gemm_clip_grad_norm(2, a, 1.0, None, norm, work, 0) if clip else g.gemm_grad_norm(2, a, norm, work, 0), INV)
+    assert "overlap" in g.last_error()
+
+
+def test_a_norm_in_an_output_is_refused(built):
+    refused(g.gemm_clip_grad_norm(1, array(GOOD), 1.0, array((0x30000, 100, 1)), 0x30010, 0x2000, 0), INV)
+    assert "overlap" in g.last_error()
+
+
 def test_neighbours_do_not_overlap(built):
     """Without a GPU the call gets as far as asking for the device."""
     rows = [(0x10000, 100, 1), (0x10000 + 400, 100, 0), (0x10000 + 600, 3, 0)]
