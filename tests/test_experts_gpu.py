@@ -438,3 +438,68 @@ def test_fp32_results_keep_their_bits_over_long_sums():
     dD, A = positive((terms, N), 53), positive((terms, rows), 54)
     near(g.gemm_experts_backward_w(dD, A, plan, out_dtype=F32), weights64(dD, A, plan)[0])
     status()
+
+
+@pytest.mark.parametrize("act", [g.ACT_RELU, g.ACT_GELU, g.ACT_GELU_TANH, g.ACT_SILU])
+def test_activation_of_long_sums_in_fp32(act):
+    plan, terms = plan_of([300, 0, 77], 9), 1000
+    A, W = values((plan.rows, terms), 61, False), values((3, 136, terms), 62, False) * terms ** -0.5
+    ref, mag = forward64(A, W, plan)
+    fn = {g.ACT_RELU: torch.relu, g.ACT_GELU: torch.nn.functional.gelu, g.ACT_SILU: torch.nn.functional.silu,
+          g.ACT_GELU_TANH: lambda t: torch.nn.functional.gelu(t, approximate="tanh")}[act]
+    got = g.gemm_experts(A, W, plan, alpha=2.0, activation=act, out_dtype=F32)
+    bound = 1.2 * (terms + 2) * 2.0 ** -23 * 2 * mag + 2.0 ** -20 * 2 * ref.abs() + EPS[F32] * 1.01 * fn(2 * ref).abs()
+    assert torch.all((got.double() - fn(2 * ref)).abs() <= bound)
+    assert torch.all(got[sum(plan.offsets.diff().tolist()):] == 0)
+    status()
+
+
+def test_what_is_not_finite_stays_in_its_expert_over_long_sums():
+    plan, N, K = plan_of([1601, 770, 903], 0), 800, 840
+    b = bounds_of(plan)
+    A, dD, W = values((plan.rows, K), 63, True), values((plan.rows, N), 64, True), values((3, N, K), 65, True)
+    C = torch.randint(-99, 100, (3, N, K), generator=gen(66), device="cuda").float()
+
+    def run():
+        return (g.gemm_experts(A, W, plan, out_dtype=F32), g.gemm_experts_backward_a(dD, W, plan, out_dtype=F32),
+                g.gemm_experts_backward_w(dD, A, plan, beta=1.0, C=C))
+
+    clean = run()
+    A[b[1]:b[2]] = float("nan")
+    dD[b[1]:b[2], 5] = float("inf")
+    C[2, 7, 9] = float("nan")
+    got = run()
+    status()
+    keep = torch.ones(plan.rows, dtype=torch.bool, device="cuda")
+    keep[b[1]:b[2]] = False
+    for x, y in zip(got[:2], clean[:2]):
+        assert torch.equal(x[keep], y[keep]) and not torch.isfinite(x[~keep]).any()
+    other = torch.ones((N, K), dtype=torch.bool, device="cuda")
+    other[7, 9] = False
+    assert torch.equal(got[2][0], clean[2][0]) and torch.isnan(got[2][1]).all()
+    assert torch.equal(got[2][2][other], clean[2][2][other]) and torch.isnan(got[2][2][7, 9])
+
+
+def test_a_captured_long_sum_follows_the_offsets():
+    """One graph, replayed with other row counts: few, none, and more than a segment, on tiles of both accumulators."""
+    E, N, K, rows = 4, 136, 832, 4000
+    plan = plan_of([1000] * 4, 0)
+    A, dD, W = values((rows, K), 71, True), values((rows, N), 72, True), values((E, N, K), 73, True)
+    D, dW = torch.empty(rows, N, device="cuda"), torch.empty(E, N, K, device="cuda")
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        g.gemm_experts(A, W, plan, out=D)
+        g.gemm_experts_backward_w(dD, A, plan, out=dW)
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            g.gemm_experts(A, W, plan, out=D)
+            g.gemm_experts_backward_w(dD, A, plan, out=dW)
+    torch.cuda.current_stream().wait_stream(side)
+    for counts in ([4000, 0, 0, 0], [1, 0, 3998, 1], [0, 0, 0, 0], [769, 1537, 15, 1600], [5, 6, 7, 8]):
+        plan.offsets.copy_(plan_of(counts, 0).offsets)
+        for _ in range(3):
+            graph.replay()
+        status()
+        check(D, forward64(A, W, plan)[0], None, K, True)
+        check(dW, weights64(dD, A, plan)[0], None, 0, True)
