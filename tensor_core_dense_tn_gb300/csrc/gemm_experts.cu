@@ -756,8 +756,8 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        if constexpr (kPair) mbar_arrive_cluster(acce_target + 8u * (a - acc));
-        else mbar_arrive(acce_bar(a));
+        if constexpr (kPair) mbar_arrive_relaxed_cluster(acce_target + 8u * (a - acc));
+        else mbar_arrive_relaxed(acce_bar(a));
       }
     };
     for (int t = first_tile + acc * step; t < num_tiles; t += (LONG ? 1 : 2) * step) {
