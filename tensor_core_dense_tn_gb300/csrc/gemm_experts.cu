@@ -769,16 +769,18 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
                ((OP == kExpertsWeights ? (long long)r.e * stride : 0) + (long long)row * ld + col) * esize;
       };
       if constexpr (LONG) {
-        // this warp's 64 rows of every segment, added up in fp32 registers
-        const int part = (warp - 2) / 4 * 64;
-        float sum[64];
+        // this warp's rows of every segment, added up in fp32 registers (with
+        // GROUPS a tile has 128 rows at most)
+        constexpr int kMine = GROUPS ? 32 : 64;
+        const int part = (warp - 2) / 4 * kMine;
+        float sum[kMine];
 #pragma unroll
-        for (int j = 0; j < 64; ++j) sum[j] = 0.0f;
+        for (int j = 0; j < kMine; ++j) sum[j] = 0.0f;
         if (S_::kWeights && p.has_c && r.col0 + (int)rank * p.col_tile + q * 32 < p.cols_out)
           // C, which no registers are left for, on its way to L2: 128 bytes of rows lane and lane + 32
           // (32 matrices of 2048 x 2048 with C, 1000 rows each: 342 us without, 298 with)
 #pragma unroll
-          for (int j = 0; j < 64; j += 32)
+          for (int j = 0; j < kMine; j += 32)
             if (part + lane + j < r.rows)
               prefetch_l2(static_cast<const uint8_t*>(element(p.C, p.ldc, p.stride_c, r.row0 + part + lane + j)) - lane * esize);
         const int whole = S_::kWeights ? (r.k_end - r.k0) / kBlockK : r.num_kb;
@@ -791,7 +793,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
           tc_fence_after();
           if (r.num_kb > 0) {
 #pragma unroll
-            for (int j = 0; j < 64; j += 16)
+            for (int j = 0; j < kMine; j += 16)
               if (part + j < r.rows) {
                 uint32_t x[16];
                 tmem_ld_rows(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * p.acc_cols + part + j), x);
@@ -804,7 +806,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
         }
         if (!ok) break;
 #pragma unroll
-        for (int j = 0; j < 64; j += 8)
+        for (int j = 0; j < kMine; j += 8)
           if (part + j < r.rows) {
             float v[8];
 #pragma unroll
