@@ -100,7 +100,7 @@ struct Shape {
   // 2048 x 2048 fp32 with C: 16 warps 404 us, 8 424); a product's long sums hide
   // the stores of 8 (one prompt through 128 experts: 818 us, with 16 840).
   // LONG: all of them take every segment, 64 rows each, whose fp32 sums fill
-  // most of a thread's 96 registers (24 to 132 bytes of them spill).
+  // most of a thread's 96 registers.
   static constexpr int kEpiWarps = kWeights || LONG ? 16 : 8;
   static constexpr int kRowsAtOnce = kWeights || LONG ? 16 : 32;
   static constexpr int kThreads = 32 * (2 + kEpiWarps + (kWeights ? 1 : 0));
@@ -146,6 +146,22 @@ template <bool CLUSTER>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Abort& ab) {
   if (try_wait<CLUSTER>(bar, parity)) return true;
   return wait_bar_slow<CLUSTER>(bar, parity, ab.flag, ab.timeout_ns, ab.status, ab.role);
+}
+
+// The same without a call, whose registers a warp full of sums would have to
+// spill: it gives up when another role has, or after kLeanLooks looks (a second
+// or more).
+constexpr uint32_t kLeanLooks = 1u << 27;
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_bar_lean(uint32_t bar, uint32_t parity, const Abort& ab) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < kLeanLooks; ++i) {
+    if (try_wait<CLUSTER>(bar, parity)) return true;
+    if (*ab.flag) return false;
+  }
+  *ab.flag = 1;
+  if (atomicCAS(ab.status, 0, kErrTimeout) == 0) atomicExch(ab.status + 1, (ab.role << 24) | (int)blockIdx.x);
+  return false;
 }
 
 __device__ __noinline__ void settle(uint64_t ns) {
@@ -747,7 +763,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
     const int acc = LONG ? 0 : (warp - 2) / (kEpiWarps / 2), c_first = (warp - 2) / 4 % (kEpiWarps / 8) * kRowsAtOnce;
     constexpr int kRowStep = kEpiWarps / 8 * kRowsAtOnce;
     Abort ab{abort_flag, p.timeout_ns, p.status, kRoleEpilogue};
-    const bool f32 = p.out_f32, pairs = p.pairs;
+    const bool f32 = LONG || p.out_f32, pairs = p.pairs;
     const int esize = f32 ? 4 : 2;
     uint32_t acc_phase = 0;
     const uint32_t acce_target = kPair ? mapa_shared(acce_bar(acc), 0) : acce_bar(acc);
@@ -788,7 +804,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
         bool ok = true;
         for (int i = 0; i < segments && ok; ++i, ++done) {
           const int a = done & 1;
-          ok = __all_sync(0xffffffffu, wait_bar<kPair>(accf_bar(a), (uint32_t)(done >> 1) & 1u, ab)) != 0;
+          ok = __all_sync(0xffffffffu, wait_bar_lean<kPair>(accf_bar(a), (uint32_t)(done >> 1) & 1u, ab)) != 0;
           if (!ok) break;
           tc_fence_after();
           if (r.num_kb > 0) {
@@ -805,9 +821,19 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
           hand_back(a);
         }
         if (!ok) break;
+        // Where it goes is worked out only now: in registers during the sum it
+        // spilled, and behind a full memory system a spilled word takes microseconds.
+        int again = t;
+        asm volatile("" : "+r"(again));
+        const Tile o = tile_of<CG, OP, GROUPS>(again, p, tb);
+        const int o_col = o.col0 + (int)rank * p.col_tile + q * 32 + lane;
+        const bool o_mine = q * 32 + lane < p.col_tile && o_col < p.cols_out;
+        auto place = [&](void* base, long long ld, long long stride, int row) {
+          return static_cast<float*>(base) + ((OP == kExpertsWeights ? (long long)o.e * stride : 0) + (long long)row * ld + o_col);
+        };
 #pragma unroll
         for (int j = 0; j < kMine; j += 8)
-          if (part + j < r.rows) {
+          if (part + j < o.rows) {
             float v[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] = p.alpha * sum[j + k];
@@ -815,11 +841,11 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
             if constexpr (OP == kExpertsWeights)
               if (p.has_c) {
                 uint32_t xc[8];
-                load_c(element(p.C, p.ldc, p.stride_c, r.row0 + part + j), p.ldc, r.rows - part - j, mine, true, false, xc);
+                load_c(place(const_cast<void*>(p.C), p.ldc, p.stride_c, o.row0 + part + j), p.ldc, o.rows - part - j, o_mine, true, false, xc);
                 add_c(xc, p.beta, true, false, v);
               }
-            store_rows_f32(reinterpret_cast<float*>(element(p.D, p.ldd, p.stride_d, r.row0 + part + j)), p.ldd,
-                           r.rows - part - j, mine, v);
+            store_rows_f32(place(p.D, p.ldd, p.stride_d, o.row0 + part + j), p.ldd,
+                           o.rows - part - j, o_mine, v);
           }
         if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
         continue;
