@@ -50,7 +50,7 @@
 //   operations       8192 tokens, 8 of 128 of 4096 x 2048, silu  684-713, floor 580
 //                    rows, 16384 rows, 8 of 8192 x 4096          599-629, floor 569
 //                    weights, the same                           587-608, floor 569
-//   both             9003 rows, 61 of 5000 x 2000, fp32          258, floor 211
+//   both             9003 rows, 61 of 5000 x 2000, fp32          239, floor 211
 //   output's bytes   weights, 64 of 2048 x 2048 fp32 with C      389, floor 336
 //                    weights, 61 of 1000 x 2000, 3 rows each      52, floor 36
 // (The ranges are of one program at different times: at 1400 W the clock moves.)
@@ -85,9 +85,9 @@ constexpr int kMaxStages = 16;
 // 2.1e-6 at 2000, about 8e-6 at 8192.  In LONG the two accumulators take segments
 // in turn and the storing warps add them, rounded, in registers.  Segments of 8,
 // 12 and 16 blocks leave 4.7e-7, 7.2e-7 and 1.0e-6 at every length; 9003 rows of
-// 61 experts of 5000 x 2000 take 270, 258 and 247 us with them, and 233 without any:
-// a segment's end costs the MMAs a wait for the warps that read the one
-// before.  bf16 results (an error of 1e-3) are added up by the tensor core alone.
+// 61 experts of 5000 x 2000 take 239, 239 and 238 us with them (233 without any),
+// 8192 tokens through 8 of 128 of 4096 x 2048 817, 795 and 790 us.  bf16 results
+// (an error of 1e-3) are added up by the tensor core alone.
 constexpr int kSegmentBlocks = 12;         // k-blocks of a segment
 static_assert(kSegmentBlocks % 4 == 0, "a whole number of stages of four k-blocks");
 
@@ -767,7 +767,9 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
     const int esize = f32 ? 4 : 2;
     uint32_t acc_phase = 0;
     const uint32_t acce_target = kPair ? mapa_shared(acce_bar(acc), 0) : acce_bar(acc);
-    // accumulator read: it goes back to the MMA warp
+    // accumulator read, its values in registers: it goes back to the MMA warp.
+    // Relaxed: a release across the cluster waits for the stores before it, 1000 to
+    // 9000 cycles (9003 rows of 61 of 5000 x 2000 in fp32: 258 us, relaxed 248).
     auto hand_back = [&](int a) {
       tc_fence_before();
       __syncwarp();
@@ -794,7 +796,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
         for (int j = 0; j < kMine; ++j) sum[j] = 0.0f;
         if (S_::kWeights && p.has_c && r.col0 + (int)rank * p.col_tile + q * 32 < p.cols_out)
           // C, which no registers are left for, on its way to L2: 128 bytes of rows lane and lane + 32
-          // (32 matrices of 2048 x 2048 with C, 1000 rows each: 342 us without, 298 with)
+          // (32 matrices of 2048 x 2048 with C, 1000 rows each: 342 us without, 298 with; 285 now)
 #pragma unroll
           for (int j = 0; j < kMine; j += 32)
             if (part + lane + j < r.rows)
