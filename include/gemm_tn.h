@@ -627,7 +627,12 @@ int gemm_w4_tn_experts(const gemm_expert_plan *plan, const void *A, int64_t lda,
  * that are multiples of 8 (GEMM_ERR_MISALIGNED otherwise).  D, dA, dW and C
  * are bf16 or fp32 (out_dtype) and may have any alignment to their element
  * size (bf16 with odd pitches or row lengths is slower).  Outputs must not overlap operands other than C.
- * Sums are fp32 and rounded once; their order does not change from run to run.
+ * Sums are held in fp32.  The tensor core cuts bits off at every 16 terms instead of
+ * rounding; for fp32 results it adds up at most 13 blocks of 64 terms by itself,
+ * and such segments are added rounded, so that the error stays below 1e-6 of the
+ * result's norm at any length (of a weights' gradient: an expert's, whatever the
+ * others have).  alpha and beta * C follow, each rounded, then the result's own
+ * rounding.  The order does not change from run to run.
  * activation is a gemm_activation; the gradients are those of the product
  * without it.
  *

@@ -88,6 +88,12 @@ constexpr int kMaxStages = 16;
 // 61 experts of 5000 x 2000 take 239, 239 and 238 us with them (233 without any),
 // 8192 tokens through 8 of 128 of 4096 x 2048 817, 795 and 790 us.  bf16 results
 // (an error of 1e-3) are added up by the tensor core alone.
+//   In `weights` every tile goes by its own expert's rows, so that an expert's
+// error, and its bits, do not depend on how many the others have.  A sum of one
+// segment takes the path without sums in registers, on which C is loaded ahead:
+// 64 matrices of 2048 x 2048 with C, 256 rows each, 404 us (539 with the other
+// path for all tiles, 391 in a kernel without it); 1000 rows each of 32, some of
+// one segment and some of two, 300.
 constexpr int kSegmentBlocks = 12;         // k-blocks of a segment
 static_assert(kSegmentBlocks % 4 == 0, "a whole number of stages of four k-blocks");
 
@@ -758,10 +764,12 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
     // Half of the warps take the tiles of one accumulator, half those of the other:
-    // while some store, the others wait for sums, read and convert.
+    // while some store, the others wait for sums, read and convert.  LONG: all take
+    // all of them, as the next segment's accumulator is the other one.
+    constexpr int kGroups = LONG ? 1 : 2;
     [[maybe_unused]] int done = 0;            // LONG: segments taken
-    const int acc = LONG ? 0 : (warp - 2) / (kEpiWarps / 2), c_first = (warp - 2) / 4 % (kEpiWarps / 8) * kRowsAtOnce;
-    constexpr int kRowStep = kEpiWarps / 8 * kRowsAtOnce;
+    const int acc = LONG ? 0 : (warp - 2) / (kEpiWarps / 2);
+    constexpr int kRowStep = kEpiWarps / (4 * kGroups) * kRowsAtOnce;
     Abort ab{abort_flag, p.timeout_ns, p.status, kRoleEpilogue};
     const bool f32 = LONG || p.out_f32, pairs = p.pairs;
     const int esize = f32 ? 4 : 2;
@@ -778,7 +786,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
         else mbar_arrive_relaxed(acce_bar(a));
       }
     };
-    for (int t = first_tile + acc * step; t < num_tiles; t += (LONG ? 1 : 2) * step) {
+    for (int t = first_tile + acc * step; t < num_tiles; t += kGroups * step) {
       const Tile r = tile_of<CG, OP, GROUPS>(t, p, tb);
       const int col = r.col0 + (int)rank * p.col_tile + q * 32 + lane;
       const bool mine = q * 32 + lane < p.col_tile && col < p.cols_out;
@@ -786,7 +794,10 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
         return const_cast<uint8_t*>(static_cast<const uint8_t*>(base)) +
                ((OP == kExpertsWeights ? (long long)r.e * stride : 0) + (long long)row * ld + col) * esize;
       };
-      if constexpr (LONG) {
+      // segments of this tile's sum (weights: of its own expert's rows)
+      const int whole = S_::kWeights ? (r.k_end - r.k0) / kBlockK : r.num_kb;
+      [[maybe_unused]] const int segments = max(1, (whole * group + kSegmentBlocks - 1) / kSegmentBlocks);
+      if (LONG && !(S_::kWeights && segments == 1)) {
         // this warp's rows of every segment, added up in fp32 registers (with
         // GROUPS a tile has 128 rows at most)
         constexpr int kMine = GROUPS ? 32 : 64;
@@ -801,8 +812,6 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
           for (int j = 0; j < kMine; j += 32)
             if (part + lane + j < r.rows)
               prefetch_l2(static_cast<const uint8_t*>(element(p.C, p.ldc, p.stride_c, r.row0 + part + lane + j)) - lane * esize);
-        const int whole = S_::kWeights ? (r.k_end - r.k0) / kBlockK : r.num_kb;
-        const int segments = max(1, (whole * group + kSegmentBlocks - 1) / kSegmentBlocks);
         bool ok = true;
         for (int i = 0; i < segments && ok; ++i, ++done) {
           const int a = done & 1;
@@ -852,19 +861,32 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
         if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
         continue;
       }
-      [[maybe_unused]] uint32_t xc[kRowsAtOnce];
+      // LONG: nothing that this path needs may be held in a register during the
+      // other's long sums, neither what follows from these (the rows' distances from
+      // one another, the same for all tiles) nor an undefined C.
+      int own = warp;
+      long long ldc = p.ldc, ldd = p.ldd;
+      if constexpr (LONG) asm volatile("" : "+r"(own), "+l"(ldc), "+l"(ldd));
+      const int c_first = (own - 2) / 4 % (kEpiWarps / (4 * kGroups)) * kRowsAtOnce;
+      [[maybe_unused]] uint32_t xc[kRowsAtOnce] = {};
       if constexpr (OP == kExpertsWeights)
         if (p.has_c)
-          load_c(element(p.C, p.ldc, p.stride_c, r.row0 + c_first), p.ldc, r.rows - c_first, mine, f32, pairs, xc);
+          load_c(element(p.C, ldc, p.stride_c, r.row0 + c_first), ldc, r.rows - c_first, mine, f32, pairs, xc);
+      const int a = LONG ? done & 1 : acc;
+      if constexpr (LONG) acc_phase = (uint32_t)(done++ >> 1) & 1u;
       // (the whole warp leaves, or none of it: what follows is warp-wide)
-      if (!__all_sync(0xffffffffu, wait_bar<kPair>(accf_bar(acc), acc_phase, ab))) break;
+      if constexpr (LONG) {
+        if (!__all_sync(0xffffffffu, wait_bar_lean<kPair>(accf_bar(a), acc_phase, ab))) break;
+      } else {
+        if (!__all_sync(0xffffffffu, wait_bar<kPair>(accf_bar(a), acc_phase, ab))) break;
+      }
       tc_fence_after();
 #pragma unroll 1
       for (int c = c_first; c < r.rows; c += kRowStep) {
         float v[kRowsAtOnce];
         if (r.num_kb > 0) {
           uint32_t x[kRowsAtOnce];
-          tmem_ld_rows(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * p.acc_cols + c), x);
+          tmem_ld_rows(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * p.acc_cols + c), x);
           tmem_wait_ld();
 #pragma unroll
           for (int j = 0; j < kRowsAtOnce; ++j) v[j] = __uint_as_float(x[j]);
@@ -883,14 +905,14 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
             // the next rows of C are on their way while these are stored
             const int next = c + kRowStep;
             if (next < r.rows)
-              load_c(element(p.C, p.ldc, p.stride_c, r.row0 + next), p.ldc, r.rows - next, mine, f32, pairs, xc);
+              load_c(element(p.C, ldc, p.stride_c, r.row0 + next), ldc, r.rows - next, mine, f32, pairs, xc);
           }
         }
-        uint8_t* to = element(p.D, p.ldd, p.stride_d, r.row0 + c);
-        if (f32) store_rows_f32(reinterpret_cast<float*>(to), p.ldd, r.rows - c, mine, v);
-        else store_rows_bf16(reinterpret_cast<uint16_t*>(to), p.ldd, r.rows - c, mine, pairs, v);
+        uint8_t* to = element(p.D, ldd, p.stride_d, r.row0 + c);
+        if (f32) store_rows_f32(reinterpret_cast<float*>(to), ldd, r.rows - c, mine, v);
+        else store_rows_bf16(reinterpret_cast<uint16_t*>(to), ldd, r.rows - c, mine, pairs, v);
       }
-      hand_back(acc);
+      hand_back(a);
       if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
       acc_phase ^= 1;
     }
@@ -934,7 +956,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
 }
 
 // 0: products on single k-blocks, 1: on groups, 2: rows, 3: weights on single
-// CTAs, 4: on pairs; from 5 on the same with long sums in fp32 (none of 3)
+// CTAs, 4: on pairs; from 5 on the same with long sums in fp32
 constexpr int kKernels = 10;
 
 int kernel_index(const ExpertsParams& p) {
@@ -947,7 +969,7 @@ const void* kernel_of(int index) {
       (const void*)gemm_experts_kernel<2, kExpertsForward, false, LONG>,
       (const void*)gemm_experts_kernel<2, kExpertsForward, true, LONG>,
       (const void*)gemm_experts_kernel<2, kExpertsRows, false, LONG>,
-      LONG ? nullptr : (const void*)gemm_experts_kernel<1, kExpertsWeights, false, false>,
+      (const void*)gemm_experts_kernel<1, kExpertsWeights, false, LONG>,
       (const void*)gemm_experts_kernel<2, kExpertsWeights, false, LONG>};
   return table[index];
 }
@@ -955,7 +977,7 @@ const void* kernel_of(int index) {
 const void* kernel_at(int index) { return index < 5 ? kernel_of<false>(index) : kernel_of<true>(index - 5); }
 
 int threads_of(int index) {
-  return index >= 5   ? (index == 9 ? Shape<kExpertsWeights, true>::kThreads : Shape<kExpertsForward, true>::kThreads)
+  return index >= 5   ? (index >= 8 ? Shape<kExpertsWeights, true>::kThreads : Shape<kExpertsForward, true>::kThreads)
          : index >= 3 ? Shape<kExpertsWeights, false>::kThreads
                       : Shape<kExpertsForward, false>::kThreads;
 }
@@ -976,11 +998,10 @@ void experts_geometry(ExpertsParams* p, int sms) {
   // where the output's memory decides: single CTAs, which need not wait for each
   // other (64 matrices of 2048 x 2048, single / pairs: 128 rows each, bf16, 130 /
   // 142 us; 256 rows 174 / 171; fp32 with C, 512 rows 444 / 454, 1024 rows 582 / 555).
-  // (LONG by the average: the sums' lengths are known on the device only, and
-  // with it for every call 256 rows each with C take 539 instead of 392 us, as C
-  // is then read behind the sum.)
-  p->long_sum = p->out_f32 && (weights ? average : p->S) > kSegmentBlocks * kBlockK;
-  p->cg = weights && !p->long_sum && average < (p->has_c ? 768 : 192) ? 1 : 2;
+  // LONG for weights wherever an expert can have more rows than a segment: how
+  // many each has is known on the device only, and every tile goes by its own.
+  p->long_sum = p->out_f32 && (weights ? p->R : p->S) > kSegmentBlocks * kBlockK;
+  p->cg = weights && average < (p->has_c ? 768 : 192) ? 1 : 2;
   const int step = 16 * p->cg;
   const int most = 2 * average < 32 ? 32 : 2 * average;
   p->tile_rows = weights || most > 256 ? 256 : (most + 31) / 32 * 32;
@@ -1048,13 +1069,12 @@ cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cu
   cfg.attrs = attr;
   if (!configured[dev]) {
     for (int i = 0; i < kKernels; ++i) {
-      if (!kernel_at(i)) continue;
       if ((e = cudaFuncSetAttribute(kernel_at(i), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax))) return e;
       cfg.gridDim = dim3(2);
       cfg.blockDim = dim3(threads_of(i));
       cfg.dynamicSmemBytes = kSmemMax;
       cfg.numAttrs = 1;
-      if (i != 3 && (e = cudaOccupancyMaxActiveClusters(&pairs[dev][i], kernel_at(i), &cfg))) return e;
+      if (i % 5 != 3 && (e = cudaOccupancyMaxActiveClusters(&pairs[dev][i], kernel_at(i), &cfg))) return e;
     }
     configured[dev] = true;
   }
@@ -1087,7 +1107,7 @@ cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cu
       "gemm_experts_kernel<rows>",            "gemm_experts_kernel<weights, 1>",
       "gemm_experts_kernel<weights, 2>",      "gemm_experts_kernel<forward, long>",
       "gemm_experts_kernel<forward, groups, long>", "gemm_experts_kernel<rows, long>",
-      nullptr,                                "gemm_experts_kernel<weights, 2, long>"};
+      "gemm_experts_kernel<weights, 1, long>", "gemm_experts_kernel<weights, 2, long>"};
   info->kernel = names[index];
   p.by_cols = fast_div(p.col_blocks);
   p.by_tiles = fast_div(p.row_blocks * p.col_blocks);
