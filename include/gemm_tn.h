@@ -653,6 +653,13 @@ int gemm_bf16_tn_experts_backward_w(const gemm_expert_plan *plan, int64_t N, int
                                     void *dW, int64_t lddw, int64_t stride_dw, float alpha, float beta,
                                     int out_dtype, void *stream);
 
+/* Limits of these three calls on the calling thread, from now on: cfg's
+ * wait_timeout_ns (how long a device-side wait may stand still) and test_fault
+ * (tests only: 1 and 2 = CTA 0 drops the loads of its first tile's first and last
+ * block, so that waits run out); its other fields are not used.  NULL: the
+ * defaults again. */
+int gemm_experts_config(const gemm_tn_config *cfg);
+
 /* ------------------------------------------------------------------------
  * The norm of many gradient tensors, and clipping by it.
  *

@@ -43,7 +43,7 @@ EXPORTED = ["gemm_bf16_tn", "gemm_bf16_tn_ex", "gemm_get_status", "gemm_get_stat
             "gemm_mma_rate", "gemm_fp8_tn_bias_act", "gemm_expert_dispatch", "gemm_expert_dispatch_backward",
             "gemm_expert_combine", "gemm_expert_combine_backward", "gemm_w4_tn", "gemm_w4_tn_experts",
             "gemm_bf16_tn_experts", "gemm_bf16_tn_experts_backward_a", "gemm_bf16_tn_experts_backward_w",
-            "gemm_grad_workspace", "gemm_grad_norm", "gemm_clip_grad_norm"]
+            "gemm_experts_config", "gemm_grad_workspace", "gemm_grad_norm", "gemm_clip_grad_norm"]
 
 FP8_E4M3, FP8_E5M2 = 0, 1
 SCHED_DEFAULT, SCHED_STATIC, SCHED_CLC = 0, 1, 2
@@ -177,6 +177,8 @@ def load(path: str = LIB_PATH):
         lib.gemm_bf16_tn_experts_backward_w.argtypes = [plan, i64, i64, vp, i64, vp, i64, vp, i64, i64, vp, i64, i64,
                                                         f32, f32, i32, vp]
         lib.gemm_bf16_tn_experts_backward_w.restype = i32
+        lib.gemm_experts_config.argtypes = [ctypes.POINTER(GemmConfig)]
+        lib.gemm_experts_config.restype = i32
         lib.gemm_grad_workspace.argtypes = [i32]
         lib.gemm_grad_workspace.restype = i64
         lib.gemm_grad_norm.argtypes = [i32, vp, vp, vp, vp]
@@ -404,6 +406,12 @@ def gemm_bf16_tn_experts_backward_w(plan, N, K, dD, lddd, A, lda, C, ldc, stride
     """Raw C-ABI call: dW_e = alpha * dD_e^T * A_e + beta * C_e."""
     return load().gemm_bf16_tn_experts_backward_w(plan, N, K, dD or None, lddd, A or None, lda, C or None, ldc, stride_c,
                                                   dW or None, lddw, stride_dw, alpha, beta, out_dtype, stream or None)
+
+
+def gemm_experts_config(config=None) -> int:
+    """Raw C-ABI call: wait_timeout_ns and test_fault of a GemmConfig for this thread's products by expert from now on
+    (None: the defaults)."""
+    return load().gemm_experts_config(ctypes.byref(config) if config is not None else None)
 
 
 def gemm_grad_workspace(num) -> int:

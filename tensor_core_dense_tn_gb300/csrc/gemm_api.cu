@@ -1084,6 +1084,8 @@ int encode_kblocks(CUtensorMap* m, const void* base, int64_t K, int64_t rows, in
   return GEMM_OK;
 }
 
+thread_local gemm_tn_config t_experts_config = {};       // gemm_experts_config
+
 // op: kExpertsForward (X = A), kExpertsRows (X = dD) with out = R rows, or
 // kExpertsWeights (X = dD, Y = A) with out = E matrices of N x K.
 int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, const void* X, int64_t ldx, const void* Y,
@@ -1148,7 +1150,8 @@ int run_experts(int op, const gemm_expert_plan* plan, int64_t N, int64_t K, cons
     return aligned_to(base, 4) && ld % 2 == 0 && (!weights || stride % 2 == 0);
   };
   p.pairs = cols % 2 == 0 && even(D, ldd, stride_d) && (!p.has_c || even(C, ldc, stride_c));
-  p.timeout_ns = timeout_ns(nullptr);
+  p.timeout_ns = timeout_ns(&t_experts_config);
+  p.fault = t_experts_config.test_fault;
   p.status = st->status;
   experts_geometry(&p, st->sms);
   const int64_t col_blocks = (cols + p.col_tile * p.cg - 1) / (p.col_tile * p.cg);
@@ -1445,6 +1448,15 @@ int gemm_bf16_tn_experts_backward_w(const gemm_expert_plan* plan, int64_t N, int
                                     void* stream) {
   return gtn::run_experts(gtn::kExpertsWeights, plan, N, K, dD, lddd, A, lda, 0, C, ldc, stride_c, dW, lddw, stride_dw,
                           alpha, beta, out_dtype, GEMM_ACT_NONE, stream);
+}
+
+int gemm_experts_config(const gemm_tn_config* cfg) {
+  using namespace gtn;
+  t_error.clear();
+  if (cfg && (cfg->test_fault < 0 || cfg->test_fault > 2))
+    return fail(GEMM_ERR_INVALID_VALUE, "test_fault must be 0, 1 or 2, got %d", cfg->test_fault);
+  t_experts_config = cfg ? *cfg : gemm_tn_config{};
+  return GEMM_OK;
 }
 
 // (The lists grow with num: what the allocator throws ends here.)

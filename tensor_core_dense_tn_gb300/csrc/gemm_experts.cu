@@ -57,11 +57,13 @@
 // In the second group the tensor pipe is active 89-91% of the time with about 1000
 // rows an expert, and 72-74% in `weights`, whose tiles are 16 k-blocks then.
 //
-// Every mbarrier wait is bounded by %globaltimer; one that gives up sets a
-// CTA abort flag and the device status word, and all roles leave.
+// Every mbarrier wait is bounded by %globaltimer; one that gives up sets the
+// abort flags of its CTA and of the pair's other one and the device status word,
+// and all roles of both leave.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 
 #include "epilogue.cuh"
@@ -77,7 +79,7 @@ constexpr int kChunkBytes = 64 * 128;      // 64 rows of 64 bf16: a chunk of an 
 constexpr int kPartBytes = 16 * 128;       // 16 rows of it: a chunk of a sum's last, shorter block
 constexpr int kColBytes = 128 * 128;       // a stage of the columns' operand: 128 of them per CTA
 constexpr int kErrTimeout = -5;            // GEMM_ERR_TIMEOUT
-constexpr int kMaxStages = 16;
+constexpr uint64_t kSettleNs = 2000000;    // what copies in flight are given to land after a wait has run out
 
 // Terms that the tensor core adds up by itself for an fp32 result of a long sum
 // (LONG).  Its accumulator cuts bits off at every MMA instead of rounding, so
@@ -112,17 +114,39 @@ struct Shape {
   static constexpr int kThreads = 32 * (2 + kEpiWarps + (kWeights ? 1 : 0));
 };
 
-// barriers: full, empty, and for ragged blocks tail and ready, per stage; accumulators; the drain
-constexpr int kBars = 4 * kMaxStages + 5;
+// Ring stages at most (of `weights`: 32 or 48 KB each, 7 fit), and barriers: full,
+// empty, and for ragged blocks tail and ready, per stage; accumulators; the drain.
+__host__ __device__ constexpr int max_stages(bool weights) { return weights ? 8 : 16; }
+__host__ __device__ constexpr int bars_of(bool weights) { return (weights ? 4 : 2) * max_stages(weights) + 5; }
 
 __host__ __device__ constexpr int table_bytes(int E) { return 4 * (2 * E + 4); }
 
+// What the roles of a CTA share at addresses known to the compiler, which take
+// no registers.
+struct __align__(16) Control {
+  uint32_t tmem;              // base of the accumulators
+  uint32_t abort;             // a wait of this CTA, or of the pair's other one, has run out
+  uint32_t since[16];         // LONG: a storing warp's clock (wait_bar_lean)
+};
+constexpr uint32_t kLate = 2;   // abort: set by wait_bar_lean
+
 struct Abort {
-  volatile uint32_t* flag;
+  Control* c;
   uint64_t timeout_ns;
   int* status;
   int role;
+  bool pair;
 };
+
+__device__ __forceinline__ bool aborting(const Control& c) { return *const_cast<const volatile uint32_t*>(&c.abort) != 0; }
+
+// This CTA and the other one of its pair leave.  (Every wait ends before its CTA
+// meets the other for the last time, so the other's shared memory is there.)
+__device__ __forceinline__ void give_up(Control* c, bool pair, int* status, int role) {
+  *const_cast<volatile uint32_t*>(&c->abort) = 1;
+  if (pair) st_shared_cluster_u32(mapa_shared(smem_u32(&c->abort), cluster_ctarank() ^ 1u), 1);
+  if (atomicCAS(status, 0, kErrTimeout) == 0) atomicExch(status + 1, (role << 24) | (int)blockIdx.x);
+}
 
 template <bool CLUSTER>
 __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
@@ -131,17 +155,16 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
 }
 
 template <bool CLUSTER>
-__device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, volatile uint32_t* flag, uint64_t timeout_ns,
-                                           int* status, int role) {
+__device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, Control* c, uint64_t timeout_ns, int* status,
+                                           int role, bool pair) {
   const uint64_t t0 = globaltimer();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (try_wait<CLUSTER>(bar, parity)) return true;
-    if (flag && *flag) return false;
+    if (aborting(*c)) return false;
     if (globaltimer() - t0 > timeout_ns) {
-      if (flag) *flag = 1;
-      if (atomicCAS(status, 0, kErrTimeout) == 0) atomicExch(status + 1, (role << 24) | (int)blockIdx.x);
+      give_up(c, pair, status, role);
       return false;
     }
   }
@@ -151,23 +174,35 @@ __device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, volati
 template <bool CLUSTER>
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Abort& ab) {
   if (try_wait<CLUSTER>(bar, parity)) return true;
-  return wait_bar_slow<CLUSTER>(bar, parity, ab.flag, ab.timeout_ns, ab.status, ab.role);
+  return wait_bar_slow<CLUSTER>(bar, parity, ab.c, ab.timeout_ns, ab.status, ab.role, ab.pair);
 }
 
 // The same without a call, whose registers a warp full of sums would have to
-// spill: it gives up when another role has, or after kLeanLooks looks (a second
-// or more).
-constexpr uint32_t kLeanLooks = 1u << 27;
+// spill, and with its clock in shared memory: in units of 2^16 ns, read every 256
+// looks.  A warp whose clock has run out tells its CTA's roles alone; the rest of
+// give_up() follows when it has left its tiles.
 template <bool CLUSTER>
-__device__ __forceinline__ bool wait_bar_lean(uint32_t bar, uint32_t parity, const Abort& ab) {
+__device__ __forceinline__ bool wait_bar_lean(uint32_t bar, uint32_t parity, Control& c, uint32_t units) {
 #pragma unroll 1
-  for (uint32_t i = 0; i < kLeanLooks; ++i) {
+  for (uint32_t i = 1;; ++i) {
     if (try_wait<CLUSTER>(bar, parity)) return true;
-    if (*ab.flag) return false;
+    if (aborting(c)) return false;
+    if (i & 255) continue;
+    volatile uint32_t* since = &c.since[(threadIdx.x >> 5) - 2];
+    const uint32_t now = (uint32_t)(globaltimer() >> 16);
+    if (i == 256) *since = now;
+    else if (now - *since > units) *const_cast<volatile uint32_t*>(&c.abort) = kLate;
   }
-  *ab.flag = 1;
-  if (atomicCAS(ab.status, 0, kErrTimeout) == 0) atomicExch(ab.status + 1, (ab.role << 24) | (int)blockIdx.x);
-  return false;
+}
+
+// The commit behind all MMAs, whether or not a wait has run out: they may take no
+// longer than what the ring holds, but a limit set short is not for them.
+template <bool CLUSTER>
+__device__ __noinline__ bool wait_drain(uint32_t bar, uint64_t timeout_ns) {
+  const uint64_t t0 = globaltimer(), limit = timeout_ns > 100000000 ? timeout_ns : 100000000;
+  while (!try_wait<CLUSTER>(bar, 0))
+    if (globaltimer() - t0 > limit) return false;
+  return true;
 }
 
 __device__ __noinline__ void settle(uint64_t ns) {
@@ -485,6 +520,8 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
   using S_ = Shape<OP, LONG>;
   constexpr int kEpiWarps = S_::kEpiWarps, kRowsAtOnce = S_::kRowsAtOnce;
   constexpr bool kPair = CG == 2;
+  constexpr int kMaxStages = max_stages(S_::kWeights), kBars = bars_of(S_::kWeights), kAccBars = kBars - 5;
+  __shared__ Control ctl;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sC = smem_u32(smem);                       // the columns' operand
@@ -495,12 +532,10 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
   auto empty_bar = [&](int s) { return bar0 + 8u * (kMaxStages + s); };
   auto tail_bar = [&](int s) { return bar0 + 8u * (2 * kMaxStages + s); };    // this CTA's bytes of a ragged block
   auto ready_bar = [&](int s) { return bar0 + 8u * (3 * kMaxStages + s); };   // leader: every CTA has zeroed it
-  auto accf_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + b); };
-  auto acce_bar = [&](int b) { return bar0 + 8u * (4 * kMaxStages + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (4 * kMaxStages + 4);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars);
-  volatile uint32_t* abort_flag = tmem_slot + 1;
-  Note* notes = reinterpret_cast<Note*>(tmem_slot + 2);     // one per stage
+  auto accf_bar = [&](int b) { return bar0 + 8u * (kAccBars + b); };
+  auto acce_bar = [&](int b) { return bar0 + 8u * (kAccBars + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (kAccBars + 4);
+  Note* notes = reinterpret_cast<Note*>(bars + kBars);      // one per stage
   Table tb;
   tb.row = reinterpret_cast<int*>(notes + kMaxStages);
   tb.tile = tb.row + p.E + 1;
@@ -516,15 +551,17 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
-      mbar_init(tail_bar(s), 1);
-      mbar_init(ready_bar(s), CG);
+      if constexpr (S_::kWeights) {
+        mbar_init(tail_bar(s), 1);
+        mbar_init(ready_bar(s), CG);
+      }
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(accf_bar(b), 1);
       mbar_init(acce_bar(b), (LONG ? kEpiWarps : kEpiWarps / 2) * CG);
     }
     mbar_init(drain_bar, 1);
-    *abort_flag = 0;
+    ctl.abort = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
     if (p.has_ab) {
@@ -534,7 +571,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
       for (int i = 0; i < (S_::kWeights ? 1 : p.row_box < 64 ? 0 : 3); ++i) tma_prefetch_desc(&maps.rows_part[i]);
     }
   }
-  if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), 2 * p.acc_cols);
+  if (warp == 1) tmem_alloc<CG>(smem_u32(&ctl.tmem), 2 * p.acc_cols);
   // Inputs may come from the previous kernel on the stream: no global memory
   // access before this point.
   griddep_wait();
@@ -546,7 +583,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
   __syncthreads();
   if constexpr (kPair) cluster_sync();
   tc_fence_after();
-  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t tmem_base = ctl.tmem;
   const int num_tiles = (S_::kWeights ? p.E * p.row_blocks : tb.tile[p.E + 1]) * p.col_blocks;
   // the rows of an expert's last block that are not its own, when the MMA would take some of them
   auto ragged = [](const Tile& r) { return S_::kWeights && ((r.k_end - r.k0) & 15) != 0; };
@@ -554,7 +591,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
   if (warp == 0) {
     // ------------------------------------------------------------ loads
     // (the whole warp, one elected lane of which issues, as below)
-    Abort ab{abort_flag, p.timeout_ns, p.status, kRoleProducer};
+    Abort ab{&ctl, p.timeout_ns, p.status, kRoleProducer, kPair};
     auto wait_empty = [&](int s, uint32_t parity) {
       return __all_sync(0xffffffffu, wait_bar<kPair>(empty_bar(s), parity, ab)) != 0;
     };
@@ -587,6 +624,8 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
           (uint32_t)(group * (p.col_tile * 128 + (S_::kWeights ? chunks * kChunkBytes : box_rows * 128)));
       const CUtensorMap* row_map = box == 3 ? &maps.rows : &maps.rows_part[box];
       const int blocks = (sum + kBlockK * group - 1) / (kBlockK * group), whole = S_::kWeights ? sum / kBlockK : blocks;
+      // (tests: the block of the first tile whose copies CTA 0 leaves out)
+      const int dropped = p.fault && blockIdx.x == 0 && t == 0 ? (p.fault & kFaultSkipTmaOnce ? 0 : blocks - 1) : -1;
       for (int kb = 0; kb < whole; ++kb) {
         ok = wait_empty(stage, phase ^ 1);
         if (!ok) break;
@@ -597,8 +636,10 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
         if (elect_one()) {
           if (kb == 0) notes[stage] = Note{n, sum, empty, box_rows};
           if (leader) mbar_arrive_expect_tx(fb, tx * CG);
-          load_cols<OP, kPair, GROUPS>(c, &maps.cols, p.wide_cols, c_at, k, e, kChunkBytes, to);
-          load_rows<OP, kPair, GROUPS>(b, row_map, p.wide_rows, r_at, k, kChunkBytes, chunks, to);
+          if (kb != dropped) {
+            load_cols<OP, kPair, GROUPS>(c, &maps.cols, p.wide_cols, c_at, k, e, kChunkBytes, to);
+            load_rows<OP, kPair, GROUPS>(b, row_map, p.wide_rows, r_at, k, kChunkBytes, chunks, to);
+          }
         }
         advance();
       }
@@ -620,7 +661,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
             else mbar_arrive_expect_tx(fb, part_tx * CG);
           }
           if (own) mbar_arrive_expect_tx(tail, part_tx);
-          for (int i = 0; i < parts; ++i) {
+          for (int i = whole == dropped ? parts : 0; i < parts; ++i) {
             const uint32_t ci = sC + stage * kColBytes + i * (kColBytes / 4), bi = sR + stage * p.row_bytes + i * (p.row_bytes / 4);
             const int k = k0 + whole * kBlockK + 16 * i;
             if (own) {
@@ -640,13 +681,12 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
       notes[stage] = Note{0, 0, empty, 0};
       mbar_arrive(full_bar(stage));
     }
-    if (!ok) settle(2000000);   // copies already issued land before teardown
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA
     // The whole warp runs this, and one elected lane issues: with one lane in
     // here alone each MMA took 69 cycles to issue and each block 590, whatever its N.
     if (leader) {
-      Abort ab{abort_flag, p.timeout_ns, p.status, kRoleMma};
+      Abort ab{&ctl, p.timeout_ns, p.status, kRoleMma, kPair};
       // (the whole warp leaves, or none of it)
       auto wait_all = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait_bar<kPair>(bar, parity, ab)) != 0;
@@ -758,8 +798,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
     }
     // Both CTAs of a pair wait: the commits before this one arrive on both, and
     // none may come after a CTA has left its shared memory to the next.
-    Abort ab_drain{nullptr, p.timeout_ns, p.status, kRoleMma};
-    wait_bar<kPair>(drain_bar, 0, ab_drain);
+    wait_drain<kPair>(drain_bar, p.timeout_ns);
   } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
@@ -770,7 +809,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
     [[maybe_unused]] int done = 0;            // LONG: segments taken
     const int acc = LONG ? 0 : (warp - 2) / (kEpiWarps / 2);
     constexpr int kRowStep = kEpiWarps / (4 * kGroups) * kRowsAtOnce;
-    Abort ab{abort_flag, p.timeout_ns, p.status, kRoleEpilogue};
+    Abort ab{&ctl, p.timeout_ns, p.status, kRoleEpilogue, kPair};
     const bool f32 = LONG || p.out_f32, pairs = p.pairs;
     const int esize = f32 ? 4 : 2;
     uint32_t acc_phase = 0;
@@ -815,7 +854,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
         bool ok = true;
         for (int i = 0; i < segments && ok; ++i, ++done) {
           const int a = done & 1;
-          ok = __all_sync(0xffffffffu, wait_bar_lean<kPair>(accf_bar(a), (uint32_t)(done >> 1) & 1u, ab)) != 0;
+          ok = __all_sync(0xffffffffu, wait_bar_lean<kPair>(accf_bar(a), (uint32_t)(done >> 1) & 1u, ctl, p.timeout_units)) != 0;
           if (!ok) break;
           tc_fence_after();
           if (r.num_kb > 0) {
@@ -858,7 +897,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
             store_rows_f32(place(p.D, p.ldd, p.stride_d, o.row0 + part + j), p.ldd,
                            o.rows - part - j, o_mine, v);
           }
-        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+        if (__any_sync(0xffffffffu, aborting(ctl))) break;
         continue;
       }
       // LONG: nothing that this path needs may be held in a register during the
@@ -876,7 +915,7 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
       if constexpr (LONG) acc_phase = (uint32_t)(done++ >> 1) & 1u;
       // (the whole warp leaves, or none of it: what follows is warp-wide)
       if constexpr (LONG) {
-        if (!__all_sync(0xffffffffu, wait_bar_lean<kPair>(accf_bar(a), acc_phase, ab))) break;
+        if (!__all_sync(0xffffffffu, wait_bar_lean<kPair>(accf_bar(a), acc_phase, ctl, p.timeout_units))) break;
       } else {
         if (!__all_sync(0xffffffffu, wait_bar<kPair>(accf_bar(a), acc_phase, ab))) break;
       }
@@ -913,12 +952,13 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
         else store_rows_bf16(reinterpret_cast<uint16_t*>(to), ldd, r.rows - c, mine, pairs, v);
       }
       hand_back(a);
-      if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+      if (__any_sync(0xffffffffu, aborting(ctl))) break;
       acc_phase ^= 1;
     }
+    if (LONG && *const_cast<volatile uint32_t*>(&ctl.abort) == kLate) give_up(&ctl, kPair, p.status, kRoleEpilogue);
   } else if constexpr (S_::kWeights) {
     // ------------------------------------------------------------ ragged blocks
-    Abort ab{abort_flag, p.timeout_ns, p.status, kRoleProducer};
+    Abort ab{&ctl, p.timeout_ns, p.status, kRoleProducer, kPair};
     int stage = 0;
     uint32_t tail_phase = 0;            // one bit per stage
     const int chunks = p.row_bytes / kChunkBytes;
@@ -948,6 +988,9 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
   }
 
   __syncthreads();
+  // Whatever wait ran out: copies already on their way, into this CTA or by it, land
+  // before either CTA gives its shared memory to the next.
+  if (aborting(ctl)) settle(kSettleNs);
   if constexpr (kPair) cluster_sync();
   if (warp == 1) {
     tc_fence_after();
@@ -982,10 +1025,11 @@ int threads_of(int index) {
                       : Shape<kExpertsForward, false>::kThreads;
 }
 
-constexpr int kSmemMax = 232448;
+constexpr int kSmemMax = 232448 - (int)sizeof(Control);      // beside what is static
 
 int smem_bytes(const ExpertsParams& p) {
-  return 1024 + p.stages * p.group * (kColBytes + p.row_bytes) + kBars * 8 + 8 + kMaxStages * (int)sizeof(Note) + table_bytes(p.E);
+  return 1024 + p.stages * p.group * (kColBytes + p.row_bytes) + bars_of(p.op == kExpertsWeights) * 8 +
+         max_stages(p.op == kExpertsWeights) * (int)sizeof(Note) + table_bytes(p.E);
 }
 
 }  // namespace
@@ -1038,7 +1082,7 @@ void experts_geometry(ExpertsParams* p, int sms) {
     for (int g = 4; g > 1 && p->group == 1; g /= 2)
       if (p->S >= g * kBlockK && room >= 3 * g * (kColBytes + p->row_bytes)) p->group = g;
   p->stages = room / (p->group * (kColBytes + p->row_bytes));
-  if (p->stages > kMaxStages) p->stages = kMaxStages;
+  if (p->stages > max_stages(weights)) p->stages = max_stages(weights);
 }
 
 FastDiv fast_div(uint32_t d) {
@@ -1109,6 +1153,7 @@ cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cu
       "gemm_experts_kernel<forward, groups, long>", "gemm_experts_kernel<rows, long>",
       "gemm_experts_kernel<weights, 1, long>", "gemm_experts_kernel<weights, 2, long>"};
   info->kernel = names[index];
+  p.timeout_units = (uint32_t)std::min<uint64_t>((p.timeout_ns >> 16) + 1, 1u << 31);
   p.by_cols = fast_div(p.col_blocks);
   p.by_tiles = fast_div(p.row_blocks * p.col_blocks);
   p.by_strip = fast_div(p.strip);

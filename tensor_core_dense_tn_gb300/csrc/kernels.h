@@ -23,6 +23,7 @@ constexpr int kL2HintAEvictLast = 1, kL2HintBEvictFirst = 2, kL2HintDEvictFirst 
 
 // Test-only fault injection bits.
 constexpr int kFaultSkipTmaOnce = 1;
+constexpr int kFaultSkipLastTma = 2;   // products by expert: the last block of the first tile
 
 // Activation codes (same values as gemm_activation in gemm_tn.h).
 constexpr int kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4;
@@ -236,7 +237,9 @@ struct ExpertsParams {
   int row_block;       // weights: rows of a tile but the last of a matrix
   int strip;           // row blocks per strip of the tile order
   FastDiv by_cols, by_tiles, by_strip, by_strip_tiles;   // launch: col_blocks, tiles of a matrix, strip, strip * col_blocks
+  int fault;           // kFault* bits (tests only)
   uint64_t timeout_ns;
+  uint32_t timeout_units;                  // launch: the same in 2^16 ns
   int* status;
 };
 
