@@ -57,9 +57,10 @@
 // In the second group the tensor pipe is active 89-91% of the time with about 1000
 // rows an expert, and 72-74% in `weights`, whose tiles are 16 k-blocks then.
 //
-// Every mbarrier wait is bounded by %globaltimer; one that gives up sets the
-// abort flags of its CTA and of the pair's other one and the device status word,
-// and all roles of both leave.
+// Every mbarrier wait is bounded by %globaltimer: it gives up where its CTA has
+// stood still (no block multiplied, no accumulator handed over) for as long as the
+// limit, however long the call takes.  It then sets the abort flags of its CTA and
+// of the pair's other one and the device status word, and all roles of both leave.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -126,6 +127,8 @@ __host__ __device__ constexpr int table_bytes(int E) { return 4 * (2 * E + 4); }
 struct __align__(16) Control {
   uint32_t tmem;              // base of the accumulators
   uint32_t abort;             // a wait of this CTA, or of the pair's other one, has run out
+  uint32_t stages;            // barriers that show progress: `stages` of them from `empty` on, two from `accf` on
+  uint32_t empty, accf;
   uint32_t since[16];         // LONG: a storing warp's clock (wait_bar_lean)
 };
 constexpr uint32_t kLate = 2;   // abort: set by wait_bar_lean
@@ -154,19 +157,39 @@ __device__ __forceinline__ bool try_wait(uint32_t bar, uint32_t parity) {
   else return mbar_try_wait(bar, parity);
 }
 
+// A number that changes with every block whose MMAs are done and every accumulator
+// that is handed over: the parities of their barriers.  (A count that the loading
+// warp keeps in shared memory cost the weights' gradients 2%.)
+__device__ __forceinline__ uint32_t progress(const Control& c) {
+  uint32_t bits = 0;
+#pragma unroll 1
+  for (uint32_t i = 0; i < c.stages; ++i) bits = bits << 1 | (uint32_t)mbar_test_wait(c.empty + 8u * i, 0);
+  return bits << 2 | (uint32_t)mbar_test_wait(c.accf, 0) << 1 | (uint32_t)mbar_test_wait(c.accf + 8u, 0);
+}
+
+// The limit is on seeing the same so many times in a row.  (A parity that has changed
+// an even number of times looks the same, but not sixteen times.)
+constexpr uint32_t kGlances = 16;
+
 template <bool CLUSTER>
 __device__ __noinline__ bool wait_bar_slow(uint32_t bar, uint32_t parity, Control* c, uint64_t timeout_ns, int* status,
                                            int role, bool pair) {
-  const uint64_t t0 = globaltimer();
+  uint64_t t0 = globaltimer();
+  uint32_t seen = ~0u, same = 0;
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 32; ++i)
       if (try_wait<CLUSTER>(bar, parity)) return true;
     if (aborting(*c)) return false;
-    if (globaltimer() - t0 > timeout_ns) {
+    if (globaltimer() - t0 <= timeout_ns / kGlances) continue;
+    const uint32_t now = progress(*c);
+    same = now == seen ? same + 1 : 0;
+    if (same == kGlances) {
       give_up(c, pair, status, role);
       return false;
     }
+    seen = now;
+    t0 = globaltimer();
   }
 }
 
@@ -179,7 +202,8 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const Ab
 
 // The same without a call, whose registers a warp full of sums would have to
 // spill, and with its clock in shared memory: in units of 2^16 ns, read every 256
-// looks.  A warp whose clock has run out tells its CTA's roles alone; the rest of
+// looks.  (It waits for one segment at a time, so that any progress but its own is
+// not looked at.)  A warp whose clock has run out tells its CTA's roles alone; the rest of
 // give_up() follows when it has left its tiles.
 template <bool CLUSTER>
 __device__ __forceinline__ bool wait_bar_lean(uint32_t bar, uint32_t parity, Control& c, uint32_t units) {
@@ -562,6 +586,9 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
     }
     mbar_init(drain_bar, 1);
     ctl.abort = 0;
+    ctl.stages = (uint32_t)p.stages;
+    ctl.empty = empty_bar(0);
+    ctl.accf = accf_bar(0);
     fence_mbar_init();
     fence_proxy_async_smem();
     if (p.has_ab) {
@@ -795,10 +822,8 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
       }
       // All MMAs that were issued complete before TMEM is released.
       if (elect_one()) commit(drain_bar);
+      if (!wait_drain<kPair>(drain_bar, p.timeout_ns)) give_up(&ctl, kPair, p.status, kRoleMma);
     }
-    // Both CTAs of a pair wait: the commits before this one arrive on both, and
-    // none may come after a CTA has left its shared memory to the next.
-    wait_drain<kPair>(drain_bar, p.timeout_ns);
   } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;                   // TMEM lane quarter this warp may access
@@ -988,6 +1013,10 @@ __global__ void __launch_bounds__(Shape<OP, LONG>::kThreads, 1)
   }
 
   __syncthreads();
+  // Both CTAs of a pair wait for the last commit: those before it arrive on both, and
+  // none may come after a CTA has left its shared memory to the next.  (The one
+  // without MMAs only now, when its other roles are done, or the call's time would count.)
+  if (kPair && !leader && warp == 1 && !wait_drain<kPair>(drain_bar, p.timeout_ns)) give_up(&ctl, kPair, p.status, kRoleMma);
   // Whatever wait ran out: copies already on their way, into this CTA or by it, land
   // before either CTA gives its shared memory to the next.
   if (aborting(ctl)) settle(kSettleNs);

@@ -65,6 +65,32 @@ def test_a_dropped_load_ends_in_a_timeout(config, which, dtype, counts, N, K, fa
         assert torch.equal(call(), right) and g.gemm_get_status(s) == 0
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("counts,N,K", [([8192] * 40 + [17], 4096, 4096), ([1 << 22], 64, 64)])
+def test_a_limit_shorter_than_the_call(config, dtype, counts, N, K):
+    """The limit is on standing still: a call of many times its length is right, also where a role waits all that time
+    (for the one ragged block, behind all others; for the sum of a single tile)."""
+    limit = 500_000
+    plan = plan_of(counts, 0)
+    A, dD, W = values((plan.rows, K), 1, False), values((plan.rows, N), 2, False), values((len(counts), N, K), 3, False)
+    s = torch.cuda.current_stream().cuda_stream
+    for call, takes_long in ((lambda: g.gemm_experts_backward_w(dD, A, plan, out_dtype=dtype), True),
+                             (lambda: g.gemm_experts(A, W, plan, out_dtype=dtype), K > 64),
+                             (lambda: g.gemm_experts_backward_a(dD, W, plan, out_dtype=dtype), K > 64)):
+        config()
+        call()
+        began, ended = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        began.record()
+        want = call()
+        ended.record()
+        assert g.gemm_get_status(s) == 0
+        took = began.elapsed_time(ended) * 1e6
+        assert config(wait_timeout_ns=limit) == 0
+        for _ in range(3):
+            assert torch.equal(call(), want) and g.gemm_get_status(s) == 0
+        assert took > 4 * limit or not takes_long, took
+
+
 def test_the_settings_are_the_threads_own(config):
     import threading
     assert config(wait_timeout_ns=LIMIT, test_fault=1) == 0
