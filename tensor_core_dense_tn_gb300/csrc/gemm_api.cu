@@ -81,6 +81,13 @@ int init_device(int* dev_out, DeviceState** st_out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
   if (dev < 0 || dev >= kMaxDevices) return fail(GEMM_ERR_UNSUPPORTED_DEVICE, "device index %d out of range", dev);
+  // A thread whose first CUDA call this is has no context yet, which the driver's
+  // encoding of tensor maps needs (it fails with 201 without one).
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    if ((e = cudaSetDevice(dev)) != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(e));
+    bound = dev;
+  }
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState& st = g_dev[dev];
   if (!st.ready) {
