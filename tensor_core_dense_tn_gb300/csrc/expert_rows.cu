@@ -749,19 +749,20 @@ cudaError_t launch_expert_dispatch(ExpertParams p, int es, int sms, cudaStream_t
   auto sort_bytes = [](int E, int n) { return ((size_t)E + 1 + n) * sizeof(int) + (size_t)32 * E * sizeof(uint16_t); };
   const void* ranks[3] = {(const void*)expert_rank_kernel<1>, (const void*)expert_rank_kernel<2>, (const void*)expert_rank_kernel<4>};
   const void* sorts[3] = {(const void*)expert_sort_kernel<1>, (const void*)expert_sort_kernel<2>, (const void*)expert_sort_kernel<4>};
-  static bool configured[64] = {};
+  static DeviceOnce configured;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 64 && !configured[dev]) {
+  e = configured.run(dev, [&] {
     constexpr cudaFuncAttribute kSmem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+    cudaError_t err = cudaSuccess;
     for (const void* f : ranks)
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(f, kSmem, (int)rank_bytes(kExpertMax));
+      if (err == cudaSuccess) err = cudaFuncSetAttribute(f, kSmem, (int)rank_bytes(kExpertMax));
     for (const void* f : sorts)
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(f, kSmem, (int)sort_bytes(kExpertMax, kExpertOneBlock));
-    if (e != cudaSuccess) return e;
-    configured[dev] = true;
-  }
+      if (err == cudaSuccess) err = cudaFuncSetAttribute(f, kSmem, (int)sort_bytes(kExpertMax, kExpertOneBlock));
+    return err;
+  });
+  if (e != cudaSuccess) return e;
   *info = LaunchInfo{};
   if (p.n <= kExpertOneBlock) {
     const size_t bytes = sort_bytes(p.E, p.n);

@@ -1125,12 +1125,11 @@ FastDiv fast_div(uint32_t d) {
 }
 
 cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cudaStream_t stream, LaunchInfo* info) {
-  static bool configured[64] = {};
-  static int pairs[64][kKernels] = {};
+  static DeviceOnce configured;
+  static int pairs[DeviceOnce::kDevices][kKernels] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64) return cudaErrorInvalidDevice;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1140,17 +1139,19 @@ cudaError_t launch_experts(const ExpertsMaps& maps, ExpertsParams p, int sms, cu
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  if (!configured[dev]) {
+  e = configured.run(dev, [&] {
     for (int i = 0; i < kKernels; ++i) {
-      if ((e = cudaFuncSetAttribute(kernel_at(i), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax))) return e;
+      cudaError_t err = cudaFuncSetAttribute(kernel_at(i), cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+      if (err != cudaSuccess) return err;
       cfg.gridDim = dim3(2);
       cfg.blockDim = dim3(threads_of(i));
       cfg.dynamicSmemBytes = kSmemMax;
       cfg.numAttrs = 1;
-      if (i % 5 != 3 && (e = cudaOccupancyMaxActiveClusters(&pairs[dev][i], kernel_at(i), &cfg))) return e;
+      if (i % 5 != 3 && (err = cudaOccupancyMaxActiveClusters(&pairs[dev][i], kernel_at(i), &cfg))) return err;
     }
-    configured[dev] = true;
-  }
+    return cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
   const int index = kernel_index(p);
   const int most = p.cg == 2 ? pairs[dev][index] : sms;
   if (most < 1) return cudaErrorInvalidConfiguration;

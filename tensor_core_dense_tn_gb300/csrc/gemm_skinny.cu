@@ -860,11 +860,11 @@ void skinny_partition(SkinnyParams* p, int num_sms, int grid_override, int skew_
 
 cudaError_t launch_skinny(const CUtensorMap& tmA, const CUtensorMap& tmB, SkinnyParams p, bool pdl,
                           cudaStream_t stream, LaunchInfo* info) {
-  static bool configured[64] = {};
+  static DeviceOnce configured;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 64 && !configured[dev]) {
+  e = configured.run(dev, [&] {
     int worst = 0;
     for (int np = 16; np <= 256; np += 16)
       for (int bm = 64; bm <= 128; bm += 64)
@@ -881,12 +881,11 @@ cudaError_t launch_skinny(const CUtensorMap& tmA, const CUtensorMap& tmB, Skinny
                                (const void*)gemm_tn_skinny_kernel<kKindF8F6F4, 128, false, 2>,
                                (const void*)gemm_tn_skinny_kernel<kKindF16, 128, true, 2>,
                                (const void*)gemm_tn_skinny_kernel<kKindF8F6F4, 128, true, 2>};
-    for (const void* k : kernels) {
-      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, worst);
-      if (e != cudaSuccess) return e;
-    }
-    configured[dev] = true;
-  }
+    for (const void* k : kernels)
+      if (cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, worst)) return err;
+    return cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
   if ((p.bm != 64 && p.bm != 128) || p.np < 16 || p.np > 256 || p.np % 16) return cudaErrorInvalidValue;
   if ((p.cg != 1 && p.cg != 2) || (p.cg == 2 && p.bm != 128)) return cudaErrorInvalidValue;
   const int npc = p.np / p.cg;  // token rows held by each CTA

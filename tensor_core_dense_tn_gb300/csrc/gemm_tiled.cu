@@ -784,19 +784,16 @@ cudaError_t launch_impl(const CUtensorMap& tmA, const CUtensorMap& tmB, const CU
   static_assert(sizeof(KernelArg<MODE, SLICE>) + 4 * sizeof(CUtensorMap) + sizeof(TileParams) < 32000,
                 "kernel parameters must stay within 32 KB");
   auto kern = gemm_tn_tiled_kernel<CG, OUT_F32, KIND, MODE, SPLIT, SLICE>;
-  static bool configured[64] = {};
+  static DeviceOnce configured;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 64 && !configured[dev]) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::SMEM);
-    if (e != cudaSuccess) return e;
-    if (CG == 2) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
-      (void)e;
-    }
-    configured[dev] = true;
-  }
+  e = configured.run(dev, [&] {
+    if (cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C_::SMEM)) return err;
+    if (CG == 2) (void)cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 0);
+    return cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[3];
   cfg.blockDim = dim3(kThreads, 1, 1);

@@ -624,19 +624,20 @@ cudaError_t launch_w4(const CUtensorMap& tm, W4Params p, int active, int sms, cu
   // Two token tiles where one would stream the weights twice.
   const int nt = p.offsets ? (p.M > 4LL * active ? 2 : 1) : (p.M > 8 ? 2 : 1);
   const int smem = smem_for(nt, fl) + list_bytes(p.E);
-  static bool configured[64] = {};
+  static DeviceOnce configured;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 64 && !configured[dev]) {
+  e = configured.run(dev, [&] {
     for (int i = 0; i < 16; ++i) {
       const int n = 1 + i / 8, f = 1 << (i / 2 % 4);
-      if ((e = cudaFuncSetAttribute(kernel_for(n, f, i % 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    smem_for(n, f) + list_bytes(kExpertMax))))
-        return e;
+      if (cudaError_t err = cudaFuncSetAttribute(kernel_for(n, f, i % 2), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 smem_for(n, f) + list_bytes(kExpertMax)))
+        return err;
     }
-    configured[dev] = true;
-  }
+    return cudaSuccess;
+  });
+  if (e != cudaSuccess) return e;
   const long long tiles = (p.N + kW4TileRows - 1) / kW4TileRows;
   const long long items = tiles * (p.offsets ? active : (p.M + 8 * nt - 1) / (8 * nt));
   p.split = w4_split(items, p.num_kb, sms);

@@ -2,7 +2,9 @@
 // translation units.  Not installed; the public surface is include/gemm_tn.h.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
+#include <mutex>
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -20,6 +22,25 @@ enum Role : int { kRoleProducer = 1, kRoleMma = 2, kRoleEpilogue = 3, kRoleFixup
 
 // L2 eviction-priority hints of the tiled kernels' copies (TileParams.l2_hints).
 constexpr int kL2HintAEvictLast = 1, kL2HintBEvictFirst = 2, kL2HintDEvictFirst = 4;
+
+// What a launch sets up once for each device; threads may make their first calls
+// at once, so the others wait for the one that does it.
+struct DeviceOnce {
+  static constexpr int kDevices = 64;
+  std::mutex mu;
+  std::atomic<bool> done[kDevices] = {};
+
+  template <typename F>
+  cudaError_t run(int dev, F set_up) {
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    if (done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    std::lock_guard<std::mutex> lk(mu);
+    if (done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    const cudaError_t e = set_up();
+    if (e == cudaSuccess) done[dev].store(true, std::memory_order_release);
+    return e;
+  }
+};
 
 // Test-only fault injection bits.
 constexpr int kFaultSkipTmaOnce = 1;

@@ -1,4 +1,7 @@
 """Calls from threads that have made no CUDA call before: nothing but this library's call has to bind the device."""
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -82,3 +85,24 @@ def test_the_first_cuda_call_of_a_thread(name):
     in_a_thread(call)
     status()
     assert torch.equal(out, want)
+
+
+def first_calls_at_once():
+    calls = make_calls()
+    torch.cuda.synchronize()
+    in_a_thread(*(call for call, _ in calls.values()))
+    status()
+    for name, (call, out) in calls.items():
+        got = out.clone()
+        out.zero_()
+        call()
+        status()
+        assert torch.equal(out, got), name
+
+
+def test_a_process_whose_first_calls_come_at_once():
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
+    done = subprocess.run([sys.executable, "-c", "import test_threads_gpu as t; t.first_calls_at_once()"], env=env, cwd=here,
+                          capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr
