@@ -95,7 +95,7 @@ typedef enum {
 
 typedef enum {
   GEMM_ACT_NONE = 0,
-  GEMM_ACT_RELU = 1,       /* max(x, 0) */
+  GEMM_ACT_RELU = 1,       /* max(x, 0), NaN for NaN */
   GEMM_ACT_GELU = 2,       /* x * Phi(x) = 0.5 x (1 + erf(x / sqrt 2)) */
   GEMM_ACT_GELU_TANH = 3,  /* 0.5 x (1 + tanh(sqrt(2/pi) (x + 0.044715 x^3))) */
   GEMM_ACT_SILU = 4        /* x / (1 + exp(-x)) */

@@ -5,7 +5,8 @@
 // The bias is a per-output-column vector (the N dimension: one value per row
 // of B, i.e. per output feature of an MLP layer), in bf16 or fp32.  The
 // activations are the usual MLP ones: ReLU, GELU (erf form and tanh
-// approximation) and SiLU, evaluated in fp32.
+// approximation) and SiLU, evaluated in fp32.  A NaN stays one, also under ReLU
+// (fmaxf would make a zero of it, and a diverged layer look like a dead one).
 //
 // The tanh form of GELU is computed as a logistic.  Since
 // 1 + tanh(u) = 2 / (1 + e^(-2u)) exactly, 0.5 x (1 + tanh(u)) = x / (1 + e^(-2u)),
@@ -22,6 +23,7 @@
 #include <cstdint>
 
 #include "kernels.h"
+#include "ptx.cuh"
 
 namespace gtn {
 
@@ -33,7 +35,7 @@ __device__ __forceinline__ float load_bias(const Epilogue& e, int n) {
 template <int ACT>
 __device__ __forceinline__ float act_of(float v) {
   if constexpr (ACT == kActRelu) {
-    return fmaxf(v, 0.0f);
+    return max_nan(v, 0.0f);
   } else if constexpr (ACT == kActGelu) {  // x * Phi(x)
     return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
   } else if constexpr (ACT == kActGeluTanh) {  // x / (1 + exp(-2 sqrt(2/pi) (x + 0.044715 x^3)))
