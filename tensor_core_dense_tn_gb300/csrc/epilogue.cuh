@@ -11,10 +11,11 @@
 // The tanh form of GELU is computed as a logistic.  Since
 // 1 + tanh(u) = 2 / (1 + e^(-2u)) exactly, 0.5 x (1 + tanh(u)) = x / (1 + e^(-2u)),
 // so that it and SiLU (x / (1 + e^(-x))) both take one expf, an add and a fast
-// divide, with no branch.  The exponent is capped at 80 so that the divisor
-// stays below 2^126, where __fdividef is accurate to 2 ulp; where the cap
-// applies the result is x / (1 + e^80) instead of a value nearer zero, a
-// difference below 2^-115 |x|.
+// divide, with no branch.  __fdividef is accurate to 2 ulp for divisors up to
+// 2^126 and gives zero beyond, up to an infinite one: for x below -87 (tanh
+// form: -10), where the exact result is below 2^-119 in size.  (A capped exponent, x / (1 +
+// e^80), would leave -1800 of x = -1e38.)  Of -infinity the quotient is NaN, as of
+// the formulas.
 // Error of either form: expf (2 ulp), the add and the divide (2 ulp) on the
 // result, plus the rounding of the argument, which moves the result by at
 // most 0.23 |x| times the argument's relative error.  The erf form keeps erff.
@@ -39,10 +40,10 @@ __device__ __forceinline__ float act_of(float v) {
   } else if constexpr (ACT == kActGelu) {  // x * Phi(x)
     return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
   } else if constexpr (ACT == kActGeluTanh) {  // x / (1 + exp(-2 sqrt(2/pi) (x + 0.044715 x^3)))
-    const float t = fminf(-1.5957691216057308f * fmaf(0.044715f * v, v * v, v), 80.0f);
+    const float t = -1.5957691216057308f * fmaf(0.044715f * v, v * v, v);
     return __fdividef(v, 1.0f + expf(t));
   } else if constexpr (ACT == kActSilu) {  // x / (1 + exp(-x))
-    return __fdividef(v, 1.0f + expf(fminf(-v, 80.0f)));
+    return __fdividef(v, 1.0f + expf(-v));
   } else {
     return v;
   }

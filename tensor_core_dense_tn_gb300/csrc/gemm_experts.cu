@@ -421,14 +421,14 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* m, bo
 // ---------------------------------------------------------------- epilogue
 // The logistic activations for a result that is rounded to bf16: __expf, whose
 // error grows with its argument (2^-22 of the value for each unit of it, below
-// 2^-15 up to the cap of 80), instead of expf.  Far below the rounding's 2^-9, and
+// 2^-15 up to 89, where it is infinite), instead of expf.  Far below the rounding's 2^-9, and
 // less work beside the MMAs.
 template <int NR>
 __device__ __forceinline__ void logistic_rows(float (&v)[NR], bool gelu) {
 #pragma unroll
   for (int j = 0; j < NR; ++j) {
     const float t = gelu ? -1.5957691216057308f * fmaf(0.044715f * v[j], v[j] * v[j], v[j]) : -v[j];
-    v[j] = __fdividef(v[j], 1.0f + __expf(fminf(t, 80.0f)));
+    v[j] = __fdividef(v[j], 1.0f + __expf(t));
   }
 }
 

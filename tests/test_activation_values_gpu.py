@@ -30,7 +30,7 @@ FORMULAS = {
     g.ACT_GELU_TANH: lambda v: v * (0.5 * (1 + torch.tanh((2 / math.pi) ** 0.5 * (v + 0.044715 * v ** 3)))),
     g.ACT_SILU: lambda v: v / (1 + torch.exp(-v)),
 }
-ACTS = [g.ACT_RELU, g.ACT_GELU]
+ACTS = list(FORMULAS)
 # the erf form loses its bits below -2 by its own formula in fp32: no values between there and -6
 VALUES = [NAN, INF, -INF, 0.0, -0.0, 1.0, -1.0, 5.5, 40.0, -40.0, -75.0, -79.5, -80.5, -85.0, -87.5, -88.5, -89.0, -100.0,
           -104.0, -1000.0, -1e10, -1e30, -3e38, 100.0, 1e4, 1e30, 3e38]
