@@ -682,7 +682,7 @@ int gemm_experts_config(const gemm_tn_config *cfg);
  * tensor twice).  norm: one fp32 in device memory.  workspace: device memory of
  * gemm_grad_workspace(num) bytes, 8-byte aligned, whose contents do not matter;
  * calls that may run at the same time need one each.  Neither may overlap a
- * tensor (GEMM_ERR_INVALID_VALUE).  No other memory is used,
+ * tensor or the other (GEMM_ERR_INVALID_VALUE).  No other memory is used,
  * so the calls may be captured and replayed on any stream. */
 typedef struct gemm_tensor {
   void *data;

@@ -1260,6 +1260,9 @@ int run_grad_norm(int num, const gemm_tensor* tensors, bool clip, float max_norm
   if (clip && !(max_norm >= 0.0f)) return fail(GEMM_ERR_INVALID_VALUE, "max_norm must not be negative or NaN");
   if (!workspace) return fail(GEMM_ERR_INVALID_VALUE, "workspace is NULL");
   if (!aligned_to(workspace, 8)) return fail(GEMM_ERR_MISALIGNED, "workspace must be 8-byte aligned");
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm), sums = reinterpret_cast<uintptr_t>(workspace);
+  if (at < sums + (uintptr_t)gemm_grad_workspace(num) && sums < at + 4)
+    return fail(GEMM_ERR_INVALID_VALUE, "norm and workspace overlap");
   static thread_local std::vector<GradTensor> list;
   list.clear();
   for (int i = 0; i < num; ++i) {
