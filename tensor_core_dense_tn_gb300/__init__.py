@@ -334,6 +334,7 @@ def gemm(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, out_dtype=None, ou
     N, Kb = B.shape
     if Kb != K:
         raise ValueError("A and B must have the same K")
+    given = out
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=A.device)
     if out.shape != (M, N) or out.dtype != out_dtype or out.stride(1) != 1:
@@ -350,6 +351,9 @@ def gemm(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, out_dtype=None, ou
             out.data_ptr(), out.stride(0), float(alpha), float(beta), code, stream)
     rc = gemm_bf16_tn_ex(*args, config=config) if config is not None else gemm_bf16_tn(*args)
     _check(rc)
+    if given is not None:
+        _t()
+        _written(given)
     return out
 
 
@@ -443,6 +447,12 @@ def _t():
         _CODES.update({torch.bfloat16: OUT_BF16, torch.float32: OUT_F32})
         _torch = torch
     return _torch
+
+
+def _written(*tensors):
+    """Counts a call's writes into tensors that the caller gave as in-place changes of them, as autograd expects
+    (torch.autograd.graph.increment_version, in half its time).  None: the call made that one itself."""
+    _torch._C._increment_version([t for t in tensors if t is not None and not t.is_inference()])
 
 
 def _out_code(dtype, what):
@@ -576,6 +586,7 @@ def expert_dispatch(ids, plan: ExpertPlan, X=None, out=None, stream=None):
         _gpu_of(gpu, "the plan")
     ld_ids = _rows_of(ids, plan.tokens, plan.slots, "ids", gpu)
     H, x, ldx, o, ldo, code = 0, None, 0, None, 0, OUT_BF16
+    given = out if X is not None else None
     if X is not None:
         code, ldx = _out_code(X.dtype, "X"), _rows_of(X, plan.tokens, None, "X", gpu)
         H, x = X.shape[1], X.data_ptr()
@@ -591,6 +602,8 @@ def expert_dispatch(ids, plan: ExpertPlan, X=None, out=None, stream=None):
     if rc:
         _check(rc)
     torch._C._increment_version(plan._versioned)    # torch.autograd.graph.increment_version, in half its time
+    if given is not None:
+        _written(given)
     return out if X is not None else None
 
 
@@ -614,6 +627,7 @@ def _combine(plan, Y, weights, out, stream):
     H = Y.shape[1]
     if weights is not None:
         wcode, ldw = _out_code(weights.dtype, "weights"), _rows_of(weights, plan.tokens, plan.slots, "weights", gpu)
+    given = out
     if out is None:
         out, ldo = torch.empty((plan.tokens, H), dtype=Y.dtype, device=Y.device), H
     else:
@@ -628,6 +642,8 @@ def _combine(plan, Y, weights, out, stream):
                                      out.data_ptr(), ldo, s)
     if rc:
         _check(rc)
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -643,6 +659,7 @@ def expert_combine_backward(plan: ExpertPlan, Y, weights, dout, dY=None, dweight
         raise ValueError("dout must have Y's type")
     lddo = _rows_of(dout, plan.tokens, H, "dout", gpu)
     wcode, ldw = _out_code(weights.dtype, "weights"), _rows_of(weights, plan.tokens, plan.slots, "weights", gpu)
+    given = dY, dweights
     if dY is None:
         dY = torch.empty((plan.rows, H), dtype=Y.dtype, device=Y.device)
     if dweights is None:
@@ -655,6 +672,8 @@ def expert_combine_backward(plan: ExpertPlan, Y, weights, dout, dY=None, dweight
         _rows_of(dweights, plan.tokens, plan.slots, "dweights", gpu), _stream_of(Y) if stream is None else stream or None)
     if rc:
         _check(rc)
+    if given[0] is not None or given[1] is not None:
+        _written(*given)
     return dY, dweights
 
 
@@ -682,6 +701,7 @@ def _w4(plan, A, W, gather, alpha, activation, out_dtype, out, stream):
     rows = A.shape[0] if plan is None else plan.tokens if gather else plan.rows
     lda = _rows_of(A, rows, W.K, "A", gpu)
     M = rows if plan is None else plan.rows
+    given = out
     if out is None:
         out, ldd = torch.empty((M, W.N), dtype=out_dtype or torch.bfloat16, device=A.device), W.N
     else:
@@ -697,6 +717,8 @@ def _w4(plan, A, W, gather, alpha, activation, out_dtype, out, stream):
                                     activation, s)
     if rc:
         _check(rc)
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -746,6 +768,7 @@ def _experts_rows(backward, X, W, plan, alpha, activation, out_dtype, out, strea
     ldw, apart = _matrices_of(W, plan.experts, N, K, "W", gpu)
     ldx = _rows_of(X, plan.rows, N if backward else K, "dD" if backward else "A", gpu)
     width = K if backward else N
+    given = out
     if out is None:
         out, ldo = torch.empty((plan.rows, width), dtype=out_dtype or torch.bfloat16, device=X.device), width
     else:
@@ -762,6 +785,8 @@ def _experts_rows(backward, X, W, plan, alpha, activation, out_dtype, out, strea
                                       alpha, code, activation, s)
     if rc:
         _check(rc)
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -778,6 +803,7 @@ def gemm_experts_backward_w(dD, A, plan: ExpertPlan, alpha: float = 1.0, beta: f
         _gpu_of(gpu, "the plan")
     lddd, lda = _rows_of(dD, plan.rows, None, "dD", gpu), _rows_of(A, plan.rows, None, "A", gpu)
     N, K, E = dD.shape[1], A.shape[1], plan.experts
+    given = out
     if out is None:
         dtype = out_dtype or (torch.bfloat16 if C is None or beta == 0.0 else C.dtype)
         out = torch.empty((E, N, K), dtype=dtype, device=A.device)
@@ -796,6 +822,8 @@ def gemm_experts_backward_w(dD, A, plan: ExpertPlan, alpha: float = 1.0, beta: f
         beta, code, _stream_of(A) if stream is None else stream or None)
     if rc:
         _check(rc)
+    if given is not None:
+        _written(given)
     return out
 
 
@@ -859,11 +887,14 @@ def grad_norm(tensors, norm=None, stream=None):
     _torch or _t()
     tensors = list(tensors)
     words, _, gpu, _ = _tensor_list(tensors, "tensors")
+    given = norm
     norm, work = _norm_buffers(len(tensors), gpu, norm, stream)
     s = _torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream
     rc = (_lib or load()).gemm_grad_norm(len(tensors), words, norm.data_ptr(), work.data_ptr(), s or None)
     if rc:
         _check(rc)
+    if given is not None:
+        _written(given)
     return norm
 
 
@@ -889,12 +920,12 @@ def clip_grad_norm(tensors, max_norm: float, out=None, norm=None, stream=None):
                 if t.numel() and not (o.is_contiguous() and t.is_contiguous()) and \
                         (o.shape != t.shape or o.stride() != t.stride()):
                     raise ValueError(f"out: tensor {i} must have its tensor's shape and order of dimensions")
+    given = norm
     norm, work = _norm_buffers(len(tensors), gpu, norm, stream)
     s = torch._C._cuda_getCurrentRawStream(gpu) if stream is None else stream
     rc = (_lib or load()).gemm_clip_grad_norm(len(tensors), words, max_norm, to, norm.data_ptr(), work.data_ptr(),
                                                s or None)
     if rc:
         _check(rc)
-    if out is None:
-        torch._C._increment_version(tuple([t for t in tensors if not t.is_inference()]))
+    _written(given, *(tensors if out is None else out))
     return norm
