@@ -1076,8 +1076,8 @@ void experts_geometry(ExpertsParams* p, int sms) {
   p->long_sum = p->out_f32 && (weights ? p->R : p->S) > kSegmentBlocks * kBlockK;
   p->cg = weights && average < (p->has_c ? 768 : 192) ? 1 : 2;
   const int step = 16 * p->cg;
-  const int most = 2 * average < 32 ? 32 : 2 * average;
-  p->tile_rows = weights || most > 256 ? 256 : (most + 31) / 32 * 32;
+  const int most = average < 16 ? 32 : average > 128 ? 256 : 2 * average;
+  p->tile_rows = weights ? 256 : (most + 31) / 32 * 32;
   if (!weights && p->tile_rows > (p->R + step - 1) / step * step) p->tile_rows = (p->R + step - 1) / step * step;
   const int share = p->tile_rows / p->cg;
   p->row_box = share;
