@@ -1069,12 +1069,16 @@ void experts_geometry(ExpertsParams* p, int sms) {
   const int average = active > 0 ? p->R / active : 0;
   // Pairs halve what a CTA loads of the other operand.  Weights of few rows,
   // where the output's memory decides: single CTAs, which need not wait for each
-  // other (64 matrices of 2048 x 2048, single / pairs: 128 rows each, bf16, 130 /
-  // 142 us; 256 rows 174 / 171; fp32 with C, 512 rows 444 / 454, 1024 rows 582 / 555).
+  // other.  64 matrices of 2048 x 2048, single / pairs, us, by the rows of each:
+  //   bf16          64: 97 / 98,    128: 109 / 107,  256: 143 / 127,  512: 225 / 184
+  //   bf16 with C   256: 284 / 288, 384: 309 / 302,  512: 328 / 321,  768: 370 / 355
+  //   fp32          64: 199 / 192,  128: 205 / 200,  384: 261 / 201,  512: 300 / 246
+  //   fp32 with C   256: 373 / 416, 512: 388 / 433, 1024: 531 / 530, 1536: 705 / 591
+  // Routed unevenly: bf16, 150 on average: 135 / 136; with C, 500: 361 / 344; fp32 with C, 1000: 299 / 298.
   // LONG for weights wherever an expert can have more rows than a segment: how
   // many each has is known on the device only, and every tile goes by its own.
   p->long_sum = p->out_f32 && (weights ? p->R : p->S) > kSegmentBlocks * kBlockK;
-  p->cg = weights && average < (p->has_c ? 768 : 192) ? 1 : 2;
+  p->cg = weights && average < (!p->has_c ? 192 : p->out_f32 ? 768 : 320) ? 1 : 2;
   const int step = 16 * p->cg;
   const int most = average < 16 ? 32 : average > 128 ? 256 : 2 * average;
   p->tile_rows = weights ? 256 : (most + 31) / 32 * 32;
