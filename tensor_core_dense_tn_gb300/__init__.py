@@ -353,7 +353,7 @@ def gemm(A, B, C=None, alpha: float = 1.0, beta: float = 0.0, out_dtype=None, ou
     _check(rc)
     if given is not None:
         _t()
-        _written(given)
+        _written((given,))
     return out
 
 
@@ -449,10 +449,11 @@ def _t():
     return _torch
 
 
-def _written(*tensors):
+def _written(tensors):
     """Counts a call's writes into tensors that the caller gave as in-place changes of them, as autograd expects
-    (torch.autograd.graph.increment_version, in half its time).  None: the call made that one itself."""
-    _torch._C._increment_version([t for t in tensors if t is not None and not t.is_inference()])
+    (torch.autograd.graph.increment_version, in half its time; tensors of inference mode, which have no version, are
+    left alone)."""
+    _torch._C._increment_version(tensors)
 
 
 def _out_code(dtype, what):
@@ -603,7 +604,7 @@ def expert_dispatch(ids, plan: ExpertPlan, X=None, out=None, stream=None):
         _check(rc)
     torch._C._increment_version(plan._versioned)    # torch.autograd.graph.increment_version, in half its time
     if given is not None:
-        _written(given)
+        _written((given,))
     return out if X is not None else None
 
 
@@ -643,7 +644,7 @@ def _combine(plan, Y, weights, out, stream):
     if rc:
         _check(rc)
     if given is not None:
-        _written(given)
+        _written((given,))
     return out
 
 
@@ -673,7 +674,7 @@ def expert_combine_backward(plan: ExpertPlan, Y, weights, dout, dY=None, dweight
     if rc:
         _check(rc)
     if given[0] is not None or given[1] is not None:
-        _written(*given)
+        _written([t for t in given if t is not None])
     return dY, dweights
 
 
@@ -718,7 +719,7 @@ def _w4(plan, A, W, gather, alpha, activation, out_dtype, out, stream):
     if rc:
         _check(rc)
     if given is not None:
-        _written(given)
+        _written((given,))
     return out
 
 
@@ -786,7 +787,7 @@ def _experts_rows(backward, X, W, plan, alpha, activation, out_dtype, out, strea
     if rc:
         _check(rc)
     if given is not None:
-        _written(given)
+        _written((given,))
     return out
 
 
@@ -823,7 +824,7 @@ def gemm_experts_backward_w(dD, A, plan: ExpertPlan, alpha: float = 1.0, beta: f
     if rc:
         _check(rc)
     if given is not None:
-        _written(given)
+        _written((given,))
     return out
 
 
@@ -894,7 +895,7 @@ def grad_norm(tensors, norm=None, stream=None):
     if rc:
         _check(rc)
     if given is not None:
-        _written(given)
+        _written((given,))
     return norm
 
 
@@ -927,5 +928,7 @@ def clip_grad_norm(tensors, max_norm: float, out=None, norm=None, stream=None):
                                                s or None)
     if rc:
         _check(rc)
-    _written(given, *(tensors if out is None else out))
+    _written(tensors if out is None else out)
+    if given is not None:
+        _written((given,))
     return norm
