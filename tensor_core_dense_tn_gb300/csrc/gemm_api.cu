@@ -81,13 +81,6 @@ int init_device(int* dev_out, DeviceState** st_out) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
   if (dev < 0 || dev >= kMaxDevices) return fail(GEMM_ERR_UNSUPPORTED_DEVICE, "device index %d out of range", dev);
-  // A thread whose first CUDA call this is has no context yet, which the driver's
-  // encoding of tensor maps needs (it fails with 201 without one).
-  static thread_local int bound = -1;
-  if (bound != dev) {
-    if ((e = cudaSetDevice(dev)) != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaSetDevice: %s", cudaGetErrorString(e));
-    bound = dev;
-  }
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState& st = g_dev[dev];
   if (!st.ready) {
@@ -113,6 +106,16 @@ int init_device(int* dev_out, DeviceState** st_out) {
       g_encode = reinterpret_cast<EncodeTiledFn>(fn);
     }
     st.ready = true;
+  }
+  // A thread whose first CUDA call this is has no context yet, which the driver's
+  // encoding of tensor maps needs (it fails with 201 without one).  Looking up a
+  // device symbol gives it the device's, and leaves one that it has made current.
+  static thread_local int bound = -1;
+  if (bound != dev) {
+    void* p = nullptr;
+    e = cudaGetSymbolAddress(&p, g_status);
+    if (e != cudaSuccess) return fail(GEMM_ERR_CUDA, "cudaGetSymbolAddress(status): %s", cudaGetErrorString(e));
+    bound = dev;
   }
   *dev_out = dev;
   *st_out = &st;
