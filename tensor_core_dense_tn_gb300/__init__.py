@@ -749,12 +749,15 @@ def gemm_experts(A, W, plan: ExpertPlan, alpha: float = 1.0, activation: int = A
     """D[r] = act(alpha * A[r] @ W[e].T) for the rows r of expert e in `plan`: A (plan.rows, K) bf16 in expert order,
     W (experts, N, K) bf16; zeros in the rows past plan.offsets[experts].  Nothing waits for the row counts.  Without
     an autograd graph: the gradients of the product without an activation are gemm_experts_backward_a() and _w().
+    Rows of A and W start on 16 bytes, those of the result without `out` follow one another without gaps: where N is
+    not a multiple of 8, the next product wants an `out` whose rows are N rounded up to 8 apart.
     Without `out` the result is the current stream's memory: a `stream` of the caller's waits for that one first."""
     return _experts_rows(False, A, W, plan, alpha, activation, out_dtype, out, stream)
 
 
 def gemm_experts_backward_a(dD, W, plan: ExpertPlan, alpha: float = 1.0, out_dtype=None, out=None, stream=None):
-    """Gradient of gemm_experts' rows: dA[r] = alpha * dD[r] @ W[e], zeros past plan.offsets[experts]."""
+    """Gradient of gemm_experts' rows: dA[r] = alpha * dD[r] @ W[e], zeros past plan.offsets[experts].  Rows of dD and W
+    start on 16 bytes, as gemm_experts()' do."""
     return _experts_rows(True, dD, W, plan, alpha, ACT_NONE, out_dtype, out, stream)
 
 

@@ -51,8 +51,8 @@
 //                    rows, 16384 rows, 8 of 8192 x 4096          599-629, floor 569
 //                    weights, the same                           587-608, floor 569
 //   both             9003 rows, 61 of 5000 x 2000, fp32          239, floor 211
-//   output's bytes   weights, 64 of 2048 x 2048 fp32 with C      389, floor 336
-//                    weights, 61 of 1000 x 2000, 3 rows each      52, floor 36
+//   output's bytes   weights, 64 of 2048 x 2048 fp32 with C      400, floor 336
+//                    weights, 61 of 1000 x 2000, 3 rows each      53, floor 36
 // (The ranges are of one program at different times: at 1400 W the clock moves.)
 // In the second group the tensor pipe is active 89-91% of the time with about 1000
 // rows an expert, and 72-74% in `weights`, whose tiles are 16 k-blocks then.
@@ -94,7 +94,7 @@ constexpr uint64_t kSettleNs = 2000000;    // what copies in flight are given to
 //   In `weights` every tile goes by its own expert's rows, so that an expert's
 // error, and its bits, do not depend on how many the others have.  A sum of one
 // segment takes the path without sums in registers, on which C is loaded ahead:
-// 64 matrices of 2048 x 2048 with C, 256 rows each, 404 us (539 with the other
+// 64 matrices of 2048 x 2048 with C, 256 rows each, 400 us (539 with the other
 // path for all tiles, 391 in a kernel without it); 1000 rows each of 32, some of
 // one segment and some of two, 300.
 constexpr int kSegmentBlocks = 12;         // k-blocks of a segment
